@@ -65,6 +65,8 @@ extern "C" {
 #define SEGPOLY_IR_MUL 1
 #define SEGPOLY_F32 0
 #define SEGPOLY_F64 1
+#define SEGPOLY_BF16 2 /* the invariant-channel operators only */
+#define SEGPOLY_F16 3  /* the invariant-channel operators only */
 #define SEGPOLY_I32 0
 #define SEGPOLY_I64 1
 
@@ -695,6 +697,123 @@ int edge_scalars_bwd(int dtype, const void* grad_out, int64_t d_emb, int64_t d_s
                      const void* dst, const void* src_perm, int idx_dtype, int64_t n_edges, int64_t n_src,
                      int64_t n_dst, void* grad_emb, void* grad_src, void* grad_dst, void* stream);
 
+
+/* --------------------------------------------------- invariant-channel operators
+ *
+ * Embedding lookup, the joined norms of a residual block, and the gated
+ * feed-forward block, on rows of plain (l = 0) channels: the species
+ * embedding, the residual update and the node-wise network around the
+ * convolution and the symmetric contraction, and the same parts of a language
+ * model.  dtype: SEGPOLY_F32, SEGPOLY_BF16 or SEGPOLY_F16 for the tensors
+ * marked T (E_UNSUPPORTED for SEGPOLY_F64); sums, statistics, activations
+ * and the norms' parameters are float32 whatever T is.  Activations are rows of contiguous elements; an
+ * argument named *_stride is the distance between rows in elements (an
+ * input's may be smaller than the width, 0 for one row read by all; an
+ * output's may not), so the invariant columns of a wider feature row need no
+ * copy.  Outputs without a stride are contiguous.  Buffers need the alignment
+ * of their element only.  All results are deterministic (no atomics on
+ * floating point) and every call may be captured into a graph.  Workspaces
+ * are device memory of the caller, 256-byte aligned, whose contents on entry
+ * do not matter.
+ */
+
+/*
+ * embedding_fwd: out[i] = scale * table[tokens[i]], a zero row for a token
+ * outside [0, rows).
+ *   table [rows, dim] T.  tokens [n] int32/int64.  out [n, dim] T.
+ */
+int embedding_fwd(int dtype, const void* table, int64_t rows, int64_t dim, const void* tokens, int idx_dtype,
+                  int64_t n, double scale, void* out, int64_t out_stride, void* stream);
+
+/* embedding_bwd_workspace: bytes embedding_bwd needs (sorted tokens and
+ * their positions, row ranges, float32 sums of 32 positions). */
+int embedding_bwd_workspace(int64_t n, int64_t rows, int64_t dim, size_t* bytes);
+
+/*
+ * embedding_bwd: the table's gradient,
+ *   grad_table[r] = scale * sum over i with tokens[i] == r of grad_out[i],
+ * summed in float32 in the order of i (in groups of 32 for rows with many
+ * tokens) and rounded once; rows no token names are zero, tokens outside
+ * [0, rows) add nothing.
+ *   grad_out [n, dim] T.  grad_table [rows, dim] T, fully overwritten.
+ */
+int embedding_bwd(int dtype, const void* grad_out, int64_t grad_stride, const void* tokens, int idx_dtype, int64_t n,
+                  int64_t rows, int64_t dim, double scale, void* grad_table, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+#define SEGPOLY_NORM_RMS 0
+#define SEGPOLY_NORM_LAYER 1
+#define SEGPOLY_GATE_NONE 0
+#define SEGPOLY_GATE_ROW 1     /* one value per row */
+#define SEGPOLY_GATE_ELEMENT 2 /* one value per element */
+#define SEGPOLY_GATE_ACT_NONE 0
+#define SEGPOLY_GATE_ACT_SIGMOID 1
+
+/*
+ * block_norm_fwd: the end of one residual block and the start of the next,
+ *   y = x + res_scale * gate * (w_post * norm(f)),     h = w_pre * norm(y),
+ *   norm(v) = (v - m) / sqrt(mean((v - m)^2) + eps),   m = mean(v) or 0 (RMS).
+ *   x, f [n, dim] T.  gate [n, dim] or [n] T, or NULL with GATE_NONE; with
+ *   GATE_ACT_SIGMOID it passes through a sigmoid first.  w_post, res_scale,
+ *   w_pre [dim] float32; res_scale NULL: 1; w_pre and h NULL: no second norm.
+ *   y, h [n, dim] T; h is of the sum before its rounding to T.
+ * dim at most 16384 (E_UNSUPPORTED above).
+ */
+int block_norm_fwd(int dtype, int kind, int gate_mode, int gate_act, const void* x, int64_t x_stride, const void* f,
+                   int64_t f_stride, const void* gate, int64_t gate_stride, const void* w_post, const void* res_scale,
+                   const void* w_pre, double eps, int64_t n, int64_t dim, void* y, void* h, void* stream);
+
+/* block_norm_bwd_workspace: bytes block_norm_bwd needs (partial column sums). */
+int block_norm_bwd_workspace(int64_t n, int64_t dim, size_t* bytes);
+
+/*
+ * block_norm_bwd: vector-Jacobian product of block_norm_fwd for grad_y,
+ * grad_h, from the stored y (read only with w_pre), f and gate:
+ *   grad_x, grad_f [n, dim] T, grad_gate as gate, grad_w_post,
+ *   grad_res_scale, grad_w_pre [dim] float32 (sums over the rows; the last
+ *   two only with their parameter, and may be NULL without it).
+ * All are fully overwritten.
+ */
+int block_norm_bwd(int dtype, int kind, int gate_mode, int gate_act, const void* y, int64_t y_stride, const void* grad_y,
+                   int64_t grad_y_stride, const void* grad_h, int64_t grad_h_stride, const void* f, int64_t f_stride,
+                   const void* gate, int64_t gate_stride, const void* w_post, const void* res_scale, const void* w_pre,
+                   double eps, int64_t n, int64_t dim, void* grad_x, void* grad_f, void* grad_gate, void* grad_w_post,
+                   void* grad_res_scale, void* grad_w_pre, void* workspace, size_t workspace_bytes, void* stream);
+
+#define SEGPOLY_ACT_SILU 0
+#define SEGPOLY_ACT_GELU 1 /* g Phi(g), with the error function */
+#define SEGPOLY_ACT_RELU 2
+#define SEGPOLY_ACT_SIGMOID 3
+
+/* gated_ffn_workspace: bytes gated_ffn_fwd (backward == 0) or gated_ffn_bwd
+ * (backward != 0) needs: the hidden rows and, where an operand's width,
+ * stride or address does not suit 16-byte accesses (float32: always, as three
+ * bf16 planes), a copy of it.  Sized for the case that every one is copied. */
+int gated_ffn_workspace(int dtype, int64_t n, int64_t d_in, int64_t hidden, int64_t d_out, int backward,
+                        size_t* bytes);
+
+/*
+ * gated_ffn_fwd: out = (act(x w_gate^T) * (x w_up^T)) w_down^T.
+ *   x [n, d_in], w_gate, w_up [hidden, d_in], w_down [d_out, hidden],
+ *   out [n, d_out], all T.
+ * Products on the matrix cores with float32 sums; the hidden rows are held
+ * in T between the two products (float32 in 24 bits).  A float32 infinity
+ * gives NaN where the product of its planes meets a zero.
+ */
+int gated_ffn_fwd(int dtype, int act, const void* x, int64_t x_stride, const void* w_gate, const void* w_up,
+                  const void* w_down, int64_t n, int64_t d_in, int64_t hidden, int64_t d_out, void* out,
+                  int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gated_ffn_bwd: vector-Jacobian product of gated_ffn_fwd for grad_out
+ * [n, d_out]; the hidden rows are computed again.  grad_x [n, d_in] or NULL;
+ * the three weight gradients, shaped as the weights, or all NULL.  With
+ * n == 0 the weight gradients are zero.
+ */
+int gated_ffn_bwd(int dtype, int act, const void* x, int64_t x_stride, const void* w_gate, const void* w_up,
+                  const void* w_down, const void* grad_out, int64_t grad_out_stride, int64_t n, int64_t d_in,
+                  int64_t hidden, int64_t d_out, void* grad_x, void* grad_w_gate, void* grad_w_up, void* grad_w_down,
+                  void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------- spherical harmonics */
 

@@ -3,7 +3,9 @@
 The functions keep the names of the C ABI in ``include/segpoly.h``:
 ``tp_create`` / ``tp_conv_fwd`` / ``tp_conv_bwd`` / ``symcon_create`` / ``symcon_fwd`` /
 ``symcon_bwd`` / ``linear_create`` / ``linear_fwd`` / ``linear_bwd`` / ``fctp_create`` /
-``fctp_fwd`` / ``fctp_bwd`` / ``sh_fwd`` / ``sh_bwd``.  Every
+``fctp_fwd`` / ``fctp_bwd`` / ``sh_fwd`` / ``sh_bwd`` / ``embedding_fwd`` /
+``embedding_bwd`` / ``block_norm_fwd`` / ``block_norm_bwd`` / ``gated_ffn_fwd`` /
+``gated_ffn_bwd``.  Every
 step of the computation runs in the library's HIP kernels; PyTorch only
 supplies device memory and the current stream.  There is no CPU fallback:
 importing this package fails loudly if the library has not been built.
@@ -22,7 +24,7 @@ LIB_PATH = os.environ.get("SEGPOLY_LIB") or os.path.join(_HERE, "libsegpoly.so")
 OK = 0
 E_INVALID, E_PARSE, E_UNSUPPORTED, E_UNSORTED, E_HIP, E_OOM, E_RANGE = -1, -2, -3, -4, -5, -6, -7
 MUL_IR, IR_MUL = 0, 1
-F32, F64 = 0, 1
+F32, F64, BF16, F16 = 0, 1, 2, 3
 I32, I64 = 0, 1
 SHARED_WEIGHTS, VALIDATE, FORCE_GENERIC, REDUCE_MEAN, MERGE_PATHS = 1, 2, 4, 8, 16
 (Q_DIM_IN1, Q_DIM_IN2, Q_DIM_OUT, Q_WEIGHT_NUMEL, Q_NUM_PATHS, Q_CG_NNZ, Q_SPECIALIZED, Q_MUL,
@@ -36,7 +38,9 @@ EXPORTS = ("tp_create", "tp_query", "tp_irreps_out", "tp_path_info", "tp_path_cg
            "tp_conv_fwd", "tp_conv_fwd_vec", "tp_rowptr_build", "tp_conv_fwd_rowptr", "tp_src_rowptr_build", "tp_conv_bwd_workspace", "tp_conv_bwd", "tp_conv_bwd_rowptr", "tp_destroy", "symcon_create", "symcon_query", "symcon_coupling_info",
            "symcon_coupling_dense", "symcon_fwd", "symcon_bwd_workspace", "symcon_bwd", "symcon_bwd_noalloc", "symcon_destroy", "linear_create", "linear_query", "linear_fwd",
            "linear_bwd_workspace", "linear_bwd", "linear_destroy", "fctp_create", "fctp_query", "fctp_path_info",
-           "fctp_fwd", "fctp_bwd_workspace", "fctp_bwd", "fctp_fwd_per_sample", "fctp_bwd_per_sample", "fctp_conv_fwd", "fctp_conv_bwd_workspace", "fctp_conv_bwd", "fctp_destroy", "edge_scalars_fwd", "edge_scalars_bwd", "sh_fwd", "sh_bwd", "segpoly_real_cg",
+           "fctp_fwd", "fctp_bwd_workspace", "fctp_bwd", "fctp_fwd_per_sample", "fctp_bwd_per_sample", "fctp_conv_fwd", "fctp_conv_bwd_workspace", "fctp_conv_bwd", "fctp_destroy", "edge_scalars_fwd", "edge_scalars_bwd",
+           "embedding_fwd", "embedding_bwd_workspace", "embedding_bwd", "block_norm_fwd", "block_norm_bwd_workspace",
+           "block_norm_bwd", "gated_ffn_workspace", "gated_ffn_fwd", "gated_ffn_bwd", "sh_fwd", "sh_bwd", "segpoly_real_cg",
            "segpoly_last_error", "segpoly_version")
 
 
@@ -118,6 +122,18 @@ def _load():
         "fctp_destroy": [vp],
         "edge_scalars_fwd": [c_int, vp, i64, vp, i64, vp, i64, vp, vp, c_int, i64, i64, i64, vp, vp],
         "edge_scalars_bwd": [c_int, vp, i64, i64, i64, vp, vp, vp, c_int, i64, i64, i64, vp, vp, vp, vp],
+        "embedding_fwd": [c_int, vp, i64, i64, vp, c_int, i64, ctypes.c_double, vp, i64, vp],
+        "embedding_bwd_workspace": [i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)],
+        "embedding_bwd": [c_int, vp, i64, vp, c_int, i64, i64, i64, ctypes.c_double, vp, vp, ctypes.c_size_t, vp],
+        "block_norm_fwd": [c_int, c_int, c_int, c_int, vp, i64, vp, i64, vp, i64, vp, vp, vp, ctypes.c_double, i64, i64,
+                           vp, vp, vp],
+        "block_norm_bwd_workspace": [i64, i64, ctypes.POINTER(ctypes.c_size_t)],
+        "block_norm_bwd": [c_int, c_int, c_int, c_int, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp,
+                           ctypes.c_double, i64, i64, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
+        "gated_ffn_workspace": [c_int, i64, i64, i64, i64, c_int, ctypes.POINTER(ctypes.c_size_t)],
+        "gated_ffn_fwd": [c_int, c_int, vp, i64, vp, vp, vp, i64, i64, i64, i64, vp, i64, vp, ctypes.c_size_t, vp],
+        "gated_ffn_bwd": [c_int, c_int, vp, i64, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp,
+                          ctypes.c_size_t, vp],
         "sh_fwd": [c_int, c_int, c_int, vp, i64, vp, vp],
         "sh_bwd": [c_int, c_int, c_int, vp, vp, i64, vp, vp],
         "segpoly_real_cg": [c_int, c_int, c_int, pd],
@@ -957,3 +973,253 @@ def sh_bwd(vec, grad_sh, lmax, normalize=True):
     _check(lib.sh_bwd(lmax, 1 if normalize else 0, _sh_dtype(vec), _ptr(vec), _ptr(grad_sh), n, _ptr(out),
                       _stream_ptr(vec.device)))
     return out
+
+
+# ------------------------------------------------ invariant-channel operators
+
+_CHANNEL_DTYPES = {}
+_NORM_KINDS = {"rms": 0, "layer": 1}
+_GATE_ACTS = {"none": 0, "sigmoid": 1}
+_ACTS = {"silu": 0, "gelu": 1, "relu": 2, "sigmoid": 3}
+
+
+def _channel_dtype(t):
+    if not _CHANNEL_DTYPES:
+        import torch
+        _CHANNEL_DTYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+    try:
+        return _CHANNEL_DTYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"float32, bfloat16 or float16 tensors, not {t.dtype}") from None
+
+
+def _rows(name, a, like, n, d, output=False):
+    """Row stride of a [n, d] device tensor of the dtype of `like` with
+    contiguous rows."""
+    if a.dtype != like.dtype or a.device != like.device or not a.is_cuda:
+        raise ValueError(f"{name} must be a {like.dtype} tensor on {like.device}")
+    if a.dim() != 2 or a.shape[0] != n or a.shape[1] != d:
+        raise ValueError(f"{name} must have the shape [{n}, {d}], not {list(a.shape)}")
+    if d > 1 and a.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    stride = a.stride(0)
+    if n <= 1:
+        return max(stride, d) if output else stride
+    if output and stride < d:
+        raise ValueError(f"the rows of {name} overlap")
+    return stride
+
+
+def _param(name, a, like, d):
+    import torch
+    if a.dtype != torch.float32 or a.device != like.device or a.shape != (d,) or not a.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {d} on {like.device}")
+
+
+def _contiguous(name, a, like, shape):
+    if a.dtype != like.dtype or a.device != like.device or not a.is_cuda or a.shape != shape or not a.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {like.dtype} tensor {list(shape)} on {like.device}")
+
+
+def _channel_workspace(workspace, nbytes, device):
+    """The caller's workspace, or a new one, and its size in bytes."""
+    import torch
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _token_dtype(tokens, device):
+    idx = _index_dtype(tokens)
+    if tokens.dim() != 1 or tokens.device != device or not tokens.is_contiguous():
+        raise ValueError(f"tokens must be a contiguous 1-d tensor on {device}")
+    return idx
+
+
+def embedding_fwd(table, tokens, scale=1.0, out=None):
+    """out[i] = scale * table[tokens[i]]; a zero row for a token outside
+    the table.  ``table`` [rows, dim] float32, bfloat16 or float16,
+    ``tokens`` [n] int32/int64; ``out`` may be columns of a wider tensor."""
+    import torch
+    dt = _channel_dtype(table)
+    if table.dim() != 2:
+        raise ValueError("table must be [rows, dim]")
+    rows, dim = table.shape
+    _contiguous("table", table, table, (rows, dim))
+    idx = _token_dtype(tokens, table.device)
+    n = tokens.shape[0]
+    if out is None:
+        out = torch.empty((n, dim), dtype=table.dtype, device=table.device)
+        stride = dim
+    else:
+        stride = _rows("out", out, table, n, dim, output=True)
+    _check(lib.embedding_fwd(dt, _ptr(table), rows, dim, _ptr(tokens), idx, n, scale, _ptr(out), stride,
+                             _stream_ptr(table.device)))
+    return out
+
+
+def embedding_bwd_workspace(n, rows, dim):
+    """Bytes of workspace of ``embedding_bwd``."""
+    v = ctypes.c_size_t()
+    _check(lib.embedding_bwd_workspace(n, rows, dim, ctypes.byref(v)))
+    return v.value
+
+
+def embedding_bwd(grad_out, tokens, rows, scale=1.0, workspace=None, grad_table=None):
+    """Gradient of the table of ``embedding_fwd`` ([rows, dim], the dtype of
+    ``grad_out``), the same bits every time."""
+    import torch
+    dt = _channel_dtype(grad_out)
+    idx = _token_dtype(tokens, grad_out.device)
+    n = tokens.shape[0]
+    if grad_out.dim() != 2:
+        raise ValueError("grad_out must be [n, dim]")
+    dim = grad_out.shape[1]
+    stride = _rows("grad_out", grad_out, grad_out, n, dim)
+    if grad_table is None:
+        grad_table = torch.empty((rows, dim), dtype=grad_out.dtype, device=grad_out.device)
+    else:
+        _contiguous("grad_table", grad_table, grad_out, (rows, dim))
+    workspace, nbytes = _channel_workspace(workspace, embedding_bwd_workspace(n, rows, dim), grad_out.device)
+    _check(lib.embedding_bwd(dt, _ptr(grad_out), stride, _ptr(tokens), idx, n, rows, dim, scale, _ptr(grad_table),
+                             _ptr(workspace), nbytes, _stream_ptr(grad_out.device)))
+    return grad_table
+
+
+def _norm_common(x, f, gate, w_post, res_scale, w_pre, kind, gate_act):
+    dt = _channel_dtype(x)
+    if kind not in _NORM_KINDS:
+        raise ValueError("kind is 'rms' or 'layer'")
+    if gate_act not in _GATE_ACTS:
+        raise ValueError("gate_act is 'none' or 'sigmoid'")
+    if x.dim() != 2:
+        raise ValueError("x must be [n, dim]")
+    n, d = x.shape
+    xs, fs, gs, mode = _rows("x", x, x, n, d), _rows("f", f, x, n, d), 0, 0
+    if gate is not None:
+        mode = 1 if gate.dim() == 2 and gate.shape[1] == 1 and d != 1 else 2
+        gs = _rows("gate", gate, x, n, 1 if mode == 1 else d)
+    _param("w_post", w_post, x, d)
+    if res_scale is not None:
+        _param("res_scale", res_scale, x, d)
+    if w_pre is not None:
+        _param("w_pre", w_pre, x, d)
+    return dt, _NORM_KINDS[kind], mode, _GATE_ACTS[gate_act], n, d, xs, fs, gs
+
+
+def block_norm_fwd(x, f, w_post, gate=None, res_scale=None, w_pre=None, kind="rms", gate_act="none", eps=1e-6,
+                   y=None, h=None):
+    """The end of one residual block and the start of the next:
+    y = x + res_scale * gate * (w_post * norm(f)) and h = w_pre * norm(y)
+    (None without ``w_pre``).  ``x``, ``f`` [n, dim] with contiguous rows;
+    ``gate`` None, [n, 1] or [n, dim]; parameters [dim] float32; ``kind``
+    'rms' or 'layer'; ``gate_act`` 'none' or 'sigmoid'."""
+    import torch
+    dt, k, mode, ga, n, d, xs, fs, gs = _norm_common(x, f, gate, w_post, res_scale, w_pre, kind, gate_act)
+    if y is None:
+        y = torch.empty((n, d), dtype=x.dtype, device=x.device)
+    else:
+        _contiguous("y", y, x, (n, d))
+    if w_pre is None:
+        if h is not None:
+            raise ValueError("h needs w_pre")
+    elif h is None:
+        h = torch.empty((n, d), dtype=x.dtype, device=x.device)
+    else:
+        _contiguous("h", h, x, (n, d))
+    _check(lib.block_norm_fwd(dt, k, mode, ga, _ptr(x), xs, _ptr(f), fs, _ptr(gate), gs, _ptr(w_post),
+                              _ptr(res_scale), _ptr(w_pre), eps, n, d, _ptr(y), _ptr(h), _stream_ptr(x.device)))
+    return y, h
+
+
+def block_norm_bwd_workspace(n, dim):
+    """Bytes of workspace of ``block_norm_bwd``."""
+    v = ctypes.c_size_t()
+    _check(lib.block_norm_bwd_workspace(n, dim, ctypes.byref(v)))
+    return v.value
+
+
+def block_norm_bwd(y, grad_y, grad_h, f, w_post, gate=None, res_scale=None, w_pre=None, kind="rms", gate_act="none",
+                   eps=1e-6, workspace=None):
+    """Gradients of ``block_norm_fwd`` from its stored sum ``y``:
+    (grad_x, grad_f, grad_gate, grad_w_post, grad_res_scale, grad_w_pre),
+    None for what was not given.  ``grad_h`` comes with ``w_pre``."""
+    import torch
+    dt, k, mode, ga, n, d, ys, fs, gs = _norm_common(y, f, gate, w_post, res_scale, w_pre, kind, gate_act)
+    gys, ghs = _rows("grad_y", grad_y, y, n, d), 0
+    if (grad_h is None) != (w_pre is None):
+        raise ValueError("grad_h comes with w_pre")
+    if grad_h is not None:
+        ghs = _rows("grad_h", grad_h, y, n, d)
+    dev = y.device
+    gx = torch.empty((n, d), dtype=y.dtype, device=dev)
+    gf = torch.empty((n, d), dtype=y.dtype, device=dev)
+    gg = None if gate is None else torch.empty(gate.shape, dtype=y.dtype, device=dev)
+    gpost = torch.empty(d, dtype=torch.float32, device=dev)
+    gscale = None if res_scale is None else torch.empty(d, dtype=torch.float32, device=dev)
+    gpre = None if w_pre is None else torch.empty(d, dtype=torch.float32, device=dev)
+    workspace, nbytes = _channel_workspace(workspace, block_norm_bwd_workspace(n, d), dev)
+    _check(lib.block_norm_bwd(dt, k, mode, ga, _ptr(y), ys, _ptr(grad_y), gys, _ptr(grad_h), ghs, _ptr(f), fs,
+                              _ptr(gate), gs, _ptr(w_post), _ptr(res_scale), _ptr(w_pre), eps, n, d, _ptr(gx),
+                              _ptr(gf), _ptr(gg), _ptr(gpost), _ptr(gscale), _ptr(gpre), _ptr(workspace), nbytes,
+                              _stream_ptr(dev)))
+    return gx, gf, gg, gpost, gscale, gpre
+
+
+def _ffn_common(x, w_gate, w_up, w_down, act):
+    dt = _channel_dtype(x)
+    if act not in _ACTS:
+        raise ValueError("act is 'silu', 'gelu', 'relu' or 'sigmoid'")
+    if x.dim() != 2 or w_gate.dim() != 2 or w_down.dim() != 2:
+        raise ValueError("x and the weights must be matrices")
+    n, d_in = x.shape
+    hidden, d_out = w_gate.shape[0], w_down.shape[0]
+    stride = _rows("x", x, x, n, d_in)
+    _contiguous("w_gate", w_gate, x, (hidden, d_in))
+    _contiguous("w_up", w_up, x, (hidden, d_in))
+    _contiguous("w_down", w_down, x, (d_out, hidden))
+    return dt, _ACTS[act], n, d_in, hidden, d_out, stride
+
+
+def gated_ffn_workspace(dtype, n, d_in, hidden, d_out, backward=False):
+    """Bytes of workspace of ``gated_ffn_fwd`` / ``gated_ffn_bwd``; ``dtype``
+    one of F32, BF16, F16."""
+    v = ctypes.c_size_t()
+    _check(lib.gated_ffn_workspace(dtype, n, d_in, hidden, d_out, int(backward), ctypes.byref(v)))
+    return v.value
+
+
+def gated_ffn_fwd(x, w_gate, w_up, w_down, act="silu", out=None, workspace=None):
+    """out = (act(x w_gate^T) * (x w_up^T)) w_down^T; ``x`` [n, d_in] with
+    contiguous rows, ``w_gate``, ``w_up`` [hidden, d_in], ``w_down``
+    [d_out, hidden], all of one dtype."""
+    import torch
+    dt, a, n, d_in, hidden, d_out, stride = _ffn_common(x, w_gate, w_up, w_down, act)
+    if out is None:
+        out = torch.empty((n, d_out), dtype=x.dtype, device=x.device)
+        os_ = d_out
+    else:
+        os_ = _rows("out", out, x, n, d_out, output=True)
+    workspace, nbytes = _channel_workspace(workspace, gated_ffn_workspace(dt, n, d_in, hidden, d_out), x.device)
+    _check(lib.gated_ffn_fwd(dt, a, _ptr(x), stride, _ptr(w_gate), _ptr(w_up), _ptr(w_down), n, d_in, hidden, d_out,
+                             _ptr(out), os_, _ptr(workspace), nbytes, _stream_ptr(x.device)))
+    return out
+
+
+def gated_ffn_bwd(x, w_gate, w_up, w_down, grad_out, act="silu", need_dx=True, need_dw=True, workspace=None):
+    """Gradients (grad_x, grad_w_gate, grad_w_up, grad_w_down) of
+    ``gated_ffn_fwd``, None where not needed."""
+    import torch
+    dt, a, n, d_in, hidden, d_out, stride = _ffn_common(x, w_gate, w_up, w_down, act)
+    gs = _rows("grad_out", grad_out, x, n, d_out)
+    if not (need_dx or need_dw):
+        return None, None, None, None
+    gx = torch.empty((n, d_in), dtype=x.dtype, device=x.device) if need_dx else None
+    gwg, gwu, gwd = (torch.empty_like(w) if need_dw else None for w in (w_gate, w_up, w_down))
+    workspace, nbytes = _channel_workspace(workspace, gated_ffn_workspace(dt, n, d_in, hidden, d_out, True), x.device)
+    _check(lib.gated_ffn_bwd(dt, a, _ptr(x), stride, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(grad_out), gs, n,
+                             d_in, hidden, d_out, _ptr(gx), _ptr(gwg), _ptr(gwu), _ptr(gwd), _ptr(workspace), nbytes,
+                             _stream_ptr(x.device)))
+    return gx, gwg, gwu, gwd

@@ -1,0 +1,83 @@
+// Arguments of the invariant-channel kernels (embedding, block norm, gated
+// feed-forward): host and device.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+
+namespace segpoly {
+
+// dtype codes of the C ABI that the invariant-channel operators take
+enum : int { kChF32 = 0, kChBF16 = 2, kChF16 = 3 };
+
+inline int64_t channel_dtype_bytes(int dtype) { return dtype == kChF32 ? 4 : 2; }
+inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+struct EmbeddingArgs {
+  const void* table;   // forward
+  const void* grad;    // backward: [n, dim], row stride grad_stride
+  const void* tokens;
+  void* out;           // forward: [n, dim], row stride out_stride; backward: [rows, dim]
+  int64_t rows, dim, n, out_stride, grad_stride;
+  float scale;
+  int dtype, idx;
+  void* workspace;     // backward
+  void* stream;
+};
+
+// Sorted positions per uniform chunk of the embedding gradient.
+constexpr int kEmbChunk = 32;
+// Tokens one workgroup ranks in a sorting pass.
+constexpr int kEmbSortBlock = 4096;
+
+// Device workspace of the embedding gradient, as byte offsets.
+struct EmbeddingPlan {
+  int bits, passes, digit_bits;
+  int64_t blocks, chunks;
+  size_t key[2], pos[2], hist, rowptr, partial, bytes;
+};
+EmbeddingPlan embedding_plan(int64_t n, int64_t rows, int64_t dim);
+
+int launch_embedding_fwd(const EmbeddingArgs& a);
+int launch_embedding_bwd(const EmbeddingArgs& a);
+
+struct BlockNormArgs {
+  const void *x, *f, *gate;
+  const float *w_post, *res_scale, *w_pre;
+  const void *gy, *gh;
+  void *y, *h;                  // forward outputs
+  void *gx, *gf, *ggate;        // backward outputs
+  float *gpost, *gscale, *gpre;
+  int64_t n, dim;
+  int64_t x_stride, f_stride, gate_stride, gy_stride, gh_stride;  // of inputs; outputs are contiguous
+  float eps;
+  int dtype, kind, gate_mode, gate_act;
+  void* workspace;              // backward
+  int64_t parts;
+  void* stream;
+};
+// widest row one workgroup holds in registers
+constexpr int64_t kBlockNormMaxDim = 16384;
+// workgroups of the backward's row loop = partial rows of its column sums
+int64_t block_norm_parts(int64_t n, int64_t dim);
+int launch_block_norm_fwd(const BlockNormArgs& a);
+int launch_block_norm_bwd(const BlockNormArgs& a);
+
+enum : int { kActSilu = 0, kActGelu = 1, kActRelu = 2, kActSigmoid = 3 };
+
+struct GatedFfnArgs {
+  const void *x, *w_gate, *w_up, *w_down;  // [n, d_in], [hidden, d_in] twice, [d_out, hidden]
+  const void* gout;                        // backward: [n, d_out]
+  void* out;                               // forward: [n, d_out]
+  void *gx, *gw_gate, *gw_up, *gw_down;    // backward, contiguous
+  int64_t n, d_in, hidden, d_out;
+  int64_t x_stride, gout_stride, out_stride;
+  int dtype, act;
+  void* workspace;
+  void* stream;
+};
+// workspace bytes for any strides and alignments of these sizes
+size_t gated_ffn_workspace_bytes(int dtype, int64_t n, int64_t d_in, int64_t hidden, int64_t d_out, bool backward);
+int launch_gated_ffn_fwd(const GatedFfnArgs& a);
+int launch_gated_ffn_bwd(const GatedFfnArgs& a);
+
+}  // namespace segpoly

@@ -1,0 +1,268 @@
+// The gated feed-forward block and its backward as tile products
+// (gemm_tile.hpp), for one element type per translation unit:
+//   forward   h = act(x Wg^T) * (x Wu^T)     one paired product, the
+//                                            activation and gating its epilogue
+//             out = h Wd^T
+//   backward  dh = g Wd
+//             h, dg, du from x, Wg, Wu, dh   the paired product again
+//             dx = dg Wg + du Wu             one product of two phases
+//             dWg = dg^T x, dWu = du^T x     one batch of two
+//             dWd = g^T h
+// Between the products h, dg and du (and dh for the 16-bit types) are held in
+// the operands' type: they are operands of matrix instructions, each rounding
+// is a relative 2^-9 (bf16) or 2^-12 (f16) of one term of a long sum, the
+// size of the inputs' own rounding.  float32 keeps them as three bf16 planes
+// (24 bits) and dh as float32.
+#pragma once
+#include <algorithm>
+
+#include "../launch.hpp"
+#include "gemm_tile.hpp"
+
+namespace segpoly {
+namespace kern {
+
+// A matrix in the form the tile loads take: planes, row stride a multiple
+// of 8, 16-byte aligned, rows zero up to a multiple of 8 columns.
+struct Operand {
+  const uint16_t* plane[3];
+  int64_t ld;
+};
+
+constexpr int kMaxPack = 5;
+struct PackArgs {
+  const void* src[kMaxPack];
+  uint16_t* dst[kMaxPack];
+  int64_t rows[kMaxPack], width[kMaxPack], src_ld[kMaxPack], dst_ld[kMaxPack], plane_stride[kMaxPack];
+};
+
+// 8 columns a lane: copied (16-bit) or split into three planes (float32),
+// zeros past the width
+template <typename Dt>
+__global__ void __launch_bounds__(256)
+pack_kernel(PackArgs g) {
+  using T = typename Dt::T;
+  using E = typename Dt::E;
+  const int o = blockIdx.y;
+  const int64_t chunks = g.dst_ld[o] / 8, total = g.rows[o] * chunks;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = i / chunks, c = i % chunks * 8;
+    const T* src = static_cast<const T*>(g.src[o]) + r * g.src_ld[o] + c;
+    T v[8];
+    if (c + 8 <= g.width[o]) {
+      __builtin_memcpy(v, src, sizeof(v));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = c + j < g.width[o] ? src[j] : T(0.f);
+    }
+    uint16_t* dst = g.dst[o] + r * g.dst_ld[o] + c;
+    if constexpr (Dt::kPlanes == 1) {
+      __builtin_memcpy(dst, v, 16);
+    } else {
+      E p[8][3];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) split3(static_cast<float>(v[j]), p[j]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        E e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = p[j][k];
+        __builtin_memcpy(dst + k * g.plane_stride[o], e, 16);
+      }
+    }
+  }
+}
+
+// Plane pairs of a float32 product, the smallest first.
+constexpr int kPairs3[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
+
+template <typename Dt>
+void add_phases(GemmArgs& g, int& at, const Operand& a, const Operand& b, const Operand* b2 = nullptr) {
+  constexpr int P = Dt::kPlanes == 1 ? 1 : 6;
+  for (int p = 0; p < P; ++p, ++at) {
+    const int ka = P == 1 ? 0 : kPairs3[p][0], kb = P == 1 ? 0 : kPairs3[p][1];
+    g.a[at] = a.plane[ka];
+    g.b[at] = b.plane[kb];
+    if (b2) g.b2[at] = b2->plane[kb];
+  }
+}
+
+template <typename Dt, int BM, int BN, int WM, int WN, bool AAcross, bool BAcross, int Epi>
+int gemm_launch_tile(GemmArgs& g, hipStream_t st) {
+  g.tiles_m = (g.m + BM - 1) / BM;
+  const int64_t bn = Epi == kEpiStore ? BN : BN / 2;
+  g.tiles_n = (g.n + bn - 1) / bn;
+  if (g.tiles_m == 0) return 0;  // no rows
+  hipLaunchKernelGGL((gemm_tile_kernel<Dt, BM, BN, WM, WN, AAcross, BAcross, Epi>),
+                     dim3(static_cast<unsigned>(g.tiles_m * g.tiles_n), 1, static_cast<unsigned>(g.batch)),
+                     dim3(WM * WN * 64), 0, st, g);
+  return static_cast<int>(hipGetLastError());
+}
+
+// The tile with the least estimated time: rounds over the 256 compute units
+// times the tile's own time, which is its share of the work over the share
+// of the matrix rate that size of tile reaches.
+template <typename Dt, bool AAcross, bool BAcross, int Epi>
+int gemm_launch(GemmArgs& g, hipStream_t st) {
+  const int64_t pair = Epi == kEpiStore ? 1 : 2;
+  auto cost = [&](int64_t b, double eff) {
+    const int64_t t = (g.m + b - 1) / b * ((g.n * pair + b - 1) / b) * g.batch;
+    return static_cast<double>((t + 255) / 256) * (b * b) / eff;
+  };
+  const double c256 = cost(256, 1.0), c128 = cost(128, 0.7), c64 = cost(64, 0.4);
+  if (c256 <= c128 && c256 <= c64) return gemm_launch_tile<Dt, 256, 256, 2, 4, AAcross, BAcross, Epi>(g, st);
+  if (c128 <= c64) return gemm_launch_tile<Dt, 128, 128, 2, 2, AAcross, BAcross, Epi>(g, st);
+  return gemm_launch_tile<Dt, 64, 64, 2, 2, AAcross, BAcross, Epi>(g, st);
+}
+
+// Hands out the workspace; with a null base only counts.
+struct Arena {
+  char* base;
+  size_t at = 0;
+  template <typename T>
+  T* take(int64_t count) {
+    const size_t o = at;
+    at += (static_cast<size_t>(count) * sizeof(T) + 255) / 256 * 256;
+    return base ? reinterpret_cast<T*>(base + o) : nullptr;
+  }
+};
+
+template <typename Dt>
+struct FfnPlan {
+  using T = typename Dt::T;
+  static constexpr int P = Dt::kPlanes;
+  Arena arena;
+  PackArgs pack{};
+  int packs = 0;
+  int64_t pack_chunks = 0;
+
+  explicit FfnPlan(void* ws) : arena{static_cast<char*>(ws)} {}
+
+  // worst: as if the matrix had to be packed (the size query)
+  Operand use(const void* src, int64_t rows, int64_t width, int64_t ld, bool worst) {
+    Operand o{};
+    if (!worst && P == 1 && width % 8 == 0 && ld % 8 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0) {
+      o.plane[0] = static_cast<const uint16_t*>(src);
+      o.ld = ld;
+      return o;
+    }
+    o.ld = round_up(width, 8);
+    uint16_t* dst = arena.take<uint16_t>(P * rows * o.ld);
+    if (dst)
+      for (int k = 0; k < P; ++k) o.plane[k] = dst + k * rows * o.ld;
+    pack.src[packs] = src, pack.dst[packs] = dst, pack.rows[packs] = rows, pack.width[packs] = width;
+    pack.src_ld[packs] = ld, pack.dst_ld[packs] = o.ld, pack.plane_stride[packs] = rows * o.ld;
+    pack_chunks = std::max(pack_chunks, rows * (o.ld / 8));
+    ++packs;
+    return o;
+  }
+  Operand hidden(int64_t n, int64_t hidden) {
+    Operand o{};
+    o.ld = round_up(hidden, 64);
+    uint16_t* p = arena.take<uint16_t>(P * n * o.ld);
+    if (p)
+      for (int k = 0; k < P; ++k) o.plane[k] = p + k * n * o.ld;
+    return o;
+  }
+  int run_pack(hipStream_t st) {
+    if (!packs) return 0;
+    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((pack_chunks + 255) / 256, 2048));
+    hipLaunchKernelGGL(pack_kernel<Dt>, dim3(static_cast<unsigned>(blocks), packs), dim3(256), 0, st, pack);
+    return static_cast<int>(hipGetLastError());
+  }
+};
+
+template <typename Dt>
+int ffn_fwd(const GatedFfnArgs& a, size_t* bytes) {
+  const bool worst = bytes != nullptr;
+  FfnPlan<Dt> plan(a.workspace);
+  const Operand x = plan.use(a.x, a.n, a.d_in, a.x_stride, worst);
+  const Operand wg = plan.use(a.w_gate, a.hidden, a.d_in, a.d_in, worst);
+  const Operand wu = plan.use(a.w_up, a.hidden, a.d_in, a.d_in, worst);
+  const Operand wd = plan.use(a.w_down, a.d_out, a.hidden, a.hidden, worst);
+  const Operand h = plan.hidden(a.n, a.hidden);
+  if (worst) {
+    *bytes = plan.arena.at;
+    return 0;
+  }
+  const hipStream_t st = static_cast<hipStream_t>(a.stream);
+  int rc = plan.run_pack(st);
+  if (rc) return rc;
+  // the two weights of the paired product share a row stride: pack decides for both alike but for their alignment
+  GemmArgs g{};
+  add_phases<Dt>(g, g.phases, x, wg, &wu);
+  g.batch = 1, g.m = a.n, g.n = a.hidden, g.k = a.d_in, g.lda = x.ld, g.ldb = wg.ld;
+  g.h = const_cast<uint16_t*>(h.plane[0]), g.ldh = h.ld, g.plane_stride = a.n * h.ld, g.act = a.act;
+  rc = gemm_launch<Dt, false, false, kEpiGated>(g, st);
+  if (rc) return rc;
+  GemmArgs d{};
+  add_phases<Dt>(d, d.phases, h, wd);
+  d.batch = 1, d.m = a.n, d.n = a.d_out, d.k = a.hidden, d.lda = h.ld, d.ldb = wd.ld, d.c[0] = a.out;
+  d.ldc = a.out_stride;
+  return gemm_launch<Dt, false, false, kEpiStore>(d, st);
+}
+
+template <typename Dt>
+int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
+  using DH = typename Dt::DH;
+  // the down projection's product stores dh in the type the gating reads it in
+  const bool worst = bytes != nullptr;
+  FfnPlan<Dt> plan(a.workspace);
+  const Operand x = plan.use(a.x, a.n, a.d_in, a.x_stride, worst);
+  const Operand wg = plan.use(a.w_gate, a.hidden, a.d_in, a.d_in, worst);
+  const Operand wu = plan.use(a.w_up, a.hidden, a.d_in, a.d_in, worst);
+  const Operand wd = plan.use(a.w_down, a.d_out, a.hidden, a.hidden, worst);
+  const Operand go = plan.use(a.gout, a.n, a.d_out, a.gout_stride, worst);
+  const Operand h = plan.hidden(a.n, a.hidden), dg = plan.hidden(a.n, a.hidden), du = plan.hidden(a.n, a.hidden);
+  DH* dh = plan.arena.template take<DH>(a.n * h.ld);
+  if (worst) {
+    *bytes = plan.arena.at;
+    return 0;
+  }
+  const hipStream_t st = static_cast<hipStream_t>(a.stream);
+  int rc = plan.run_pack(st);
+  if (rc) return rc;
+  GemmArgs g{};
+  add_phases<Dt>(g, g.phases, go, wd);
+  g.batch = 1, g.m = a.n, g.n = a.hidden, g.k = a.d_out, g.lda = go.ld, g.ldb = wd.ld, g.c[0] = dh, g.ldc = h.ld;
+  rc = gemm_launch<Dt, false, true, kEpiStore>(g, st);
+  if (rc) return rc;
+  g = GemmArgs{};
+  add_phases<Dt>(g, g.phases, x, wg, &wu);
+  g.batch = 1, g.m = a.n, g.n = a.hidden, g.k = a.d_in, g.lda = x.ld, g.ldb = wg.ld;
+  g.h = const_cast<uint16_t*>(h.plane[0]), g.dg = const_cast<uint16_t*>(dg.plane[0]);
+  g.du = const_cast<uint16_t*>(du.plane[0]), g.dh = dh;
+  g.ldh = h.ld, g.plane_stride = a.n * h.ld, g.act = a.act;
+  rc = gemm_launch<Dt, false, false, kEpiGatedBwd>(g, st);
+  if (rc) return rc;
+  if (a.gx) {
+    g = GemmArgs{};
+    add_phases<Dt>(g, g.phases, dg, wg);
+    add_phases<Dt>(g, g.phases, du, wu);
+    g.batch = 1, g.m = a.n, g.n = a.d_in, g.k = a.hidden, g.lda = dg.ld, g.ldb = wg.ld, g.c[0] = a.gx;
+    g.ldc = a.d_in;
+    rc = gemm_launch<Dt, false, true, kEpiStore>(g, st);
+    if (rc) return rc;
+  }
+  if (a.gw_gate) {
+    g = GemmArgs{};
+    int at = 0;
+    add_phases<Dt>(g, at, dg, x);
+    g.phases = at;
+    add_phases<Dt>(g, at, du, x);
+    g.batch = 2, g.m = a.hidden, g.n = a.d_in, g.k = a.n, g.lda = dg.ld, g.ldb = x.ld;
+    g.c[0] = a.gw_gate, g.c[1] = a.gw_up, g.ldc = a.d_in;
+    rc = gemm_launch<Dt, true, true, kEpiStore>(g, st);
+    if (rc) return rc;
+    g = GemmArgs{};
+    add_phases<Dt>(g, g.phases, go, h);
+    g.batch = 1, g.m = a.d_out, g.n = a.hidden, g.k = a.n, g.lda = go.ld, g.ldb = h.ld, g.c[0] = a.gw_down;
+    g.ldc = a.hidden;
+    rc = gemm_launch<Dt, true, true, kEpiStore>(g, st);
+  }
+  return rc;
+}
+
+}  // namespace kern
+}  // namespace segpoly
