@@ -51,10 +51,11 @@ struct GemmArgs {
 
 enum { kEpiStore = 0, kEpiGated = 1, kEpiGatedBwd = 2 };
 
-// io type T, matrix type E, planes per operand
-struct DtBF16 { using T = bf16; using E = bf16; static constexpr int kPlanes = 1; };
-struct DtF16 { using T = f16; using E = f16; static constexpr int kPlanes = 1; };
-struct DtF32 { using T = float; using E = bf16; static constexpr int kPlanes = 3; };
+// io type T, matrix type E, type DH the hidden gradient is held in between its
+// product and the gating, planes per operand
+struct DtBF16 { using T = bf16; using E = bf16; using DH = bf16; static constexpr int kPlanes = 1; };
+struct DtF16 { using T = f16; using E = f16; using DH = f16; static constexpr int kPlanes = 1; };
+struct DtF32 { using T = float; using E = bf16; using DH = float; static constexpr int kPlanes = 3; };
 
 using u16x8 = uint16_t __attribute__((ext_vector_type(8)));
 using s16x4 = short __attribute__((ext_vector_type(4)));
