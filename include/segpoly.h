@@ -726,14 +726,15 @@ int embedding_fwd(int dtype, const void* table, int64_t rows, int64_t dim, const
                   int64_t n, double scale, void* out, int64_t out_stride, void* stream);
 
 /* embedding_bwd_workspace: bytes embedding_bwd needs (sorted tokens and
- * their positions, row ranges, float32 sums of 32 positions). */
+ * their positions, row ranges, float32 sums of 16 positions; for at most 16
+ * rows the float32 sums of up to 512 segments of the positions). */
 int embedding_bwd_workspace(int64_t n, int64_t rows, int64_t dim, size_t* bytes);
 
 /*
  * embedding_bwd: the table's gradient,
  *   grad_table[r] = scale * sum over i with tokens[i] == r of grad_out[i],
- * summed in float32 in the order of i (in groups of 32 for rows with many
- * tokens) and rounded once; rows no token names are zero, tokens outside
+ * summed in float32 in an order that depends on the sizes and tokens only and
+ * rounded once; rows no token names are zero, tokens outside
  * [0, rows) add nothing.
  *   grad_out [n, dim] T.  grad_table [rows, dim] T, fully overwritten.
  */

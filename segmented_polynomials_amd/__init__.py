@@ -12,6 +12,7 @@ importing this package fails loudly if the library has not been built.
 """
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -977,6 +978,10 @@ def sh_bwd(vec, grad_sh, lmax, normalize=True):
 
 # ------------------------------------------------ invariant-channel operators
 
+# A small call's time is the binding's: sizes of workspaces are remembered, a
+# tensor's address goes to the library as a plain number, and devices are
+# compared by index.
+
 _CHANNEL_DTYPES = {}
 _NORM_KINDS = {"rms": 0, "layer": 1}
 _GATE_ACTS = {"none": 0, "sigmoid": 1}
@@ -993,16 +998,30 @@ def _channel_dtype(t):
         raise ValueError(f"float32, bfloat16 or float16 tensors, not {t.dtype}") from None
 
 
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(index):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on(name, a, like):
+    """Refuses a tensor of another dtype or device than ``like``, or on the host."""
+    if a.dtype != like.dtype or a.get_device() != like.get_device() or not a.is_cuda:
+        raise ValueError(f"{name} must be a {like.dtype} tensor on {like.device}")
+
+
 def _rows(name, a, like, n, d, output=False):
     """Row stride of a [n, d] device tensor of the dtype of `like` with
     contiguous rows."""
-    if a.dtype != like.dtype or a.device != like.device or not a.is_cuda:
-        raise ValueError(f"{name} must be a {like.dtype} tensor on {like.device}")
-    if a.dim() != 2 or a.shape[0] != n or a.shape[1] != d:
+    _on(name, a, like)
+    if a.shape != (n, d):
         raise ValueError(f"{name} must have the shape [{n}, {d}], not {list(a.shape)}")
-    if d > 1 and a.stride(1) != 1:
+    stride, inner = a.stride()
+    if d > 1 and inner != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    stride = a.stride(0)
     if n <= 1:
         return max(stride, d) if output else stride
     if output and stride < d:
@@ -1011,13 +1030,19 @@ def _rows(name, a, like, n, d, output=False):
 
 
 def _param(name, a, like, d):
-    import torch
-    if a.dtype != torch.float32 or a.device != like.device or a.shape != (d,) or not a.is_contiguous():
+    if a.dtype != _f32() or a.get_device() != like.get_device() or a.shape != (d,) or not a.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of {d} on {like.device}")
 
 
+@functools.lru_cache(None)
+def _f32():
+    import torch
+    return torch.float32
+
+
 def _contiguous(name, a, like, shape):
-    if a.dtype != like.dtype or a.device != like.device or not a.is_cuda or a.shape != shape or not a.is_contiguous():
+    _on(name, a, like)
+    if a.shape != shape or not a.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {like.dtype} tensor {list(shape)} on {like.device}")
 
 
@@ -1025,16 +1050,16 @@ def _channel_workspace(workspace, nbytes, device):
     """The caller's workspace, or a new one, and its size in bytes."""
     import torch
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+    if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _token_dtype(tokens, device):
+def _token_dtype(tokens, like):
     idx = _index_dtype(tokens)
-    if tokens.dim() != 1 or tokens.device != device or not tokens.is_contiguous():
-        raise ValueError(f"tokens must be a contiguous 1-d tensor on {device}")
+    if tokens.dim() != 1 or tokens.get_device() != like.get_device() or not tokens.is_contiguous():
+        raise ValueError(f"tokens must be a contiguous 1-d tensor on {like.device}")
     return idx
 
 
@@ -1048,18 +1073,19 @@ def embedding_fwd(table, tokens, scale=1.0, out=None):
         raise ValueError("table must be [rows, dim]")
     rows, dim = table.shape
     _contiguous("table", table, table, (rows, dim))
-    idx = _token_dtype(tokens, table.device)
+    idx = _token_dtype(tokens, table)
     n = tokens.shape[0]
     if out is None:
         out = torch.empty((n, dim), dtype=table.dtype, device=table.device)
         stride = dim
     else:
         stride = _rows("out", out, table, n, dim, output=True)
-    _check(lib.embedding_fwd(dt, _ptr(table), rows, dim, _ptr(tokens), idx, n, scale, _ptr(out), stride,
-                             _stream_ptr(table.device)))
+    _check(lib.embedding_fwd(dt, _adr(table), rows, dim, _adr(tokens), idx, n, scale, _adr(out), stride,
+                             _raw_stream(table.get_device())))
     return out
 
 
+@functools.lru_cache(256)
 def embedding_bwd_workspace(n, rows, dim):
     """Bytes of workspace of ``embedding_bwd``."""
     v = ctypes.c_size_t()
@@ -1072,7 +1098,7 @@ def embedding_bwd(grad_out, tokens, rows, scale=1.0, workspace=None, grad_table=
     ``grad_out``), the same bits every time."""
     import torch
     dt = _channel_dtype(grad_out)
-    idx = _token_dtype(tokens, grad_out.device)
+    idx = _token_dtype(tokens, grad_out)
     n = tokens.shape[0]
     if grad_out.dim() != 2:
         raise ValueError("grad_out must be [n, dim]")
@@ -1083,8 +1109,8 @@ def embedding_bwd(grad_out, tokens, rows, scale=1.0, workspace=None, grad_table=
     else:
         _contiguous("grad_table", grad_table, grad_out, (rows, dim))
     workspace, nbytes = _channel_workspace(workspace, embedding_bwd_workspace(n, rows, dim), grad_out.device)
-    _check(lib.embedding_bwd(dt, _ptr(grad_out), stride, _ptr(tokens), idx, n, rows, dim, scale, _ptr(grad_table),
-                             _ptr(workspace), nbytes, _stream_ptr(grad_out.device)))
+    _check(lib.embedding_bwd(dt, _adr(grad_out), stride, _adr(tokens), idx, n, rows, dim, scale, _adr(grad_table),
+                             _adr(workspace), nbytes, _raw_stream(grad_out.get_device())))
     return grad_table
 
 
@@ -1129,11 +1155,12 @@ def block_norm_fwd(x, f, w_post, gate=None, res_scale=None, w_pre=None, kind="rm
         h = torch.empty((n, d), dtype=x.dtype, device=x.device)
     else:
         _contiguous("h", h, x, (n, d))
-    _check(lib.block_norm_fwd(dt, k, mode, ga, _ptr(x), xs, _ptr(f), fs, _ptr(gate), gs, _ptr(w_post),
-                              _ptr(res_scale), _ptr(w_pre), eps, n, d, _ptr(y), _ptr(h), _stream_ptr(x.device)))
+    _check(lib.block_norm_fwd(dt, k, mode, ga, _adr(x), xs, _adr(f), fs, _adr(gate), gs, _adr(w_post),
+                              _adr(res_scale), _adr(w_pre), eps, n, d, _adr(y), _adr(h), _raw_stream(x.get_device())))
     return y, h
 
 
+@functools.lru_cache(256)
 def block_norm_bwd_workspace(n, dim):
     """Bytes of workspace of ``block_norm_bwd``."""
     v = ctypes.c_size_t()
@@ -1161,10 +1188,10 @@ def block_norm_bwd(y, grad_y, grad_h, f, w_post, gate=None, res_scale=None, w_pr
     gscale = None if res_scale is None else torch.empty(d, dtype=torch.float32, device=dev)
     gpre = None if w_pre is None else torch.empty(d, dtype=torch.float32, device=dev)
     workspace, nbytes = _channel_workspace(workspace, block_norm_bwd_workspace(n, d), dev)
-    _check(lib.block_norm_bwd(dt, k, mode, ga, _ptr(y), ys, _ptr(grad_y), gys, _ptr(grad_h), ghs, _ptr(f), fs,
-                              _ptr(gate), gs, _ptr(w_post), _ptr(res_scale), _ptr(w_pre), eps, n, d, _ptr(gx),
-                              _ptr(gf), _ptr(gg), _ptr(gpost), _ptr(gscale), _ptr(gpre), _ptr(workspace), nbytes,
-                              _stream_ptr(dev)))
+    _check(lib.block_norm_bwd(dt, k, mode, ga, _adr(y), ys, _adr(grad_y), gys, _adr(grad_h), ghs, _adr(f), fs,
+                              _adr(gate), gs, _adr(w_post), _adr(res_scale), _adr(w_pre), eps, n, d, _adr(gx),
+                              _adr(gf), _adr(gg), _adr(gpost), _adr(gscale), _adr(gpre), _adr(workspace), nbytes,
+                              _raw_stream(y.get_device())))
     return gx, gf, gg, gpost, gscale, gpre
 
 
@@ -1183,6 +1210,7 @@ def _ffn_common(x, w_gate, w_up, w_down, act):
     return dt, _ACTS[act], n, d_in, hidden, d_out, stride
 
 
+@functools.lru_cache(256)
 def gated_ffn_workspace(dtype, n, d_in, hidden, d_out, backward=False):
     """Bytes of workspace of ``gated_ffn_fwd`` / ``gated_ffn_bwd``; ``dtype``
     one of F32, BF16, F16."""
@@ -1203,8 +1231,8 @@ def gated_ffn_fwd(x, w_gate, w_up, w_down, act="silu", out=None, workspace=None)
     else:
         os_ = _rows("out", out, x, n, d_out, output=True)
     workspace, nbytes = _channel_workspace(workspace, gated_ffn_workspace(dt, n, d_in, hidden, d_out), x.device)
-    _check(lib.gated_ffn_fwd(dt, a, _ptr(x), stride, _ptr(w_gate), _ptr(w_up), _ptr(w_down), n, d_in, hidden, d_out,
-                             _ptr(out), os_, _ptr(workspace), nbytes, _stream_ptr(x.device)))
+    _check(lib.gated_ffn_fwd(dt, a, _adr(x), stride, _adr(w_gate), _adr(w_up), _adr(w_down), n, d_in, hidden, d_out,
+                             _adr(out), os_, _adr(workspace), nbytes, _raw_stream(x.get_device())))
     return out
 
 
@@ -1219,7 +1247,7 @@ def gated_ffn_bwd(x, w_gate, w_up, w_down, grad_out, act="silu", need_dx=True, n
     gx = torch.empty((n, d_in), dtype=x.dtype, device=x.device) if need_dx else None
     gwg, gwu, gwd = (torch.empty_like(w) if need_dw else None for w in (w_gate, w_up, w_down))
     workspace, nbytes = _channel_workspace(workspace, gated_ffn_workspace(dt, n, d_in, hidden, d_out, True), x.device)
-    _check(lib.gated_ffn_bwd(dt, a, _ptr(x), stride, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(grad_out), gs, n,
-                             d_in, hidden, d_out, _ptr(gx), _ptr(gwg), _ptr(gwu), _ptr(gwd), _ptr(workspace), nbytes,
-                             _stream_ptr(x.device)))
+    _check(lib.gated_ffn_bwd(dt, a, _adr(x), stride, _adr(w_gate), _adr(w_up), _adr(w_down), _adr(grad_out), gs, n,
+                             d_in, hidden, d_out, _adr(gx), _adr(gwg), _adr(gwu), _adr(gwd), _adr(workspace), nbytes,
+                             _raw_stream(x.get_device())))
     return gx, gwg, gwu, gwd

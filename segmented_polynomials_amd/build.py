@@ -71,7 +71,8 @@ def build(verbose=False, jobs=None):
     jobs_list.append(["g++", *HOST_FLAGS, *inc, "-c", os.path.join(gen, "registry.cpp"),
                       "-o", os.path.join(obj, "registry.cpp.o")])
     kernels = [os.path.join(CSRC, "kernels", k) for k in ("generic.hip", "linear.hip", "sh.hip", "fctp_f32.hip", "fctp_f64.hip", "fcconv.hip", "fcconv_bwd.hip", "fctp_ps.hip", "edge_scalars.hip",
-                                                                "embedding.hip", "block_norm.hip", "gated_ffn.hip", "gated_ffn_bf16.hip",
+                                                                "embedding.hip", "block_norm.hip", "block_norm_bf16.hip",
+                                                                "block_norm_f16.hip", "block_norm_f32.hip", "gated_ffn.hip", "gated_ffn_bf16.hip",
                                                                 "gated_ffn_f16.hip", "gated_ffn_f32.hip")]
     kernels.append(os.path.join(CSRC, "noalloc.hip"))
     for h in kernels + gen_hip:

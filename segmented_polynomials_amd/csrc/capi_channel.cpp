@@ -143,7 +143,7 @@ int block_norm_bwd_workspace(int64_t n, int64_t dim, size_t* bytes) {
   if (!bytes) return fail(SEGPOLY_E_INVALID, "null bytes");
   int rc = check_norm(SEGPOLY_F32, SEGPOLY_NORM_RMS, SEGPOLY_GATE_NONE, SEGPOLY_GATE_ACT_NONE, 0, n, dim);
   if (rc) return rc;
-  *bytes = dim == 0 ? 0 : static_cast<size_t>(block_norm_parts(n, dim)) * 3 * dim * 4;
+  *bytes = dim == 0 ? 0 : static_cast<size_t>(block_norm_parts(n, dim)) * 2 * dim * 4;
   return ok();
 }
 
@@ -163,7 +163,7 @@ int block_norm_bwd(int dtype, int kind, int gate_mode, int gate_act, const void*
             (w_pre && (!y || !grad_h))))
     return fail(SEGPOLY_E_INVALID, "null buffer");
   const int64_t parts = block_norm_parts(n, dim);
-  rc = check_workspace(workspace, workspace_bytes, static_cast<size_t>(parts) * 3 * dim * 4);
+  rc = check_workspace(workspace, workspace_bytes, static_cast<size_t>(parts) * 2 * dim * 4);
   if (rc) return rc;
   BlockNormArgs a{};
   a.x = y, a.gy = grad_y, a.gh = grad_h, a.f = f, a.gate = gate, a.w_post = static_cast<const float*>(w_post);

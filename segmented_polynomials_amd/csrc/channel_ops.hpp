@@ -25,12 +25,17 @@ struct EmbeddingArgs {
 };
 
 // Sorted positions per uniform chunk of the embedding gradient.
-constexpr int kEmbChunk = 32;
-// Tokens one workgroup ranks in a sorting pass.
+constexpr int kEmbChunk = 16;
+// Tokens one workgroup ranks in a pass of the sort over several workgroups,
+// and the longest list that one workgroup sorts alone.
 constexpr int kEmbSortBlock = 4096;
+constexpr int kEmbSortAlone = 16384;
+// Tables of at most this many rows are summed in LDS, without a sort.
+constexpr int kEmbDirectRows = 16;
 
 // Device workspace of the embedding gradient, as byte offsets.
 struct EmbeddingPlan {
+  int64_t segments;  // of positions, of a table summed in LDS; else 0
   int bits, passes, digit_bits;
   int64_t blocks, chunks;
   size_t key[2], pos[2], hist, rowptr, partial, bytes;

@@ -471,3 +471,24 @@ def test_graph_replays_and_side_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(captured, step()))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,rows,dim", [(3000, 16, 2056), (50001, 10, 128), (700, 2, 9), (16384, 17, 33),
+                                        (16385, 65536, 40), (15000, 30000, 1032), (5, 4, 4097)])
+def test_embedding_gradient_variants(n, rows, dim, dtype):
+    """Tables summed in LDS (at most 16 rows; several column tiles), the list
+    sorted by one workgroup and by several, ranges with and without whole chunks."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"embedding gradient n={n} rows={rows} dim={dim} {dtype}")
+    g = gen(n + 3 * rows + dim)
+    tok, grad = tokens_of(g, n, rows, torch.int64), rnd(g, n, dim, dtype=dtype)
+    ok = (tok >= 0) & (tok < rows)
+    at, src = tok.clamp(0, rows - 1), grad.double() * ok[:, None]
+    ref = torch.zeros(rows, dim, dtype=torch.float64, device="cuda").index_add_(0, at, src)
+    mag = torch.zeros(rows, dim, dtype=torch.float64, device="cuda").index_add_(0, at, src.abs())
+    count = torch.zeros(rows, dtype=torch.float64, device="cuda").index_add_(0, at, ok.double())
+    d = sp.embedding_bwd(grad, tok, rows)
+    check(d, ref, (count[:, None] + 2) * E24 * mag, dtype, "grad_table")
+    assert torch.equal(sp.embedding_bwd(grad, tok, rows), d)
