@@ -682,7 +682,7 @@ def linear_bwd(h, x, w, grad_out, classes=None, num_classes=None, need_dw=True, 
     if grad_out.shape != (n, h.dim_out) or grad_out.dtype != t or not grad_out.is_contiguous():
         raise ValueError("grad_out has the wrong shape or dtype")
     gx = torch.empty_like(x)
-    gw = torch.empty_like(w) if need_dw else None
+    gw = w.new_empty(w.shape) if need_dw else None
     if need_dw and workspace is None:
         workspace = torch.empty(max(1, linear_bwd_workspace(h, n, nc if classes is not None else 0)),
                                 dtype=torch.uint8, device=x.device)
@@ -1009,7 +1009,8 @@ def _raw_stream(index):
 
 def _on(name, a, like):
     """Refuses a tensor of another dtype or device than ``like``, or on the host."""
-    if a.dtype != like.dtype or a.get_device() != like.get_device() or not a.is_cuda:
+    index = a.get_device()
+    if a is not like and (a.dtype != like.dtype or index != like.get_device()) or index < 0:
         raise ValueError(f"{name} must be a {like.dtype} tensor on {like.device}")
 
 
@@ -1067,7 +1068,6 @@ def embedding_fwd(table, tokens, scale=1.0, out=None):
     """out[i] = scale * table[tokens[i]]; a zero row for a token outside
     the table.  ``table`` [rows, dim] float32, bfloat16 or float16,
     ``tokens`` [n] int32/int64; ``out`` may be columns of a wider tensor."""
-    import torch
     dt = _channel_dtype(table)
     if table.dim() != 2:
         raise ValueError("table must be [rows, dim]")
@@ -1076,7 +1076,7 @@ def embedding_fwd(table, tokens, scale=1.0, out=None):
     idx = _token_dtype(tokens, table)
     n = tokens.shape[0]
     if out is None:
-        out = torch.empty((n, dim), dtype=table.dtype, device=table.device)
+        out = table.new_empty((n, dim))
         stride = dim
     else:
         stride = _rows("out", out, table, n, dim, output=True)
@@ -1096,7 +1096,6 @@ def embedding_bwd_workspace(n, rows, dim):
 def embedding_bwd(grad_out, tokens, rows, scale=1.0, workspace=None, grad_table=None):
     """Gradient of the table of ``embedding_fwd`` ([rows, dim], the dtype of
     ``grad_out``), the same bits every time."""
-    import torch
     dt = _channel_dtype(grad_out)
     idx = _token_dtype(tokens, grad_out)
     n = tokens.shape[0]
@@ -1105,7 +1104,7 @@ def embedding_bwd(grad_out, tokens, rows, scale=1.0, workspace=None, grad_table=
     dim = grad_out.shape[1]
     stride = _rows("grad_out", grad_out, grad_out, n, dim)
     if grad_table is None:
-        grad_table = torch.empty((rows, dim), dtype=grad_out.dtype, device=grad_out.device)
+        grad_table = grad_out.new_empty((rows, dim))
     else:
         _contiguous("grad_table", grad_table, grad_out, (rows, dim))
     workspace, nbytes = _channel_workspace(workspace, embedding_bwd_workspace(n, rows, dim), grad_out.device)
@@ -1142,17 +1141,16 @@ def block_norm_fwd(x, f, w_post, gate=None, res_scale=None, w_pre=None, kind="rm
     (None without ``w_pre``).  ``x``, ``f`` [n, dim] with contiguous rows;
     ``gate`` None, [n, 1] or [n, dim]; parameters [dim] float32; ``kind``
     'rms' or 'layer'; ``gate_act`` 'none' or 'sigmoid'."""
-    import torch
     dt, k, mode, ga, n, d, xs, fs, gs = _norm_common(x, f, gate, w_post, res_scale, w_pre, kind, gate_act)
     if y is None:
-        y = torch.empty((n, d), dtype=x.dtype, device=x.device)
+        y = x.new_empty((n, d))
     else:
         _contiguous("y", y, x, (n, d))
     if w_pre is None:
         if h is not None:
             raise ValueError("h needs w_pre")
     elif h is None:
-        h = torch.empty((n, d), dtype=x.dtype, device=x.device)
+        h = x.new_empty((n, d))
     else:
         _contiguous("h", h, x, (n, d))
     _check(lib.block_norm_fwd(dt, k, mode, ga, _adr(x), xs, _adr(f), fs, _adr(gate), gs, _adr(w_post),
@@ -1173,7 +1171,6 @@ def block_norm_bwd(y, grad_y, grad_h, f, w_post, gate=None, res_scale=None, w_pr
     """Gradients of ``block_norm_fwd`` from its stored sum ``y``:
     (grad_x, grad_f, grad_gate, grad_w_post, grad_res_scale, grad_w_pre),
     None for what was not given.  ``grad_h`` comes with ``w_pre``."""
-    import torch
     dt, k, mode, ga, n, d, ys, fs, gs = _norm_common(y, f, gate, w_post, res_scale, w_pre, kind, gate_act)
     gys, ghs = _rows("grad_y", grad_y, y, n, d), 0
     if (grad_h is None) != (w_pre is None):
@@ -1181,12 +1178,12 @@ def block_norm_bwd(y, grad_y, grad_h, f, w_post, gate=None, res_scale=None, w_pr
     if grad_h is not None:
         ghs = _rows("grad_h", grad_h, y, n, d)
     dev = y.device
-    gx = torch.empty((n, d), dtype=y.dtype, device=dev)
-    gf = torch.empty((n, d), dtype=y.dtype, device=dev)
-    gg = None if gate is None else torch.empty(gate.shape, dtype=y.dtype, device=dev)
-    gpost = torch.empty(d, dtype=torch.float32, device=dev)
-    gscale = None if res_scale is None else torch.empty(d, dtype=torch.float32, device=dev)
-    gpre = None if w_pre is None else torch.empty(d, dtype=torch.float32, device=dev)
+    gx = y.new_empty((n, d))
+    gf = y.new_empty((n, d))
+    gg = None if gate is None else y.new_empty(gate.shape)
+    gpost = w_post.new_empty(d)
+    gscale = None if res_scale is None else w_post.new_empty(d)
+    gpre = None if w_pre is None else w_post.new_empty(d)
     workspace, nbytes = _channel_workspace(workspace, block_norm_bwd_workspace(n, d), dev)
     _check(lib.block_norm_bwd(dt, k, mode, ga, _adr(y), ys, _adr(grad_y), gys, _adr(grad_h), ghs, _adr(f), fs,
                               _adr(gate), gs, _adr(w_post), _adr(res_scale), _adr(w_pre), eps, n, d, _adr(gx),
@@ -1223,10 +1220,9 @@ def gated_ffn_fwd(x, w_gate, w_up, w_down, act="silu", out=None, workspace=None)
     """out = (act(x w_gate^T) * (x w_up^T)) w_down^T; ``x`` [n, d_in] with
     contiguous rows, ``w_gate``, ``w_up`` [hidden, d_in], ``w_down``
     [d_out, hidden], all of one dtype."""
-    import torch
     dt, a, n, d_in, hidden, d_out, stride = _ffn_common(x, w_gate, w_up, w_down, act)
     if out is None:
-        out = torch.empty((n, d_out), dtype=x.dtype, device=x.device)
+        out = x.new_empty((n, d_out))
         os_ = d_out
     else:
         os_ = _rows("out", out, x, n, d_out, output=True)
@@ -1239,13 +1235,12 @@ def gated_ffn_fwd(x, w_gate, w_up, w_down, act="silu", out=None, workspace=None)
 def gated_ffn_bwd(x, w_gate, w_up, w_down, grad_out, act="silu", need_dx=True, need_dw=True, workspace=None):
     """Gradients (grad_x, grad_w_gate, grad_w_up, grad_w_down) of
     ``gated_ffn_fwd``, None where not needed."""
-    import torch
     dt, a, n, d_in, hidden, d_out, stride = _ffn_common(x, w_gate, w_up, w_down, act)
     gs = _rows("grad_out", grad_out, x, n, d_out)
     if not (need_dx or need_dw):
         return None, None, None, None
-    gx = torch.empty((n, d_in), dtype=x.dtype, device=x.device) if need_dx else None
-    gwg, gwu, gwd = (torch.empty_like(w) if need_dw else None for w in (w_gate, w_up, w_down))
+    gx = x.new_empty((n, d_in)) if need_dx else None
+    gwg, gwu, gwd = (w.new_empty(w.shape) if need_dw else None for w in (w_gate, w_up, w_down))
     workspace, nbytes = _channel_workspace(workspace, gated_ffn_workspace(dt, n, d_in, hidden, d_out, True), x.device)
     _check(lib.gated_ffn_bwd(dt, a, _adr(x), stride, _adr(w_gate), _adr(w_up), _adr(w_down), _adr(grad_out), gs, n,
                              d_in, hidden, d_out, _adr(gx), _adr(gwg), _adr(gwu), _adr(gwd), _adr(workspace), nbytes,

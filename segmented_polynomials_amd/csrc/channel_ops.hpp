@@ -29,7 +29,7 @@ constexpr int kEmbChunk = 16;
 // Tokens one workgroup ranks in a pass of the sort over several workgroups,
 // and the longest list that one workgroup sorts alone.
 constexpr int kEmbSortBlock = 4096;
-constexpr int kEmbSortAlone = 16384;
+constexpr int kEmbSortAlone = 4096;
 // Tables of at most this many rows are summed in LDS, without a sort.
 constexpr int kEmbDirectRows = 16;
 

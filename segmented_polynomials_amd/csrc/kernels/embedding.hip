@@ -523,8 +523,7 @@ int embedding_bwd_launch(const EmbeddingArgs& a) {
   const Index* tokens = static_cast<const Index*>(a.tokens);
   int last = 0;
   if (p.blocks == 1) {
-    auto* sort = a.n <= 4096 ? embedding_sort_kernel<Index, true, 4> : embedding_sort_kernel<Index, true, kEmbSortAlone / 1024>;
-    hipLaunchKernelGGL(sort, dim3(1), dim3(1024), 0, st, tokens, nullptr, nullptr, a.rows, a.n, 0, p.passes,
+    hipLaunchKernelGGL((embedding_sort_kernel<Index, true, kEmbSortAlone / 1024>), dim3(1), dim3(1024), 0, st, tokens, nullptr, nullptr, a.rows, a.n, 0, p.passes,
                        p.digit_bits, nullptr, int64_t{1}, key[0], pos[0]);
   } else {
     for (int q = 0; q < p.passes; ++q) {

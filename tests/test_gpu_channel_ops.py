@@ -475,7 +475,7 @@ def test_graph_replays_and_side_stream():
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("n,rows,dim", [(3000, 16, 2056), (50001, 10, 128), (700, 2, 9), (16384, 17, 33),
-                                        (16385, 65536, 40), (15000, 30000, 1032), (5, 4, 4097)])
+                                        (16385, 65536, 40), (40000, 5000, 24), (15000, 30000, 1032), (5, 4, 4097)])
 def test_embedding_gradient_variants(n, rows, dim, dtype):
     """Tables summed in LDS (at most 16 rows; several column tiles), the list
     sorted by one workgroup and by several, ranges with and without whole chunks."""
