@@ -26,7 +26,7 @@ using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 // The chunk at column c of a row of `width` elements, by one 16-byte load
 // from an address that is only element aligned (global accesses of this
 // target may be unaligned).  A chunk that crosses the row's end is loaded
-// from further left, so that it ends with the row; unpack_chunk moves its
+// from further left, so that it ends with the row; settle_chunk moves its
 // elements down and fills up with zeros, after the load has landed: several
 // chunks can be in flight.  Rows narrower than a chunk are read by elements.
 template <typename T>
@@ -53,7 +53,7 @@ __device__ __forceinline__ u32x4 load_raw(const T* row, int c, int width) {
 }
 
 template <typename T>
-__device__ __forceinline__ void unpack_chunk(u32x4 r, int c, int width, float* v) {
+__device__ __forceinline__ u32x4 settle_chunk(u32x4 r, int c, int width) {
   constexpr int N = Chunk<T>::kN;
   if (c < width && c + N > width && width >= N) {
     const int bits = (c + N - width) * (128 / N);  // 1 .. N - 1 elements
@@ -68,6 +68,13 @@ __device__ __forceinline__ void unpack_chunk(u32x4 r, int c, int width, float* v
     r = u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
               static_cast<uint32_t>(hi >> 32)};
   }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack_chunk(u32x4 r, int c, int width, float* v) {
+  constexpr int N = Chunk<T>::kN;
+  r = settle_chunk<T>(r, c, width);
   T t[N];
   __builtin_memcpy(t, &r, 16);
 #pragma unroll

@@ -8,11 +8,12 @@
 //             dx = dg Wg + du Wu             one product of two phases
 //             dWg = dg^T x, dWu = du^T x     one batch of two
 //             dWd = g^T h
-// Between the products h, dg and du (and dh for the 16-bit types) are held in
-// the operands' type: they are operands of matrix instructions, each rounding
-// is a relative 2^-9 (bf16) or 2^-12 (f16) of one term of a long sum, the
-// size of the inputs' own rounding.  float32 keeps them as three bf16 planes
-// (24 bits) and dh as float32.
+// Between the products h, dg and du are held in the operands' type: they are
+// operands of matrix instructions, each rounding is at most a relative 2^-9
+// (bf16) or 2^-12 (f16) of one term of a long sum, the size of the inputs' own
+// rounding.  float32 keeps them as three bf16 planes (24 bits).  dh is no
+// operand and stays float32: rounded as well, it would add half again to the
+// error of dx, dWg and dWu.
 #pragma once
 #include <algorithm>
 
@@ -74,46 +75,67 @@ pack_kernel(PackArgs g) {
   }
 }
 
-// Plane pairs of a float32 product, the smallest first.
-constexpr int kPairs3[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
-
 template <typename Dt>
-void add_phases(GemmArgs& g, int& at, const Operand& a, const Operand& b, const Operand* b2 = nullptr) {
-  constexpr int P = Dt::kPlanes == 1 ? 1 : 6;
-  for (int p = 0; p < P; ++p, ++at) {
-    const int ka = P == 1 ? 0 : kPairs3[p][0], kb = P == 1 ? 0 : kPairs3[p][1];
-    g.a[at] = a.plane[ka];
-    g.b[at] = b.plane[kb];
-    if (b2) g.b2[at] = b2->plane[kb];
+void add_phase(GemmArgs& g, int& at, const Operand& a, const Operand& b, const Operand* b2 = nullptr) {
+  for (int p = 0; p < Dt::kPlanes; ++p) {
+    const int i = at * Dt::kPlanes + p;
+    g.a[i] = a.plane[p];
+    g.b[i] = b.plane[p];
+    if (b2) g.b2[i] = b2->plane[p];
   }
+  ++at;
 }
 
-template <typename Dt, int BM, int BN, int WM, int WN, bool AAcross, bool BAcross, int Epi>
+template <typename Dt, int BM, int BN, int WM, int WN, int KS, int S, bool AAcross, bool BAcross, int Epi>
 int gemm_launch_tile(GemmArgs& g, hipStream_t st) {
   g.tiles_m = (g.m + BM - 1) / BM;
-  const int64_t bn = Epi == kEpiStore ? BN : BN / 2;
+  const int64_t bn = Epi == kEpiGated || Epi == kEpiGatedBwd ? BN / 2 : BN;
   g.tiles_n = (g.n + bn - 1) / bn;
   if (g.tiles_m == 0) return 0;  // no rows
-  hipLaunchKernelGGL((gemm_tile_kernel<Dt, BM, BN, WM, WN, AAcross, BAcross, Epi>),
+  hipLaunchKernelGGL((gemm_tile_kernel<Dt, BM, BN, WM, WN, KS, S, AAcross, BAcross, Epi>),
                      dim3(static_cast<unsigned>(g.tiles_m * g.tiles_n), 1, static_cast<unsigned>(g.batch)),
                      dim3(WM * WN * 64), 0, st, g);
   return static_cast<int>(hipGetLastError());
 }
 
-// The tile with the least estimated time: rounds over the 256 compute units
-// times the tile's own time, which is its share of the work over the share
-// of the matrix rate that size of tile reaches.
+// The tile with the least estimated time.  `each` workgroups of a tile share a
+// compute unit; a full round of 256 x each tiles takes their area over the
+// share of the matrix rate that the tile reaches, a last round with one
+// workgroup or less per unit has them alone, at about 0.6 of that rate.
+// One MI355X, 8192 rows, widths 2048 and 5632, bf16, TFLOP/s: the paired
+// product 1090 with 256 x 256 tiles, 1020 with 128 x 128; its backward form,
+// whose epilogue moves 460 MB, 885 with 256 x 128 in three buffers, 722 with
+// 256 x 256, 831 with 128 x 128; one operand across k 1060 and 1395 with
+// 256 x 256, 970 and 1085 with 128 x 128; both across 1150 and 952 with
+// 256 x 128 in steps of 32, two workgroups a unit, 1086 and 997 with 256 x 256.
 template <typename Dt, bool AAcross, bool BAcross, int Epi>
 int gemm_launch(GemmArgs& g, hipStream_t st) {
-  const int64_t pair = Epi == kEpiStore ? 1 : 2;
-  auto cost = [&](int64_t b, double eff) {
-    const int64_t t = (g.m + b - 1) / b * ((g.n * pair + b - 1) / b) * g.batch;
-    return static_cast<double>((t + 255) / 256) * (b * b) / eff;
+  const int64_t pair = Epi == kEpiGated || Epi == kEpiGatedBwd ? 2 : 1;
+  auto cost = [&](int64_t bm, int64_t bn, int64_t each, double rate) {
+    const int64_t t = (g.m + bm - 1) / bm * ((g.n * pair + bn - 1) / bn) * g.batch;
+    const int64_t full = t / (256 * each), rest = t % (256 * each);
+    const double area = static_cast<double>(bm * bn) / rate, round = area * static_cast<double>(each);
+    return static_cast<double>(full) * round + (rest == 0 ? 0. : rest <= 256 && each > 1 ? area / 0.6 : round);
   };
-  const double c256 = cost(256, 1.0), c128 = cost(128, 0.7), c64 = cost(64, 0.4);
-  if (c256 <= c128 && c256 <= c64) return gemm_launch_tile<Dt, 256, 256, 2, 4, AAcross, BAcross, Epi>(g, st);
-  if (c128 <= c64) return gemm_launch_tile<Dt, 128, 128, 2, 2, AAcross, BAcross, Epi>(g, st);
-  return gemm_launch_tile<Dt, 64, 64, 2, 2, AAcross, BAcross, Epi>(g, st);
+  if constexpr (Dt::kPlanes == 1) {
+    constexpr bool kTwoAcross = AAcross && BAcross, kBwd = Epi == kEpiGatedBwd;
+    const double large = kTwoAcross || kBwd ? cost(256, 128, kBwd ? 1 : 2, 1.0) : cost(256, 256, 1, 1.0);
+    const double c128 = cost(128, 128, 2, 0.9), c64 = cost(64, 64, 2, 0.45);
+    if (large <= c128 && large <= c64) {
+      if constexpr (kTwoAcross)
+        return gemm_launch_tile<Dt, 256, 128, 2, 2, 32, 3, AAcross, BAcross, Epi>(g, st);
+      else if constexpr (kBwd)
+        return gemm_launch_tile<Dt, 256, 128, 4, 2, 64, 3, AAcross, BAcross, Epi>(g, st);
+      else
+        return gemm_launch_tile<Dt, 256, 256, 2, 4, 64, 2, AAcross, BAcross, Epi>(g, st);
+    }
+    if (c128 <= c64) return gemm_launch_tile<Dt, 128, 128, 2, 2, 64, 2, AAcross, BAcross, Epi>(g, st);
+    return gemm_launch_tile<Dt, 64, 64, 2, 2, 64, 4, AAcross, BAcross, Epi>(g, st);
+  } else {
+    if (cost(128, 128, 1, 0.9) <= cost(64, 64, 2, 0.45))
+      return gemm_launch_tile<Dt, 128, 128, 2, 4, 32, 3, AAcross, BAcross, Epi>(g, st);
+    return gemm_launch_tile<Dt, 64, 64, 2, 2, 32, 3, AAcross, BAcross, Epi>(g, st);
+  }
 }
 
 // Hands out the workspace; with a null base only counts.
@@ -191,13 +213,13 @@ int ffn_fwd(const GatedFfnArgs& a, size_t* bytes) {
   if (rc) return rc;
   // the two weights of the paired product share a row stride: pack decides for both alike but for their alignment
   GemmArgs g{};
-  add_phases<Dt>(g, g.phases, x, wg, &wu);
+  add_phase<Dt>(g, g.phases, x, wg, &wu);
   g.batch = 1, g.m = a.n, g.n = a.hidden, g.k = a.d_in, g.lda = x.ld, g.ldb = wg.ld;
   g.h = const_cast<uint16_t*>(h.plane[0]), g.ldh = h.ld, g.plane_stride = a.n * h.ld, g.act = a.act;
   rc = gemm_launch<Dt, false, false, kEpiGated>(g, st);
   if (rc) return rc;
   GemmArgs d{};
-  add_phases<Dt>(d, d.phases, h, wd);
+  add_phase<Dt>(d, d.phases, h, wd);
   d.batch = 1, d.m = a.n, d.n = a.d_out, d.k = a.hidden, d.lda = h.ld, d.ldb = wd.ld, d.c[0] = a.out;
   d.ldc = a.out_stride;
   return gemm_launch<Dt, false, false, kEpiStore>(d, st);
@@ -205,8 +227,6 @@ int ffn_fwd(const GatedFfnArgs& a, size_t* bytes) {
 
 template <typename Dt>
 int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
-  using DH = typename Dt::DH;
-  // the down projection's product stores dh in the type the gating reads it in
   const bool worst = bytes != nullptr;
   FfnPlan<Dt> plan(a.workspace);
   const Operand x = plan.use(a.x, a.n, a.d_in, a.x_stride, worst);
@@ -215,7 +235,7 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
   const Operand wd = plan.use(a.w_down, a.d_out, a.hidden, a.hidden, worst);
   const Operand go = plan.use(a.gout, a.n, a.d_out, a.gout_stride, worst);
   const Operand h = plan.hidden(a.n, a.hidden), dg = plan.hidden(a.n, a.hidden), du = plan.hidden(a.n, a.hidden);
-  DH* dh = plan.arena.template take<DH>(a.n * h.ld);
+  float* dh = plan.arena.template take<float>(a.n * h.ld);
   if (worst) {
     *bytes = plan.arena.at;
     return 0;
@@ -224,12 +244,12 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
   int rc = plan.run_pack(st);
   if (rc) return rc;
   GemmArgs g{};
-  add_phases<Dt>(g, g.phases, go, wd);
+  add_phase<Dt>(g, g.phases, go, wd);
   g.batch = 1, g.m = a.n, g.n = a.hidden, g.k = a.d_out, g.lda = go.ld, g.ldb = wd.ld, g.c[0] = dh, g.ldc = h.ld;
-  rc = gemm_launch<Dt, false, true, kEpiStore>(g, st);
+  rc = gemm_launch<Dt, false, true, kEpiStoreF32>(g, st);
   if (rc) return rc;
   g = GemmArgs{};
-  add_phases<Dt>(g, g.phases, x, wg, &wu);
+  add_phase<Dt>(g, g.phases, x, wg, &wu);
   g.batch = 1, g.m = a.n, g.n = a.hidden, g.k = a.d_in, g.lda = x.ld, g.ldb = wg.ld;
   g.h = const_cast<uint16_t*>(h.plane[0]), g.dg = const_cast<uint16_t*>(dg.plane[0]);
   g.du = const_cast<uint16_t*>(du.plane[0]), g.dh = dh;
@@ -238,8 +258,8 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
   if (rc) return rc;
   if (a.gx) {
     g = GemmArgs{};
-    add_phases<Dt>(g, g.phases, dg, wg);
-    add_phases<Dt>(g, g.phases, du, wu);
+    add_phase<Dt>(g, g.phases, dg, wg);
+    add_phase<Dt>(g, g.phases, du, wu);
     g.batch = 1, g.m = a.n, g.n = a.d_in, g.k = a.hidden, g.lda = dg.ld, g.ldb = wg.ld, g.c[0] = a.gx;
     g.ldc = a.d_in;
     rc = gemm_launch<Dt, false, true, kEpiStore>(g, st);
@@ -248,15 +268,15 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
   if (a.gw_gate) {
     g = GemmArgs{};
     int at = 0;
-    add_phases<Dt>(g, at, dg, x);
+    add_phase<Dt>(g, at, dg, x);
     g.phases = at;
-    add_phases<Dt>(g, at, du, x);
+    add_phase<Dt>(g, at, du, x);
     g.batch = 2, g.m = a.hidden, g.n = a.d_in, g.k = a.n, g.lda = dg.ld, g.ldb = x.ld;
     g.c[0] = a.gw_gate, g.c[1] = a.gw_up, g.ldc = a.d_in;
     rc = gemm_launch<Dt, true, true, kEpiStore>(g, st);
     if (rc) return rc;
     g = GemmArgs{};
-    add_phases<Dt>(g, g.phases, go, h);
+    add_phase<Dt>(g, g.phases, go, h);
     g.batch = 1, g.m = a.d_out, g.n = a.hidden, g.k = a.n, g.lda = go.ld, g.ldb = h.ld, g.c[0] = a.gw_down;
     g.ldc = a.hidden;
     rc = gemm_launch<Dt, true, true, kEpiStore>(g, st);

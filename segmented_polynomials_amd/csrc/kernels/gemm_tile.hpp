@@ -5,22 +5,26 @@
 // ([k][rows]): the second form goes through the transposing LDS read, so no
 // gradient product needs a transposed copy.  float32 operands come as three
 // bf16 planes x = x1 + x2 + x3 (each the bf16 rounding of what is left: 24
-// bits, the whole significand), and a product is the six phases of the plane
-// pairs down to 2^-16 of the first; what is left out is below 2^-24 of it.
+// bits, the whole significand), and a product is the six plane pairs down to
+// 2^-16 of the first, the smallest first; what is left out is below 2^-24 of
+// it.  A step loads the three planes once for its six products.
 //
-// One workgroup computes a BM x BN tile in steps of 64 k.  Both operand
-// tiles go from global memory to LDS directly (16 bytes a lane), one step
-// ahead of the matrix instructions, in two buffers and with one barrier a
-// step.  Such a load writes its wave's 64 lanes in order, so the swizzle that
-// keeps the fragment reads free of bank conflicts is applied to the global
-// address: 16-byte slot s of row r holds chunk s ^ swizzle(r).  Rows, columns and k
-// past the operand's end read as zero (the buffer descriptor's range check).
-// The matrix instruction gets the operands swapped, so a lane holds four
-// neighbouring n of one m and stores them together.
+// One workgroup computes a BM x BN tile in steps of KS k.  The operand tiles
+// go from global memory to LDS directly (16 bytes a lane) into S buffers in
+// turn, S - 1 steps ahead of the matrix instructions and with one barrier a
+// step: the loads of a step have the time of S - 1 steps to land, which a
+// small tile's step alone is too short for.  Such a load writes its wave's 64
+// lanes in order, so the swizzle that keeps the fragment reads free of bank
+// conflicts is applied to the global address: 16-byte slot s of row r holds
+// chunk s ^ swizzle(r).  Rows, columns and k past the operand's end read as
+// zero (the buffer descriptor's range check).  The matrix instruction gets
+// the operands swapped, so a lane holds four neighbouring n of one m and
+// stores them together.
 #pragma once
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../channel_ops.hpp"
 #include "channel_types.hpp"
@@ -29,33 +33,35 @@
 namespace segpoly {
 namespace kern {
 
-constexpr int kStepK = 64;
-constexpr int kMaxPhases = 24;
+constexpr int kMaxPlanes = 6;
 
 struct GemmArgs {
-  const uint16_t* a[kMaxPhases];  // phase p of batch z at [z * phases + p]
-  const uint16_t* b[kMaxPhases];
-  const uint16_t* b2[kMaxPhases];  // second B of a paired product (rows n of both belong together)
+  // plane k of phase p of batch z at [(z * phases + p) * planes + k]
+  const uint16_t* a[kMaxPlanes];
+  const uint16_t* b[kMaxPlanes];
+  const uint16_t* b2[kMaxPlanes];  // second B of a paired product (rows n of both belong together)
   int phases, batch;
-  int64_t m, n, k;        // k: steps run to round_up(k, 64); the operands end at k
+  int64_t m, n, k;        // the sum over k of every phase
   int64_t lda, ldb;       // elements; multiples of 8
   int64_t tiles_m, tiles_n;
   // epilogue
   void* c[2];             // per batch
   int64_t ldc;
   uint16_t *h, *dg, *du;  // paired products: planes of [m][ldh], plane_stride apart
-  const void* dh;         // [m][ldh], the product's 16-bit type or float32
+  const float* dh;        // [m][ldh]
   int64_t ldh, plane_stride;
   int act;
 };
 
-enum { kEpiStore = 0, kEpiGated = 1, kEpiGatedBwd = 2 };
+enum { kEpiStore = 0, kEpiStoreF32 = 1, kEpiGated = 2, kEpiGatedBwd = 3 };
 
-// io type T, matrix type E, type DH the hidden gradient is held in between its
-// product and the gating, planes per operand
-struct DtBF16 { using T = bf16; using E = bf16; using DH = bf16; static constexpr int kPlanes = 1; };
-struct DtF16 { using T = f16; using E = f16; using DH = f16; static constexpr int kPlanes = 1; };
-struct DtF32 { using T = float; using E = bf16; using DH = float; static constexpr int kPlanes = 3; };
+// io type T, matrix type E, planes per operand
+struct DtBF16 { using T = bf16; using E = bf16; static constexpr int kPlanes = 1; };
+struct DtF16 { using T = f16; using E = f16; static constexpr int kPlanes = 1; };
+struct DtF32 { using T = float; using E = bf16; static constexpr int kPlanes = 3; };
+
+// Plane pairs of a float32 product, the smallest first.
+constexpr int kPairs3[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
 
 using u16x8 = uint16_t __attribute__((ext_vector_type(8)));
 using s16x4 = short __attribute__((ext_vector_type(4)));
@@ -112,42 +118,59 @@ __device__ __forceinline__ void act_both(float g, int act, float& a, float& da) 
 
 // ------------------------------------------------------------ operand tiles
 
-// A tile of R rows and 64 k in LDS; Across: stored [k][R], else [R][k].
-template <int R, int Waves, bool Across>
+// A tile of R rows and KS k in LDS; Across: stored [k][R], else [R][k].
+template <int R, int KS, int Waves, bool Across>
 struct TileLoad {
-  static constexpr int kInstr = R / 8 / Waves;  // 1 KB each
-  static constexpr int kRowChunks = Across ? R / 8 : 8;
-  // swizzle of a [k][R] row: the 16 rows that one transposing read of a wave
-  // touches get 16 (fewer: as many as fit) different 32-byte columns
-  __device__ __forceinline__ static int fold(int k) { return (2 * (k % 4 + 4 * (k / 8))) % kRowChunks; }
+  static constexpr int kInstr = R * KS / 512 / Waves;  // 1 KB each
+  static constexpr int kRowChunks = (Across ? R : KS) / 8;
+  static_assert(kInstr >= 1, "every wave loads");
+  // Swizzle of a row.  Stored along k: the 16 rows of a fragment read are 128
+  // (64) bytes apart.  A 16-byte read goes out in groups of 16 lanes such as
+  // 0-3, 12-15, 20-23, 24-27, that is rows 0-3 and 12-15 of one chunk with rows
+  // 4-11 of the next: those get different 16-byte columns of the 256 bytes
+  // that the banks span.  Across: the 16 k that one transposing read of a
+  // wave touches get 16 (fewer: as many as fit) different 32-byte columns.
+  __device__ __forceinline__ static int fold(int row) {
+    if constexpr (Across) return (2 * (row % 4 + 4 * (row / 8))) % kRowChunks;
+    if constexpr (KS == 64) return row % 8;
+    const int x = row / 4 % 4;  // 0, 2, 3, 1
+    return ((x ^ x / 2) & 1) * 2 + x / 2;
+  }
+  // which chunk of its row a lane loads: the same for every instruction of a tile stored along k
+  __device__ __forceinline__ static int lane_chunk(int lane) {
+    return KS == 64 ? (lane % 8) ^ fold(lane / 8) : (lane % 4) ^ fold(lane / 4);
+  }
 
-  uint32_t off[kInstr];  // byte offset of the lane's chunk from the tile's corner
+  uint32_t off[kInstr];  // byte offset of the lane's chunk from the tile's corner (paired: its half's)
+  template <bool Pair>
   __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
 #pragma unroll
     for (int j = 0; j < kInstr; ++j) {
       const int unit = (j * Waves + wave) * 64 + lane;
       const int row = unit / kRowChunks, slot = unit % kRowChunks;
-      const int chunk = Across ? slot ^ fold(row) : slot ^ (row % 8);
-      off[j] = static_cast<uint32_t>(row * ld * 2 + chunk * 16);
+      off[j] = static_cast<uint32_t>((Pair ? row % (R / 2) : row) * ld * 2 + (slot ^ fold(row)) * 16);
     }
   }
-  // k0: first k of the step; row0 may differ per instruction for paired B
+  // an instruction of the second half of a paired tile (whole rows: the same for a wave's lanes)
+  __device__ __forceinline__ static bool second(int j, int wave) {
+    return (j * Waves + wave) * 64 / kRowChunks >= R / 2;
+  }
   template <typename F>
-  __device__ __forceinline__ void issue(uint16_t* lds, int wave, F&& rsrc) const {
+  __device__ __forceinline__ void issue(uint16_t* lds, int wave, bool past, F&& rsrc) const {
 #pragma unroll
     for (int j = 0; j < kInstr; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(j), (LdsVoid*)(lds + (j * Waves + wave) * 512), 16, off[j], 0, 0,
-                                               0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(j), (LdsVoid*)(lds + (j * Waves + wave) * 512), 16,
+                                               past ? 0x80000000u : off[j], 0, 0, 0);
   }
 };
 
-template <int R, bool Across>
+template <int R, int KS, bool Across>
 __device__ __forceinline__ u16x8 read_fragment(const uint16_t* lds, int row0, int kk, int lane) {
+  using Tile = TileLoad<R, KS, 1, Across>;
   if constexpr (!Across) {
     const int r = row0 + lane % 16, chunk = kk * 4 + lane / 16;
-    return *reinterpret_cast<const u16x8*>(lds + r * 64 + ((chunk ^ (r % 8)) * 8));
+    return *reinterpret_cast<const u16x8*>(lds + r * KS + ((chunk ^ Tile::fold(r)) * 8));
   } else {
-    using Tile = TileLoad<R, 1, true>;
     const int i = lane % 16, k = kk * 32 + lane / 16 * 8 + i / 4;
     const int chunk = row0 / 8 + i % 4 / 2;
     const uint16_t* p = lds + k * R + ((chunk ^ Tile::fold(k)) * 8) + i % 2 * 4;
@@ -159,26 +182,43 @@ __device__ __forceinline__ u16x8 read_fragment(const uint16_t* lds, int row0, in
   }
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const uint16_t* base, int64_t first, int64_t end) {
-  // elements [first, end) of base; nothing past 2^31 bytes is addressed from one tile corner
-  const int64_t bytes = first < end ? (end - first) * 2 : 0;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (first < end ? first : 0)), 0,
-                                           static_cast<int>(bytes < 0x7fffffff ? bytes : 0x7fffffff), 0x00020000);
+// `left` bytes from p on; nothing past 2^31 bytes is addressed from one tile corner
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const char* p, int64_t left) {
+  const int bytes = left < 0x7fffffff ? (left > 0 ? static_cast<int>(left) : 0) : 0x7fffffff;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, bytes, 0x00020000);
 }
 
 // ------------------------------------------------------------ the kernel
 
-template <typename Dt, int BM, int BN, int WM, int WN, bool AAcross, bool BAcross, int Epi>
-__global__ void __launch_bounds__(WM * WN * 64)
+// at most N vector memory accesses outstanding, none of LDS, then the barrier;
+// nothing moves across it
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | N / 16 << 14);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <typename Dt, int BM, int BN, int WM, int WN, int KS, int S, bool AAcross, bool BAcross, int Epi>
+__global__ void __launch_bounds__(WM * WN * 64, 2)
 gemm_tile_kernel(GemmArgs g) {
   using E = typename Dt::E;
-  constexpr bool kPair = Epi != kEpiStore;
-  constexpr int kWaves = WM * WN;
+  constexpr bool kPair = Epi == kEpiGated || Epi == kEpiGatedBwd;
+  constexpr int kWaves = WM * WN, P = Dt::kPlanes;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // fragments per wave
-  __shared__ __attribute__((aligned(16))) uint16_t a0[BM * kStepK];
-  __shared__ __attribute__((aligned(16))) uint16_t a1[BM * kStepK];
-  __shared__ __attribute__((aligned(16))) uint16_t b0[BN * kStepK];
-  __shared__ __attribute__((aligned(16))) uint16_t b1[BN * kStepK];
+  constexpr int kStageA = P * BM * KS, kStageB = P * BN * KS;
+  static_assert(S >= 2 && S <= 4, "buffers");
+  // one object per operand and buffer: the compiler then has a fragment read
+  // wait for direct loads into its own object only
+  __shared__ __attribute__((aligned(16))) uint16_t a0[kStageA];
+  __shared__ __attribute__((aligned(16))) uint16_t b0[kStageB];
+  __shared__ __attribute__((aligned(16))) uint16_t a1[kStageA];
+  __shared__ __attribute__((aligned(16))) uint16_t b1[kStageB];
+  __shared__ __attribute__((aligned(16))) uint16_t a2[S > 2 ? kStageA : 8];
+  __shared__ __attribute__((aligned(16))) uint16_t b2[S > 2 ? kStageB : 8];
+  __shared__ __attribute__((aligned(16))) uint16_t a3[S > 3 ? kStageA : 8];
+  __shared__ __attribute__((aligned(16))) uint16_t b3[S > 3 ? kStageB : 8];
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wm = wave / WN, wn = wave % WN;
@@ -197,60 +237,71 @@ gemm_tile_kernel(GemmArgs g) {
   const int64_t n0 = in_band / band_rows * (kPair ? BN / 2 : BN);
   const int z = blockIdx.z;
 
-  TileLoad<BM, kWaves, AAcross> la;
-  TileLoad<BN, kWaves, BAcross> lb;
-  la.init(g.lda, wave, lane);
-  lb.init(g.ldb, wave, lane);
-  if constexpr (kPair) {  // the upper half of the tile's rows is the second matrix's, from its own corner
-#pragma unroll
-    for (int j = lb.kInstr / 2; j < lb.kInstr; ++j) lb.off[j] = lb.off[j - lb.kInstr / 2];
-  }
-  const int64_t steps = (g.k + kStepK - 1) / kStepK;
+  TileLoad<BM, KS, kWaves, AAcross> la;
+  TileLoad<BN, KS, kWaves, BAcross> lb;
+  la.template init<false>(g.lda, wave, lane);
+  lb.template init<kPair>(g.ldb, wave, lane);
   // rows are held (along k: with zeros) up to a multiple of eight elements, and
   // the range check drops a whole chunk that crosses the end
   const int64_t k8 = (g.k + 7) / 8 * 8, m8 = (g.m + 7) / 8 * 8, n8 = (g.n + 7) / 8 * 8;
-  const int64_t a_end = AAcross ? (g.k - 1) * g.lda + m8 : (g.m - 1) * g.lda + k8;
-  const int64_t b_end = BAcross ? (g.k - 1) * g.ldb + n8 : (g.n - 1) * g.ldb + k8;
+  const int64_t fa = AAcross ? m0 : m0 * g.lda, fb = BAcross ? n0 : n0 * g.ldb;  // the tile's corners
+  const int64_t left_a0 = ((AAcross ? (g.k - 1) * g.lda + m8 : (g.m - 1) * g.lda + k8) - fa) * 2;
+  const int64_t left_b0 = ((BAcross ? (g.k - 1) * g.ldb + n8 : (g.n - 1) * g.ldb + k8) - fb) * 2;
+  const int step_a = static_cast<int>(AAcross ? KS * g.lda * 2 : KS * 2);  // bytes
+  const int step_b = static_cast<int>(BAcross ? KS * g.ldb * 2 : KS * 2);
 
-  int phase = 0;
-  int64_t ks = 0;  // step within the phase, of the next load
-  auto issue = [&](uint16_t* la_lds, uint16_t* lb_lds) {
-    const int p = z * g.phases + phase;
-    const int64_t k0 = ks * kStepK;
-    const int64_t left = g.k - k0;  // the last step ends inside a row stored along k
-    const int64_t fa = AAcross ? k0 * g.lda + m0 : m0 * g.lda + k0;
-    const int64_t fb = BAcross ? k0 * g.ldb + n0 : n0 * g.ldb + k0;
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(g.a[p], fa, a_end);
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(g.b[p], fb, b_end);
-    if (left >= kStepK || (AAcross && BAcross)) {
-      la.issue(la_lds, wave, [&](int) { return ra; });
-      if constexpr (kPair) {
-        const __amdgpu_buffer_rsrc_t rb2 = make_rsrc(g.b2[p], fb, b_end);
-        lb.issue(lb_lds, wave, [&](int j) { return j < lb.kInstr / 2 ? rb : rb2; });
-      } else {
-        lb.issue(lb_lds, wave, [&](int) { return rb; });
-      }
-    } else {
-      // chunks at or past k read out of range, that is zero
-      TileLoad<BM, kWaves, AAcross> ta = la;
-      TileLoad<BN, kWaves, BAcross> tb = lb;
-      const int chunk = (lane % 8) ^ (lane / 8);
-      const bool past = chunk * 8 >= left;
-      if constexpr (!AAcross)
+  // the next step to load: its k left, its corners and the bytes from there to the operands' ends
+  int phase = 0, k_left = 0;
+  int64_t left_a = 0, left_b = 0;
+  const char *pa[P], *pb[P], *pb2[P];
+  auto matrices = [&] {
 #pragma unroll
-        for (int j = 0; j < ta.kInstr; ++j) ta.off[j] = past ? 0x80000000u : ta.off[j];
-      if constexpr (!BAcross)
-#pragma unroll
-        for (int j = 0; j < tb.kInstr; ++j) tb.off[j] = past ? 0x80000000u : tb.off[j];
-      ta.issue(la_lds, wave, [&](int) { return ra; });
-      if constexpr (kPair) {
-        const __amdgpu_buffer_rsrc_t rb2 = make_rsrc(g.b2[p], fb, b_end);
-        tb.issue(lb_lds, wave, [&](int j) { return j < tb.kInstr / 2 ? rb : rb2; });
-      } else {
-        tb.issue(lb_lds, wave, [&](int) { return rb; });
-      }
+    for (int q = 0; q < P; ++q) {
+      const int at = (z * g.phases + phase) * P + q;
+      pa[q] = reinterpret_cast<const char*>(g.a[at] + fa);
+      pb[q] = reinterpret_cast<const char*>(g.b[at] + fb);
+      if constexpr (kPair) pb2[q] = reinterpret_cast<const char*>(g.b2[at] + fb);
     }
-    if (++ks == steps) ks = 0, ++phase;
+    k_left = static_cast<int>(g.k);
+    left_a = left_a0;
+    left_b = left_b0;
+  };
+  matrices();
+  if (g.k == 0) left_a = left_b = 0;
+  // Loads are issued for exactly S - 1 steps past the last one too (of nothing:
+  // the range is empty), so that the count of those outstanding is the same in
+  // every step, for the wait below and for the compiler's own.
+  auto issue = [&](uint16_t* to_a, uint16_t* to_b) {
+    // the last step ends inside a row stored along k: chunks at or past k read out of range, that is zero
+    const bool a_past = !AAcross && la.lane_chunk(lane) * 8 >= k_left;
+    const bool b_past = !BAcross && lb.lane_chunk(lane) * 8 >= k_left;
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      const __amdgpu_buffer_rsrc_t ra = make_rsrc(pa[q], left_a);
+      la.issue(to_a + q * BM * KS, wave, a_past, [&](int) { return ra; });
+      pa[q] += step_a;
+    }
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      uint16_t* to = to_b + q * BN * KS;
+      if constexpr (kPair) {
+        lb.issue(to, wave, b_past, [&](int j) { return make_rsrc(lb.second(j, wave) ? pb2[q] : pb[q], left_b); });
+        pb2[q] += step_b;
+      } else {
+        const __amdgpu_buffer_rsrc_t rb = make_rsrc(pb[q], left_b);
+        lb.issue(to, wave, b_past, [&](int) { return rb; });
+      }
+      pb[q] += step_b;
+    }
+    left_a -= step_a;
+    left_b -= step_b;
+    k_left -= KS;
+    if (k_left <= 0) {
+      if (++phase < g.phases)
+        matrices();
+      else
+        left_a = left_b = 0;
+    }
   };
 
   v4f acc[FM][FN];
@@ -266,44 +317,76 @@ gemm_tile_kernel(GemmArgs g) {
     else
       return wn * (BN / WN) + j * 16;
   };
-  auto compute = [&](const uint16_t* pa, const uint16_t* pb) {
+  auto compute = [&](const uint16_t* at_a, const uint16_t* at_b) {
 #pragma unroll
-    for (int kk = 0; kk < kStepK / 32; ++kk) {
-      u16x8 fa[FM], fb[FN];
+    for (int kk = 0; kk < KS / 32; ++kk) {
+      // the transposing reads of two halves at once do not fit in the registers beside a large tile
+      if (AAcross && BAcross && FM * FN >= 32 && kk > 0) asm volatile("" ::: "memory");
+      u16x8 fa[P][FM], fb[P][FN];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) fb[j] = read_fragment<BN, BAcross>(pb, b_row(j), kk, lane);
+      for (int q = 0; q < P; ++q) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) fa[i] = read_fragment<BM, AAcross>(pa, wm * (BM / WM) + i * 16, kk, lane);
+        for (int j = 0; j < FN; ++j)
+          fb[q][j] = read_fragment<BN, KS, BAcross>(at_b + q * BN * KS, b_row(j), kk, lane);
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+        for (int i = 0; i < FM; ++i)
+          fa[q][i] = read_fragment<BM, KS, AAcross>(at_a + q * BM * KS, wm * (BM / WM) + i * 16, kk, lane);
+      }
+      constexpr int kProducts = P == 1 ? 1 : 6;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mma16(E{}, fb[j], fa[i], acc[i][j]);
+      for (int t = 0; t < kProducts; ++t)
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = mma16(E{}, fb[P == 1 ? 0 : kPairs3[t][1]][j], fa[P == 1 ? 0 : kPairs3[t][0]][i], acc[i][j]);
     }
   };
-  auto landed = [] {
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-    __syncthreads();
-  };
 
-  const int64_t total = steps * g.phases;
-  if (total > 0) issue(a0, b0);  // none: a gradient over no rows is zero
-  for (int64_t s = 0; s < total; s += 2) {
-    landed();  // this step's tiles; the other buffers have been read
-    if (s + 1 < total) issue(a1, b1);
-    compute(a0, b0);
-    if (s + 1 >= total) break;
-    landed();
-    if (s + 2 < total) issue(a0, b0);
-    compute(a1, b1);
+  constexpr int kLoads = P * (la.kInstr + lb.kInstr);  // of a wave in a step
+  // One step: its own loads have landed (those of the S - 2 steps after it may
+  // not have) and the buffer read a step ago is free for the one S - 1 ahead.
+  auto step = [&](uint16_t* now_a, uint16_t* now_b, uint16_t* ahead_a, uint16_t* ahead_b) {
+    wait_and_meet<(S - 2) * kLoads>();
+    issue(ahead_a, ahead_b);
+    compute(now_a, now_b);
+  };
+  auto first = [&] {
+    if constexpr (S == 2)
+      step(a0, b0, a1, b1);
+    else if constexpr (S == 3)
+      step(a0, b0, a2, b2);
+    else
+      step(a0, b0, a3, b3);
+  };
+  issue(a0, b0);
+  if constexpr (S > 2) issue(a1, b1);
+  if constexpr (S > 3) issue(a2, b2);
+  // whole turns of the buffers, then what is left: a loop with exits between
+  // the steps would have the compiler wait for loads that are not due
+  int left = (static_cast<int>(g.k) + KS - 1) / KS * g.phases;  // none: a gradient over no rows is zero
+  for (; left >= S; left -= S) {
+    first();
+    step(a1, b1, a0, b0);
+    if constexpr (S > 2) step(a2, b2, a1, b1);
+    if constexpr (S > 3) step(a3, b3, a2, b2);
   }
+  if (left > 0) {
+    first();
+    if (S > 2 && left > 1) {
+      step(a1, b1, a0, b0);
+      if (S > 3 && left > 2) step(a2, b2, a1, b1);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // no load into LDS outlives the workgroup
 
   // ---------------------------------------------------------- epilogue
+  if constexpr (!kPair) {
+    using T = std::conditional_t<Epi == kEpiStoreF32, float, typename Dt::T>;
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t m = m0 + wm * (BM / WM) + i * 16 + lane % 16;
-    if (m >= g.m) continue;
-    if constexpr (Epi == kEpiStore) {
-      using T = typename Dt::T;
+    for (int i = 0; i < FM; ++i) {
+      const int64_t m = m0 + wm * (BM / WM) + i * 16 + lane % 16;
+      if (m >= g.m) continue;
       T* row = static_cast<T*>(g.c[z]) + m * g.ldc;
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
@@ -319,52 +402,99 @@ gemm_tile_kernel(GemmArgs g) {
             if (n + q < g.n) row[n + q] = v[q];
         }
       }
-    } else {
-      const int64_t width = (g.n + 7) / 8 * 8;  // rows of the products' operands are read in 16-byte chunks
+    }
+  } else {
+    // A fragment's lanes hold four columns of sixteen rows, 32 bytes of a line:
+    // the results go through LDS, one 16-bit plane after another in two buffers,
+    // and leave in whole lines.  16-byte slot s of row r holds chunk s ^ r, so
+    // that sixteen rows of a column fall into different banks.
+    constexpr int kChunks = BN / 16;  // of a row
+    constexpr bool kSplit = BM * BN / 2 > kStageA;  // the second half of the rows beside the first
+    static_assert(!kSplit || (WM == 2 && BM * BN / 4 <= kStageA && BM * BN / 4 <= kStageB), "a plane fits in a buffer");
+    const int64_t width = (g.n + 7) / 8 * 8;  // rows of the products' operands are read in 16-byte chunks
+    const int row0 = wm * (BM / WM) + lane % 16, col0 = wn * (BN / 2 / WN) + lane / 16 * 4;
+    auto place = [&](uint16_t* lo, uint16_t* hi, int i, int j, const E(&e)[4]) {
+      const int r = row0 + i * 16, c = col0 + j * 16, at = r * (BN / 2) + ((c / 8 ^ r % kChunks) * 8) + c % 8;
+      if (kSplit && wm == 1)
+        __builtin_memcpy(hi + (at - BM * BN / 4), e, 8);
+      else
+        __builtin_memcpy(lo + at, e, 8);
+    };
+    auto leave = [&](const uint16_t* lo, const uint16_t* hi, uint16_t* to) {
+      wait_and_meet<63>();
 #pragma unroll
-      for (int j = 0; j < FN / 2; ++j) {
-        const int64_t n = n0 + wn * (BN / 2 / WN) + j * 16 + lane / 16 * 4;
-        if (n >= width) continue;
-        const int64_t at = m * g.ldh + n;
-        float h[4], dg[4], du[4];
-        if constexpr (Epi == kEpiGated) {
+      for (int t = 0; t < BM * kChunks / (kWaves * 64); ++t) {
+        const int u = t * kWaves * 64 + static_cast<int>(threadIdx.x), r = u / kChunks, c = u % kChunks;
+        const int at = r * (BN / 2) + (c ^ r % kChunks) * 8;
+        const bool second = kSplit && t >= BM * kChunks / (kWaves * 128);
+        const int64_t m = m0 + r, n = n0 + c * 8;
+        if (m < g.m && n < width)
+          *reinterpret_cast<u16x8*>(to + m * g.ldh + n) =
+              *reinterpret_cast<const u16x8*>(second ? hi + (at - BM * BN / 4) : lo + at);
+      }
+    };
+    int turn = 0;
+    // value(i, j, q): element q of a fragment, as a plane's type
+    auto store = [&](uint16_t* to, auto value) {
+      uint16_t *lo = turn % 2 ? a1 : a0, *hi = turn % 2 ? b1 : b0;
+      ++turn;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) h[q] = act_value(acc[i][j][q], g.act) * acc[i][j + FN / 2][q];
-        } else {
-          typename Dt::DH d[4];
-          __builtin_memcpy(d, static_cast<const typename Dt::DH*>(g.dh) + at, sizeof(d));
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN / 2; ++j) {
+          const E e[4] = {value(i, j, 0), value(i, j, 1), value(i, j, 2), value(i, j, 3)};
+          place(lo, hi, i, j, e);
+        }
+      leave(lo, hi, to);
+    };
+    auto plane = [&](float v, int p) {
+      if constexpr (P == 1) {
+        return static_cast<E>(v);
+      } else {
+        bf16 s[3];
+        split3(v, s);
+        return s[p];
+      }
+    };
+    wait_and_meet<0>();  // every wave has read its last fragments
+    if constexpr (Epi == kEpiGated || P > 1) {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        store(g.h + p * g.plane_stride, [&](int i, int j, int q) {
+          return plane(act_value(acc[i][j][q], g.act) * acc[i][j + FN / 2][q], p);
+        });
+    }
+    if constexpr (Epi == kEpiGatedBwd) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN / 2; ++j) {
+          const int64_t m = m0 + row0 + i * 16, n = n0 + col0 + j * 16;
+          float d[4] = {0.f, 0.f, 0.f, 0.f}, h[4];
+          if (m < g.m && n < width) __builtin_memcpy(d, g.dh + m * g.ldh + n, sizeof(d));
+          // the gradients replace the two products
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float u = acc[i][j + FN / 2][q], dh = n + q < g.n ? static_cast<float>(d[q]) : 0.f;
-            float a, da;
-            act_both(acc[i][j][q], g.act, a, da);
-            h[q] = a * u;
-            dg[q] = dh * u * da;
-            du[q] = dh * a;
+            const float u = acc[i][j + FN / 2][q], dh = n + q < g.n ? d[q] : 0.f;
+            float v, dv;
+            act_both(acc[i][j][q], g.act, v, dv);
+            h[q] = v * u;
+            acc[i][j][q] = dh * u * dv;
+            acc[i][j + FN / 2][q] = dh * v;
+          }
+          if constexpr (P == 1) {
+            const E e[4] = {static_cast<E>(h[0]), static_cast<E>(h[1]), static_cast<E>(h[2]), static_cast<E>(h[3])};
+            place(a0, b0, i, j, e);
           }
         }
-        auto put = [&](uint16_t* to, const float(&v)[4]) {
-          if constexpr (Dt::kPlanes == 1) {
-            E e[4];
+      if constexpr (P == 1) {  // the float32 form has stored h
+        leave(a0, b0, g.h);
+        turn = 1;
+      }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) e[q] = static_cast<E>(v[q]);
-            __builtin_memcpy(to + at, e, 8);
-          } else {
-            bf16 p[4][3];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) split3(v[q], p[q]);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              bf16 e[4] = {p[0][k], p[1][k], p[2][k], p[3][k]};
-              __builtin_memcpy(to + k * g.plane_stride + at, e, 8);
-            }
-          }
-        };
-        put(g.h, h);
-        if constexpr (Epi == kEpiGatedBwd) {
-          put(g.dg, dg);
-          put(g.du, du);
-        }
+      for (int p = 0; p < P; ++p) {
+        store(g.dg + p * g.plane_stride, [&](int i, int j, int q) { return plane(acc[i][j][q], p); });
+        store(g.du + p * g.plane_stride, [&](int i, int j, int q) { return plane(acc[i][j + FN / 2][q], p); });
       }
     }
   }
