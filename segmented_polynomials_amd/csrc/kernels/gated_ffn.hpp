@@ -6,8 +6,7 @@
 //   backward  dh = g Wd
 //             h, dg, du from x, Wg, Wu, dh   the paired product again
 //             dx = dg Wg + du Wu             one product of two phases
-//             dWg = dg^T x, dWu = du^T x     one batch of two
-//             dWd = g^T h
+//             dWg = dg^T x, dWu = du^T x, dWd = g^T h     one launch of the three
 // Between the products h, dg and du are held in the operands' type: they are
 // operands of matrix instructions, each rounding is at most a relative 2^-9
 // (bf16) or 2^-12 (f16) of one term of a long sum, the size of the inputs' own
@@ -16,6 +15,7 @@
 // error of dx, dWg and dWu.
 #pragma once
 #include <algorithm>
+#include <cmath>
 
 #include "../launch.hpp"
 #include "gemm_tile.hpp"
@@ -88,20 +88,23 @@ void add_phase(GemmArgs& g, int& at, const Operand& a, const Operand& b, const O
 
 template <typename Dt, int BM, int BN, int WM, int WN, int KS, int S, bool AAcross, bool BAcross, int Epi>
 int gemm_launch_tile(GemmArgs& g, hipStream_t st) {
-  g.tiles_m = (g.m + BM - 1) / BM;
   const int64_t bn = Epi == kEpiGated || Epi == kEpiGatedBwd ? BN / 2 : BN;
-  g.tiles_n = (g.n + bn - 1) / bn;
-  if (g.tiles_m == 0) return 0;  // no rows
+  int64_t tiles = 0;
+  for (int z = 0; z < g.batch; ++z) {
+    g.tiles_m[z] = (g.m[z] + BM - 1) / BM;
+    g.tiles_n[z] = (g.n[z] + bn - 1) / bn;
+    tiles += g.tiles_m[z] * g.tiles_n[z];
+  }
+  if (tiles == 0) return 0;  // no rows
   hipLaunchKernelGGL((gemm_tile_kernel<Dt, BM, BN, WM, WN, KS, S, AAcross, BAcross, Epi>),
-                     dim3(static_cast<unsigned>(g.tiles_m * g.tiles_n), 1, static_cast<unsigned>(g.batch)),
-                     dim3(WM * WN * 64), 0, st, g);
+                     dim3(static_cast<unsigned>(tiles)), dim3(WM * WN * 64), 0, st, g);
   return static_cast<int>(hipGetLastError());
 }
 
 // The tile with the least estimated time.  `each` workgroups of a tile share a
-// compute unit; a full round of 256 x each tiles takes their area over the
-// share of the matrix rate that the tile reaches, a last round with one
-// workgroup or less per unit has them alone, at about 0.6 of that rate.
+// compute unit; a round of 256 x each tiles takes their area over the share of
+// the matrix rate that the tile reaches.  A last round that is not full counts
+// half way between a whole one and its share (whole with one workgroup a unit).
 // One MI355X, 8192 rows, widths 2048 and 5632, bf16, TFLOP/s: the paired
 // product 1090 with 256 x 256 tiles, 1020 with 128 x 128; its backward form,
 // whose epilogue moves 460 MB, 885 with 256 x 128 in three buffers, 722 with
@@ -111,11 +114,11 @@ int gemm_launch_tile(GemmArgs& g, hipStream_t st) {
 template <typename Dt, bool AAcross, bool BAcross, int Epi>
 int gemm_launch(GemmArgs& g, hipStream_t st) {
   const int64_t pair = Epi == kEpiGated || Epi == kEpiGatedBwd ? 2 : 1;
-  auto cost = [&](int64_t bm, int64_t bn, int64_t each, double rate) {
-    const int64_t t = (g.m + bm - 1) / bm * ((g.n * pair + bn - 1) / bn) * g.batch;
-    const int64_t full = t / (256 * each), rest = t % (256 * each);
-    const double area = static_cast<double>(bm * bn) / rate, round = area * static_cast<double>(each);
-    return static_cast<double>(full) * round + (rest == 0 ? 0. : rest <= 256 && each > 1 ? area / 0.6 : round);
+  auto cost = [&](int64_t bm, int64_t bn, int each, double rate) {
+    int64_t t = 0;
+    for (int z = 0; z < g.batch; ++z) t += (g.m[z] + bm - 1) / bm * ((g.n[z] * pair + bn - 1) / bn);
+    const double rounds = static_cast<double>(t) / (256 * each), whole = std::ceil(rounds);
+    return (each > 1 && rounds > 1 ? 0.5 * (rounds + whole) : whole) * static_cast<double>(bm * bn * each) / rate;
   };
   if constexpr (Dt::kPlanes == 1) {
     constexpr bool kTwoAcross = AAcross && BAcross, kBwd = Epi == kEpiGatedBwd;
@@ -132,9 +135,10 @@ int gemm_launch(GemmArgs& g, hipStream_t st) {
     if (c128 <= c64) return gemm_launch_tile<Dt, 128, 128, 2, 2, 64, 2, AAcross, BAcross, Epi>(g, st);
     return gemm_launch_tile<Dt, 64, 64, 2, 2, 64, 4, AAcross, BAcross, Epi>(g, st);
   } else {
-    if (cost(128, 128, 1, 0.9) <= cost(64, 64, 2, 0.45))
-      return gemm_launch_tile<Dt, 128, 128, 2, 4, 32, 3, AAcross, BAcross, Epi>(g, st);
-    return gemm_launch_tile<Dt, 64, 64, 2, 2, 32, 3, AAcross, BAcross, Epi>(g, st);
+    // 20000 rows of 128 x 512: paired 52 us with 128 x 128 tiles, 48 us with 64 x 64, three workgroups a unit
+    if (cost(128, 128, 1, 0.9) <= cost(64, 64, 3, 0.9))
+      return gemm_launch_tile<Dt, 128, 128, 2, 4, 32, 2, AAcross, BAcross, Epi>(g, st);
+    return gemm_launch_tile<Dt, 64, 64, 2, 2, 32, 2, AAcross, BAcross, Epi>(g, st);
   }
 }
 
@@ -214,14 +218,14 @@ int ffn_fwd(const GatedFfnArgs& a, size_t* bytes) {
   // the two weights of the paired product share a row stride: pack decides for both alike but for their alignment
   GemmArgs g{};
   add_phase<Dt>(g, g.phases, x, wg, &wu);
-  g.batch = 1, g.m = a.n, g.n = a.hidden, g.k = a.d_in, g.lda = x.ld, g.ldb = wg.ld;
+  g.batch = 1, g.m[0] = a.n, g.n[0] = a.hidden, g.k = a.d_in, g.lda[0] = x.ld, g.ldb[0] = wg.ld;
   g.h = const_cast<uint16_t*>(h.plane[0]), g.ldh = h.ld, g.plane_stride = a.n * h.ld, g.act = a.act;
   rc = gemm_launch<Dt, false, false, kEpiGated>(g, st);
   if (rc) return rc;
   GemmArgs d{};
   add_phase<Dt>(d, d.phases, h, wd);
-  d.batch = 1, d.m = a.n, d.n = a.d_out, d.k = a.hidden, d.lda = h.ld, d.ldb = wd.ld, d.c[0] = a.out;
-  d.ldc = a.out_stride;
+  d.batch = 1, d.m[0] = a.n, d.n[0] = a.d_out, d.k = a.hidden, d.lda[0] = h.ld, d.ldb[0] = wd.ld, d.c[0] = a.out;
+  d.ldc[0] = a.out_stride;
   return gemm_launch<Dt, false, false, kEpiStore>(d, st);
 }
 
@@ -245,12 +249,13 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
   if (rc) return rc;
   GemmArgs g{};
   add_phase<Dt>(g, g.phases, go, wd);
-  g.batch = 1, g.m = a.n, g.n = a.hidden, g.k = a.d_out, g.lda = go.ld, g.ldb = wd.ld, g.c[0] = dh, g.ldc = h.ld;
+  g.batch = 1, g.m[0] = a.n, g.n[0] = a.hidden, g.k = a.d_out, g.lda[0] = go.ld, g.ldb[0] = wd.ld, g.c[0] = dh;
+  g.ldc[0] = h.ld;
   rc = gemm_launch<Dt, false, true, kEpiStoreF32>(g, st);
   if (rc) return rc;
   g = GemmArgs{};
   add_phase<Dt>(g, g.phases, x, wg, &wu);
-  g.batch = 1, g.m = a.n, g.n = a.hidden, g.k = a.d_in, g.lda = x.ld, g.ldb = wg.ld;
+  g.batch = 1, g.m[0] = a.n, g.n[0] = a.hidden, g.k = a.d_in, g.lda[0] = x.ld, g.ldb[0] = wg.ld;
   g.h = const_cast<uint16_t*>(h.plane[0]), g.dg = const_cast<uint16_t*>(dg.plane[0]);
   g.du = const_cast<uint16_t*>(du.plane[0]), g.dh = dh;
   g.ldh = h.ld, g.plane_stride = a.n * h.ld, g.act = a.act;
@@ -260,8 +265,8 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
     g = GemmArgs{};
     add_phase<Dt>(g, g.phases, dg, wg);
     add_phase<Dt>(g, g.phases, du, wu);
-    g.batch = 1, g.m = a.n, g.n = a.d_in, g.k = a.hidden, g.lda = dg.ld, g.ldb = wg.ld, g.c[0] = a.gx;
-    g.ldc = a.d_in;
+    g.batch = 1, g.m[0] = a.n, g.n[0] = a.d_in, g.k = a.hidden, g.lda[0] = dg.ld, g.ldb[0] = wg.ld, g.c[0] = a.gx;
+    g.ldc[0] = a.d_in;
     rc = gemm_launch<Dt, false, true, kEpiStore>(g, st);
     if (rc) return rc;
   }
@@ -271,14 +276,24 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
     add_phase<Dt>(g, at, dg, x);
     g.phases = at;
     add_phase<Dt>(g, at, du, x);
-    g.batch = 2, g.m = a.hidden, g.n = a.d_in, g.k = a.n, g.lda = dg.ld, g.ldb = x.ld;
-    g.c[0] = a.gw_gate, g.c[1] = a.gw_up, g.ldc = a.d_in;
-    rc = gemm_launch<Dt, true, true, kEpiStore>(g, st);
-    if (rc) return rc;
-    g = GemmArgs{};
-    add_phase<Dt>(g, g.phases, go, h);
-    g.batch = 1, g.m = a.d_out, g.n = a.hidden, g.k = a.n, g.lda = go.ld, g.ldb = h.ld, g.c[0] = a.gw_down;
-    g.ldc = a.hidden;
+    add_phase<Dt>(g, at, go, h);
+    g.batch = 3, g.k = a.n;
+    for (int z = 0; z < 2; ++z)
+      g.m[z] = a.hidden, g.n[z] = a.d_in, g.lda[z] = dg.ld, g.ldb[z] = x.ld, g.ldc[z] = a.d_in;
+    g.m[2] = a.d_out, g.n[2] = a.hidden, g.lda[2] = go.ld, g.ldb[2] = h.ld, g.ldc[2] = a.hidden;
+    g.c[0] = a.gw_gate, g.c[1] = a.gw_up, g.c[2] = a.gw_down;
+    // Products that do not fill the card share a launch (1357 rows of 322 x 853 x 257: 10 + 9 us apart);
+    // large ones are chosen tiles for each (8192 x 2048 x 5632: 329 + 192 us apart, 578 us together).
+    const int64_t tiles = round_up(a.hidden, 64) / 64 * (round_up(a.d_in, 64) / 64 * 2 + round_up(a.d_out, 64) / 64);
+    if (tiles > 1024) {
+      GemmArgs d{};
+      add_phase<Dt>(d, d.phases, go, h);
+      d.batch = 1, d.k = a.n, d.m[0] = g.m[2], d.n[0] = g.n[2], d.lda[0] = go.ld, d.ldb[0] = h.ld;
+      d.c[0] = a.gw_down, d.ldc[0] = a.hidden;
+      rc = gemm_launch<Dt, true, true, kEpiStore>(d, st);
+      if (rc) return rc;
+      g.batch = 2;
+    }
     rc = gemm_launch<Dt, true, true, kEpiStore>(g, st);
   }
   return rc;
