@@ -2,7 +2,7 @@
 // (gemm_tile.hpp), for one element type per translation unit:
 //   forward   h = act(x Wg^T) * (x Wu^T)     one paired product, the
 //                                            activation and gating its epilogue
-//             out = h Wd^T
+//             out = h Wd^T                   (at most 64 rows: gemm_rows.hpp)
 //   backward  dh = g Wd
 //             h, dg, du from x, Wg, Wu, dh   the paired product again
 //             dx = dg Wg + du Wu             one product of two phases
@@ -18,6 +18,7 @@
 #include <cmath>
 
 #include "../launch.hpp"
+#include "gemm_rows.hpp"
 #include "gemm_tile.hpp"
 
 namespace segpoly {
@@ -123,7 +124,7 @@ int gemm_launch(GemmArgs& g, hipStream_t st) {
   if constexpr (Dt::kPlanes == 1) {
     constexpr bool kTwoAcross = AAcross && BAcross, kBwd = Epi == kEpiGatedBwd;
     const double large = kTwoAcross || kBwd ? cost(256, 128, kBwd ? 1 : 2, 1.0) : cost(256, 256, 1, 1.0);
-    const double c128 = cost(128, 128, 2, 0.9), c64 = cost(64, 64, 2, 0.45);
+    const double c128 = cost(128, 128, 2, 0.8), c64 = cost(64, 64, 2, 0.45);
     if (large <= c128 && large <= c64) {
       if constexpr (kTwoAcross)
         return gemm_launch_tile<Dt, 256, 128, 2, 2, 32, 3, AAcross, BAcross, Epi>(g, st);
@@ -202,6 +203,18 @@ struct FfnPlan {
 template <typename Dt>
 int ffn_fwd(const GatedFfnArgs& a, size_t* bytes) {
   const bool worst = bytes != nullptr;
+  if (a.n <= kFewRows) {
+    Arena arena{static_cast<char*>(a.workspace)};
+    const int64_t ldh = round_up(a.hidden, 8);
+    void* h = arena.take<typename Dt::T>(a.n * ldh);
+    if (worst) {
+      *bytes = arena.at;
+      return 0;
+    }
+    const hipStream_t st = static_cast<hipStream_t>(a.stream);
+    const int rc = gemm_rows<Dt, true>({a.x, a.w_gate, a.w_up, h, a.n, a.hidden, a.d_in, a.x_stride, ldh, a.act}, st);
+    return rc ? rc : gemm_rows<Dt, false>({h, a.w_down, nullptr, a.out, a.n, a.d_out, a.hidden, ldh, a.out_stride, 0}, st);
+  }
   FfnPlan<Dt> plan(a.workspace);
   const Operand x = plan.use(a.x, a.n, a.d_in, a.x_stride, worst);
   const Operand wg = plan.use(a.w_gate, a.hidden, a.d_in, a.d_in, worst);

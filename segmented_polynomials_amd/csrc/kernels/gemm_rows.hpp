@@ -1,0 +1,160 @@
+// Products of a few rows with a weight matrix, out[m, o] = sum over k of
+// x[m, k] w[o, k] for m < 64: bound by reading the weights once.  A workgroup
+// takes 16 weight rows (paired: of both matrices) and its waves share out the
+// sum over k, 64 k at a time; weights and rows go from memory straight into
+// the matrix instructions' registers, with no staging and no barrier before
+// the waves' sums are added, in order, through LDS.  So many loads are in
+// flight that one pass over them is hardly longer than a single load: with 16
+// waves of 4 KB each 64 workgroups already ask for the whole of 8 MB.  Loads
+// are of 16 bytes at any alignment, float32 is split into its planes in
+// registers: no operand is copied first.
+// One MI355X, 3 rows, 1024 x 4096 bf16: gate, up and down take 6 + 8 us, as tiles of
+// 64 x 64 (gemm_tile.hpp) 8 + 18 us.
+#pragma once
+#include <algorithm>
+
+#include "gemm_tile.hpp"
+
+namespace segpoly {
+namespace kern {
+
+// Rows at most this many take this form.
+constexpr int64_t kFewRows = 64;
+
+struct RowsArgs {
+  const void *x, *w, *w2;  // [m][k] with row stride ldx, [n][k] dense; w2 of a paired product
+  void* out;               // [m][ldo]
+  int64_t m, n, k, ldx, ldo;
+  int act;
+};
+
+// eight k of a row from column c on, as the planes of a matrix operand
+template <typename Dt>
+struct RowChunk {
+  using T = typename Dt::T;
+  static constexpr int kLoads = sizeof(T) / 2;
+  u32x4 raw[kLoads];
+  __device__ __forceinline__ void load(const T* row, int c, int width) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) raw[i] = load_raw(row, c + i * 4, width);
+  }
+  __device__ __forceinline__ void planes(int c, int width, u16x8 (&p)[Dt::kPlanes]) const {
+    if constexpr (Dt::kPlanes == 1) {
+      p[0] = __builtin_bit_cast(u16x8, settle_chunk<T>(raw[0], c, width));
+    } else {
+      float v[8];
+      unpack_chunk<T>(raw[0], c, width, v);
+      unpack_chunk<T>(raw[1], c + 4, width, v + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        bf16 s[3];
+        split3(v[i], s);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) p[q][i] = __builtin_bit_cast(uint16_t, s[q]);
+      }
+    }
+  }
+};
+
+// Waves of a workgroup: eight where the planes of more rows take their registers.
+template <typename Dt>
+constexpr int rows_waves(int m16) {
+  return Dt::kPlanes > 1 && m16 > 1 ? 8 : 16;
+}
+
+// M16: blocks of 16 rows of x
+template <typename Dt, int M16, bool Pair>
+__global__ void __launch_bounds__(rows_waves<Dt>(M16) * 64)
+gemm_rows_kernel(RowsArgs g) {
+  using T = typename Dt::T;
+  constexpr int P = Dt::kPlanes, W = Pair ? 2 : 1;
+  __shared__ v4f sums[rows_waves<Dt>(M16)][W][64];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, waves = blockDim.x / 64;
+  const int k = static_cast<int>(g.k);
+  const int64_t o = static_cast<int64_t>(blockIdx.x) * 16 + lane % 16, last = g.n - 1;
+  const T* w[W];  // rows past the last repeat it, and are not stored
+  w[0] = static_cast<const T*>(g.w) + (o < last ? o : last) * g.k;
+  if constexpr (Pair) w[1] = static_cast<const T*>(g.w2) + (o < last ? o : last) * g.k;
+  const T* x[M16];
+#pragma unroll
+  for (int i = 0; i < M16; ++i) {
+    const int64_t m = i * 16 + lane % 16;
+    x[i] = static_cast<const T*>(g.x) + (m < g.m ? m : g.m - 1) * g.ldx;
+  }
+  v4f acc[W][M16];
+#pragma unroll
+  for (int j = 0; j < W; ++j)
+#pragma unroll
+    for (int i = 0; i < M16; ++i) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+  for (int k0 = wave * 64; k0 < k; k0 += waves * 64) {
+    RowChunk<Dt> rw[2][W], rx[2][M16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = k0 + h * 32 + lane / 16 * 8;
+#pragma unroll
+      for (int j = 0; j < W; ++j) rw[h][j].load(w[j], c, k);
+#pragma unroll
+      for (int i = 0; i < M16; ++i) rx[h][i].load(x[i], c, k);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = k0 + h * 32 + lane / 16 * 8;
+      u16x8 pw[W][P];
+#pragma unroll
+      for (int j = 0; j < W; ++j) rw[h][j].planes(c, k, pw[j]);
+#pragma unroll
+      for (int i = 0; i < M16; ++i) {
+        u16x8 px[P];
+        rx[h][i].planes(c, k, px);
+        constexpr int kProducts = P == 1 ? 1 : 6;
+#pragma unroll
+        for (int t = 0; t < kProducts; ++t)
+#pragma unroll
+          for (int j = 0; j < W; ++j)
+            acc[j][i] = mma16(typename Dt::E{}, pw[j][P == 1 ? 0 : kPairs3[t][1]], px[P == 1 ? 0 : kPairs3[t][0]],
+                              acc[j][i]);
+      }
+    }
+  }
+  // lane l of a fragment holds weight rows l / 16 * 4 + q of row l % 16
+#pragma unroll
+  for (int i = 0; i < M16; ++i) {
+    if (i) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < W; ++j) sums[wave][j][lane] = acc[j][i];
+    __syncthreads();
+    if (threadIdx.x < 256) {
+      const int l = threadIdx.x / 16 + threadIdx.x % 16 / 4 * 16, q = threadIdx.x % 4;
+      float v[W];
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        v[j] = 0.f;
+        for (int s = 0; s < waves; ++s) v[j] += sums[s][j][l][q];
+      }
+      const int64_t m = i * 16 + l % 16, n = static_cast<int64_t>(blockIdx.x) * 16 + l / 16 * 4 + q;
+      if (m < g.m && n < g.n) {
+        if constexpr (Pair) v[0] = act_value(v[0], g.act) * v[1];
+        static_cast<T*>(g.out)[m * g.ldo + n] = static_cast<T>(v[0]);
+      }
+    }
+  }
+}
+
+template <typename Dt, int M16, bool Pair>
+int gemm_rows_launch(const RowsArgs& g, hipStream_t st) {
+  const int64_t waves = std::min<int64_t>(rows_waves<Dt>(M16), std::max<int64_t>(4, (g.k + 63) / 64));
+  hipLaunchKernelGGL((gemm_rows_kernel<Dt, M16, Pair>), dim3(static_cast<unsigned>((g.n + 15) / 16)),
+                     dim3(static_cast<unsigned>(waves * 64)), 0, st, g);
+  return static_cast<int>(hipGetLastError());
+}
+
+template <typename Dt, bool Pair>
+int gemm_rows(const RowsArgs& g, hipStream_t st) {
+  if (g.m <= 16) return gemm_rows_launch<Dt, 1, Pair>(g, st);
+  if (g.m <= 32) return gemm_rows_launch<Dt, 2, Pair>(g, st);
+  return gemm_rows_launch<Dt, 4, Pair>(g, st);
+}
+
+}  // namespace kern
+}  // namespace segpoly

@@ -492,3 +492,25 @@ def test_embedding_gradient_variants(n, rows, dim, dtype):
     d = sp.embedding_bwd(grad, tok, rows)
     check(d, ref, (count[:, None] + 2) * E24 * mag, dtype, "grad_table")
     assert torch.equal(sp.embedding_bwd(grad, tok, rows), d)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,di,F,do", [(1, 2048, 5632, 2048), (16, 70, 33, 130), (31, 129, 1000, 15), (64, 515, 77, 64),
+                                       (40, 5, 3, 2)])
+def test_gated_ffn_few_rows(n, di, F, do, dtype):
+    """The form of at most 64 rows, with rows off 16 bytes, one row read by
+    all, and untouched neighbours of the output."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"gated ffn, few rows n={n} d_in={di} hidden={F} d_out={do} {dtype}")
+    x, wg, wu, wd, gy = ffn_case(n, di, F, do, dtype, n + di)
+    (out, eout), _ = ffn_reference(x, wg, wu, wd, gy, "gelu", dtype)
+    got = sp.gated_ffn_fwd(x, wg, wu, wd, act="gelu")
+    check(got, out, eout, dtype, "out")
+    wide = torch.full((n, di + 7), float("nan"), dtype=T[dtype], device="cuda")
+    wide[:, 3:3 + di] = x
+    to = torch.full((n, do + 9), 5.0, dtype=T[dtype], device="cuda")
+    sp.gated_ffn_fwd(wide[:, 3:3 + di], wg, wu, wd, act="gelu", out=to[:, 4:4 + do])
+    assert torch.equal(to[:, 4:4 + do], got) and bool((to[:, :4] == 5).all()) and bool((to[:, 4 + do:] == 5).all())
+    one = sp.gated_ffn_fwd(x[:1].expand(n, di), wg, wu, wd, act="gelu")
+    assert torch.equal(one, got[:1].expand(n, do))
