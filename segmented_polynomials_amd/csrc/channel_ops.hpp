@@ -26,16 +26,22 @@ struct EmbeddingArgs {
 
 // Sorted positions per uniform chunk of the embedding gradient.
 constexpr int kEmbChunk = 16;
-// Tokens one workgroup ranks in a pass of the sort over several workgroups,
-// and the longest list that one workgroup sorts alone.
+// Tokens one workgroup ranks in a sorting pass.
 constexpr int kEmbSortBlock = 4096;
-constexpr int kEmbSortAlone = 4096;
+// Lists up to this many tokens into up to this many rows are ordered in one
+// launch: kEmbGroups workgroups, group w those of the rows r = w modulo kEmbGroups.
+constexpr int kEmbGroups = 256;
+constexpr int64_t kEmbOrderTokens = 32768;
+constexpr int64_t kEmbOrderRows = 512 * kEmbGroups;
 // Tables of at most this many rows are summed in LDS, without a sort.
 constexpr int kEmbDirectRows = 16;
 
 // Device workspace of the embedding gradient, as byte offsets.
 struct EmbeddingPlan {
   int64_t segments;  // of positions, of a table summed in LDS; else 0
+  // Row r has range (r % groups) * per_group + r / groups of the sorted list.
+  int groups;              // kEmbGroups for a list ordered in one launch, else 1
+  int64_t per_group, keys;  // keys: ranges, and the key of a token out of range
   int bits, passes, digit_bits;
   int64_t blocks, chunks;
   size_t key[2], pos[2], hist, rowptr, partial, bytes;

@@ -7,10 +7,11 @@
 // every time; sums are float32 and rounded once.  A table of a few rows is
 // summed in LDS, every lane group into a copy of its own, over as many
 // segments of positions as fill the chip, whose sums a second kernel adds.
-// For other tables a stable radix sort orders (token, position), each table
-// row is one range of the sorted list, and whole chunks of kEmbChunk
-// positions of one row are summed first, so that a frequent token's range
-// is shared out.
+// For other tables a stable sort orders (token, position), each table row is
+// one range of the sorted list, and whole chunks of kEmbChunk positions of one
+// row are summed first, so that a frequent token's range is shared out.  The
+// sort is one launch where every workgroup can read all tokens and keep those
+// of its rows in LDS, a radix sort above.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -29,11 +30,15 @@ EmbeddingPlan embedding_plan(int64_t n, int64_t rows, int64_t dim) {
     p.bytes = round_up(4 * p.segments * rows * dim, 256);
     return p;
   }
+  const bool order = n <= kEmbOrderTokens && rows <= kEmbOrderRows;
+  p.groups = order ? kEmbGroups : 1;
+  p.per_group = (rows + p.groups - 1) / p.groups;
+  p.keys = p.per_group * p.groups;
   p.bits = 1;
   while ((int64_t{1} << p.bits) <= rows) ++p.bits;  // keys 0 .. rows (rows: token out of range)
-  p.passes = (p.bits + 9) / 10;
-  p.digit_bits = (p.bits + p.passes - 1) / p.passes;
-  p.blocks = n > kEmbSortAlone ? (n + kEmbSortBlock - 1) / kEmbSortBlock : 1;
+  p.passes = order ? 0 : (p.bits + 9) / 10;
+  p.digit_bits = order ? 0 : (p.bits + p.passes - 1) / p.passes;
+  p.blocks = (n + kEmbSortBlock - 1) / kEmbSortBlock;
   p.chunks = n / kEmbChunk;
   size_t at = 0;
   auto take = [&at](size_t bytes) {
@@ -41,9 +46,9 @@ EmbeddingPlan embedding_plan(int64_t n, int64_t rows, int64_t dim) {
     at += (bytes + 255) / 256 * 256;
     return o;
   };
-  for (int i = 0; i < 2; ++i) p.key[i] = take(4 * n), p.pos[i] = take(4 * n);
+  for (int i = 0; i < (order ? 1 : 2); ++i) p.key[i] = take(4 * n), p.pos[i] = take(4 * n);
   p.hist = take((size_t{4} << p.digit_bits) * p.blocks);
-  p.rowptr = take(4 * (rows + 1));
+  p.rowptr = take(4 * (p.keys + 1));
   p.partial = take(4 * p.chunks * round_up(dim, 8));
   p.bytes = at;
   return p;
@@ -212,120 +217,198 @@ __device__ __forceinline__ uint32_t scan1024(uint32_t v, uint32_t* wave_sum) {
   return before + s - v;
 }
 
-// One stable pass over a block of positions: wave w owns consecutive ones in
-// steps of 64 (as many as share the list evenly); the lanes of a step with an equal digit are
-// found by one ballot per digit bit, so a position's rank is its wave's
-// running count of the digit plus the equal lanes below it.  With `Single`
-// the whole list is one block and every pass runs here, through LDS.
-template <typename Index, bool Single, int kSteps>
+// lanes of the wave that are on and have the same key of `bits` bits, by one ballot per bit
+__device__ __forceinline__ uint64_t equal_lanes(bool on, uint32_t key, int bits) {
+  uint64_t peers = __ballot(on);
+  for (int b = 0; b < bits; ++b) {
+    const bool bit = (key >> b) & 1;
+    const uint64_t with = __ballot(bit);
+    peers &= bit ? with : ~with;
+  }
+  return peers;
+}
+__device__ __forceinline__ uint32_t lanes_below(uint64_t mask) {
+  return __popcll(mask & ((uint64_t{1} << (threadIdx.x % 64)) - 1));
+}
+
+// One stable pass over a block of positions: wave w owns 256 consecutive
+// ones in four steps of 64; a position's rank is its wave's running count of
+// the digit plus the equal lanes below it.
+template <typename Index>
 __global__ void __launch_bounds__(1024)
 embedding_sort_kernel(const Index* __restrict__ tokens, const uint32_t* __restrict__ keys_in,
-                      const uint32_t* __restrict__ pos_in, int64_t rows, int64_t n, int pass, int passes, int bits,
+                      const uint32_t* __restrict__ pos_in, int64_t rows, int64_t n, int shift, int bits,
                       const uint32_t* __restrict__ hist, int64_t blocks, uint32_t* __restrict__ keys_out,
                       uint32_t* __restrict__ pos_out) {
+  constexpr int kSteps = kEmbSortBlock / 1024;
   __shared__ uint16_t count[16 * 1024];
   __shared__ uint32_t base[1024];
   __shared__ uint32_t wave_sum[16];
-  __shared__ uint32_t lkey[Single ? kSteps * 1024 : 1];
-  __shared__ uint16_t lpos[Single ? kSteps * 1024 : 1];
   const int D = 1 << bits;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t b0 = static_cast<int64_t>(blockIdx.x) * kEmbSortBlock;
-  const int steps = Single ? static_cast<int>((n + 1023) / 1024) : kSteps;
-  const int p0 = wave * steps * 64 + lane;  // position within the block at step 0
-  uint32_t key[kSteps], pos[kSteps];
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kEmbSortBlock + wave * 256 + lane;
+  uint32_t key[kSteps], pos[kSteps], rank[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    const int64_t i = b0 + p0 + s * 64;
+    const int64_t i = i0 + s * 64;
     key[s] = 0, pos[s] = 0;
-    if (s < steps && i < n) {
+    if (i < n) {
       key[s] = keys_in ? keys_in[i] : token_key(tokens[i], rows);
       pos[s] = pos_in ? pos_in[i] : static_cast<uint32_t>(i);
     }
   }
+  for (int d = threadIdx.x; d < 16 * D; d += 1024) count[d] = 0;
+  __syncthreads();
   volatile uint16_t* mine = count + wave * D;
-  for (int p = Single ? 0 : pass; p < (Single ? passes : pass + 1); ++p) {
-    const int shift = p * bits;
-    for (int d = threadIdx.x; d < 16 * D; d += 1024) count[d] = 0;
-    __syncthreads();
-    uint32_t rank[kSteps];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      if (s >= steps) break;
-      const bool on = b0 + p0 + s * 64 < n;
-      const uint32_t d = (key[s] >> shift) & (D - 1);
-      uint64_t peers = __ballot(on);
-      for (int b = 0; b < bits; ++b) {
-        const bool bit = (d >> b) & 1;
-        const uint64_t with = __ballot(bit);
-        peers &= bit ? with : ~with;
-      }
-      const uint32_t below = __popcll(peers & ((uint64_t{1} << lane) - 1));
-      rank[s] = 0;
-      if (on) {
-        const uint32_t seen = mine[d];
-        rank[s] = seen + below;
-        if (below == 0) mine[d] = static_cast<uint16_t>(seen + __popcll(peers));
-      }
-      __builtin_amdgcn_wave_barrier();
+  for (int s = 0; s < kSteps; ++s) {
+    const bool on = i0 + s * 64 < n;
+    const uint32_t d = (key[s] >> shift) & (D - 1);
+    const uint64_t peers = equal_lanes(on, d, bits);
+    const uint32_t below = lanes_below(peers);
+    rank[s] = 0;
+    if (on) {
+      const uint32_t seen = mine[d];
+      rank[s] = seen + below;
+      if (below == 0) mine[d] = static_cast<uint16_t>(seen + __popcll(peers));
     }
-    __syncthreads();
-    // per digit: exclusive sums over the waves, then over the digits
-    uint32_t total = 0, prior = 0;
-    const int d0 = threadIdx.x;
-    if (d0 < D) {
-      for (int w = 0; w < 16; ++w) {
-        const uint32_t c = count[w * D + d0];
-        count[w * D + d0] = static_cast<uint16_t>(total);
-        total += c;
-      }
-      if (!Single) {
-        total = 0;
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  // per digit: exclusive sums over the waves, then over the digits and the workgroups before
+  uint32_t total = 0, prior = 0;
+  const int d0 = threadIdx.x;
+  if (d0 < D) {
+    for (int w = 0; w < 16; ++w) {
+      const uint32_t c = count[w * D + d0];
+      count[w * D + d0] = static_cast<uint16_t>(total);
+      total += c;
+    }
+    total = 0;
 #pragma unroll 8
-        for (int64_t b = 0; b < blocks; ++b) {
-          const uint32_t c = hist[b * D + d0];
-          total += c;
-          if (b < static_cast<int64_t>(blockIdx.x)) prior += c;
-        }
-      }
-    }
-    const uint32_t before = scan1024(total, wave_sum);
-    if (d0 < D) base[d0] = before + prior;
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      if (s < steps && b0 + p0 + s * 64 < n) {
-        const uint32_t d = (key[s] >> shift) & (D - 1);
-        const uint32_t to = base[d] + count[wave * D + d] + rank[s];
-        if constexpr (Single) {
-          lkey[to] = key[s];
-          lpos[to] = static_cast<uint16_t>(pos[s]);
-        } else {
-          keys_out[to] = key[s];
-          pos_out[to] = pos[s];
-        }
-      }
-    }
-    if constexpr (Single) {
-      __syncthreads();
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        if (s < steps && p0 + s * 64 < n) {
-          key[s] = lkey[p0 + s * 64];
-          pos[s] = lpos[p0 + s * 64];
-        }
-      }
-      __syncthreads();
+    for (int64_t b = 0; b < blocks; ++b) {
+      const uint32_t c = hist[b * D + d0];
+      total += c;
+      if (b < static_cast<int64_t>(blockIdx.x)) prior += c;
     }
   }
-  if constexpr (Single) {
+  const uint32_t before = scan1024(total, wave_sum);
+  if (d0 < D) base[d0] = before + prior;
+  __syncthreads();
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      if (s < steps && p0 + s * 64 < n) {
-        keys_out[p0 + s * 64] = key[s];
-        pos_out[p0 + s * 64] = pos[s];
-      }
+  for (int s = 0; s < kSteps; ++s) {
+    if (i0 + s * 64 < n) {
+      const uint32_t d = (key[s] >> shift) & (D - 1);
+      const uint32_t to = base[d] + count[wave * D + d] + rank[s];
+      keys_out[to] = key[s];
+      pos_out[to] = pos[s];
     }
+  }
+}
+
+// The whole order in one launch.  Workgroup w reads all tokens, wave by wave
+// consecutive ones, keeps those of the rows r = w modulo kEmbGroups in LDS in
+// order, counts those of the groups before w, which is where its ranges
+// start, and sorts what it kept by r / kEmbGroups as above.  Every workgroup
+// reads the same tokens, at most 256 KB, from its L2.  16384 tokens into 32768
+// rows on one MI355X: @@ us; as two radix passes of two launches each 29 us.
+template <typename Index>
+__global__ void __launch_bounds__(1024)
+embedding_order_kernel(const Index* __restrict__ tokens, int64_t rows, int n, int per_group, int bits,
+                       uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out,
+                       uint32_t* __restrict__ rowptr) {
+  constexpr int kSteps = kEmbOrderTokens / 1024, kKeys = kEmbOrderRows / kEmbGroups;
+  __shared__ uint16_t list_key[kEmbOrderTokens];
+  __shared__ uint16_t list_pos[kEmbOrderTokens];
+  __shared__ uint16_t count[16 * kKeys];
+  __shared__ uint32_t wave_sum[16], wave_kept[16], wave_before[16];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const uint32_t group = blockIdx.x;
+  const int steps = (n + 1023) / 1024, i0 = wave * steps * 64 + lane;
+  uint32_t key[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int i = i0 + s * 64;
+    key[s] = s < steps && i < n ? token_key(tokens[i], rows) : static_cast<uint32_t>(rows);
+  }
+  uint32_t kept = 0, before = 0;
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    if (s >= steps) break;
+    const bool valid = key[s] < static_cast<uint32_t>(rows);
+    const uint32_t of = key[s] % kEmbGroups;
+    kept += __popcll(__ballot(valid && of == group));
+    before += __popcll(__ballot(valid && of < group));
+  }
+  if (lane == 0) wave_kept[wave] = kept, wave_before[wave] = before;
+  for (int d = threadIdx.x; d < 16 * per_group; d += 1024) count[d] = 0;
+  __syncthreads();
+  uint32_t at = 0, length = 0, first = 0;  // this wave's place in the list, the list's length, the group's first range
+#pragma unroll
+  for (int w = 0; w < 16; ++w) {
+    if (w < wave) at += wave_kept[w];
+    length += wave_kept[w];
+    first += wave_before[w];
+  }
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    if (s >= steps) break;
+    const bool mine = key[s] < static_cast<uint32_t>(rows) && key[s] % kEmbGroups == group;
+    const uint64_t all = __ballot(mine);
+    if (mine) {
+      const uint32_t to = at + lanes_below(all);
+      list_key[to] = static_cast<uint16_t>(key[s] / kEmbGroups);
+      list_pos[to] = static_cast<uint16_t>(i0 + s * 64);
+    }
+    at += __popcll(all);
+  }
+  __syncthreads();
+  // counts of each wave's share of the list, then its first place of each key
+  const int share = (length + 1023) / 1024 * 64;
+  volatile uint16_t* my = count + wave * per_group;
+  for (int s = 0; s < share; s += 64) {
+    const uint32_t i = wave * share + s + lane;
+    const bool on = i < length;
+    const uint32_t k = on ? list_key[i] : 0;
+    const uint64_t peers = equal_lanes(on, k, bits);
+    if (on && lanes_below(peers) == 0) my[k] = static_cast<uint16_t>(my[k] + __popcll(peers));
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  uint32_t total = 0;
+  const int k0 = threadIdx.x;
+  if (k0 < per_group)
+    for (int w = 0; w < 16; ++w) total += count[w * per_group + k0];
+  const uint32_t start = scan1024(total, wave_sum);
+  if (k0 < per_group) {
+    rowptr[group * per_group + k0] = first + start;
+    uint32_t place = start;
+    for (int w = 0; w < 16; ++w) {
+      const uint32_t c = count[w * per_group + k0];
+      count[w * per_group + k0] = static_cast<uint16_t>(place);
+      place += c;
+    }
+  }
+  __syncthreads();
+  for (int s = 0; s < share; s += 64) {
+    const uint32_t i = wave * share + s + lane;
+    const bool on = i < length;
+    const uint32_t k = on ? list_key[i] : 0;
+    const uint64_t peers = equal_lanes(on, k, bits);
+    const uint32_t below = lanes_below(peers);
+    if (on) {
+      const uint32_t seen = my[k], to = first + seen + below;
+      keys_out[to] = group * per_group + k;
+      pos_out[to] = list_pos[i];
+      if (below == 0) my[k] = static_cast<uint16_t>(seen + __popcll(peers));
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  if (group == kEmbGroups - 1) {
+    const uint32_t end = first + length;
+    if (threadIdx.x == 0) rowptr[kEmbGroups * per_group] = end;
+    for (uint32_t i = end + threadIdx.x; i < static_cast<uint32_t>(n); i += 1024)
+      keys_out[i] = kEmbGroups * static_cast<uint32_t>(per_group);  // tokens out of range
   }
 }
 
@@ -403,73 +486,111 @@ embedding_chunk_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t
   }
 }
 
-// One table row per workgroup (Whole) or per group of `lanes` lanes (at most
-// a wave): the positions before the row's first whole chunk, the chunks' sums,
-// the positions after the last, zero where the range is empty.  A lane holds
-// kCols chunks of columns, so a row of positions gives that many loads at
-// once; the positions themselves are read by the lanes side by side.
-template <typename T, bool Whole>
-__global__ void __launch_bounds__(256)
-embedding_rows_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t* __restrict__ pos,
-                      const uint32_t* __restrict__ rowptr, const float* __restrict__ partial, int64_t pstride,
-                      int64_t rows, int dim, float scale, int lanes, T* __restrict__ out) {
-  constexpr int V = Chunk<T>::kN, kCols = Whole ? 1 : 2;
-  __shared__ float acc_lds[Whole ? 256 * V : 1];
-  const int groups = 256 / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-  const int64_t r = Whole ? static_cast<int64_t>(blockIdx.x) : static_cast<int64_t>(blockIdx.x) * groups + group;
-  if (!Whole && r >= rows) return;
-  const int64_t s = rowptr[r], e = rowptr[r + 1];
-  int64_t c_lo = (s + kEmbChunk - 1) / kEmbChunk, c_hi = e / kEmbChunk;
-  const int head = static_cast<int>(c_lo < c_hi ? c_lo * kEmbChunk - s : e - s);  // loose positions from s
-  const int64_t nchunk = c_lo < c_hi ? c_hi - c_lo : 0;
-  const int64_t tail0 = c_lo < c_hi ? c_hi * kEmbChunk : e;                       // loose positions from tail0 to e
-  const int loose = head + static_cast<int>(e - tail0);                           // fewer than 2 kEmbChunk
-  const int first = Whole ? group : 0, step = Whole ? groups : 1;
-  const int wide = lanes < 64 ? lanes : 64;  // each wave of a group reads the positions for itself
-  for (int c0 = 0; c0 < dim; c0 += lanes * V * kCols) {
-    float acc[kCols][V] = {};
-    for (int i0 = 0; i0 < loose; i0 += wide) {
-      const int have = loose - i0 < wide ? loose - i0 : wide, i = i0 + lane % wide;
-      const int at = i < loose ? static_cast<int>(pos[i < head ? s + i : tail0 + (i - head)]) : 0;
+// Adds to acc the items first, first + step, ... of a range [s, e) of the sorted
+// list, for the columns c0 + (lane + u lanes) V: the positions before the first
+// whole chunk and after the last, then the chunks' sums.
+template <typename T, int kCols>
+__device__ __forceinline__ void sum_range(const T* __restrict__ g, int64_t g_stride, const uint32_t* __restrict__ pos,
+                                          const float* __restrict__ partial, int64_t pstride, int64_t s, int64_t e,
+                                          int dim, int c0, int lane, int lanes, int first, int step,
+                                          float (&acc)[kCols][Chunk<T>::kN]) {
+  constexpr int V = Chunk<T>::kN;
+  const int64_t c_lo = (s + kEmbChunk - 1) / kEmbChunk, c_hi = e / kEmbChunk;
+  const bool whole = c_lo < c_hi;
+  const int head = static_cast<int>(whole ? c_lo * kEmbChunk - s : e - s);
+  const int64_t tail = whole ? c_hi * kEmbChunk : e;
+  const int loose = head + static_cast<int>(e - tail);  // fewer than 2 kEmbChunk
 #pragma unroll 4
-      for (int j = first; j < have; j += step) {
-        const T* row = g + static_cast<int64_t>(__shfl(at, j, wide)) * g_stride;
+  for (int i = first; i < loose; i += step) {
+    const T* row = g + static_cast<int64_t>(pos[i < head ? s + i : tail + (i - head)]) * g_stride;
 #pragma unroll
-        for (int u = 0; u < kCols; ++u) {
-          float v[V];
-          load_chunk(row, c0 + (lane + u * lanes) * V, dim, v);
+    for (int u = 0; u < kCols; ++u) {
+      float v[V];
+      load_chunk(row, c0 + (lane + u * lanes) * V, dim, v);
 #pragma unroll
-          for (int t = 0; t < V; ++t) acc[u][t] += v[t];
-        }
-      }
+      for (int t = 0; t < V; ++t) acc[u][t] += v[t];
     }
+  }
+  if (!whole) return;
+#pragma unroll 4
+  for (int64_t i = c_lo + first; i < c_hi; i += step) {
 #pragma unroll
     for (int u = 0; u < kCols; ++u) {
       const int c = c0 + (lane + u * lanes) * V;
       if (c >= dim) continue;
-#pragma unroll 8
-      for (int64_t i = first; i < nchunk; i += step) {
-        const float* p = partial + (c_lo + i) * pstride + c;
+      const float* p = partial + i * pstride + c;
 #pragma unroll
-        for (int t = 0; t < V; ++t) acc[u][t] += p[t];
-      }
+      for (int t = 0; t < V; ++t) acc[u][t] += p[t];
     }
-    if constexpr (Whole) {
-#pragma unroll
-      for (int t = 0; t < V; ++t) acc_lds[t * 256 + threadIdx.x] = acc[0][t];
-      __syncthreads();
-      if (group == 0)
-        for (int q = 1; q < groups; ++q)
-#pragma unroll
-          for (int t = 0; t < V; ++t) acc[0][t] += acc_lds[t * 256 + q * lanes + lane];
-      __syncthreads();
-      if (group != 0) continue;
-    }
+  }
+}
+
+// A workgroup takes 256 / lanes table rows (`lanes` at most a wave).  A group
+// of lanes sums a short range alone, zeros for an empty one; a range of more
+// than kAlone items is shared out over all groups, whose sums are added in
+// order: the few frequent tokens would otherwise be the kernel's last groups.
+// Few: one row per workgroup, where a table's rows would not fill the chip.
+template <typename T, bool Few>
+__global__ void __launch_bounds__(256)
+embedding_rows_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t* __restrict__ pos,
+                      const uint32_t* __restrict__ rowptr, const float* __restrict__ partial, int64_t pstride,
+                      int64_t rows, int groups_of_rows, int64_t per_group, int dim, float scale, int lanes,
+                      T* __restrict__ out) {
+  constexpr int V = Chunk<T>::kN, kCols = 2, kAlone = Few ? -1 : 8;
+  __shared__ float acc_lds[256 * V * kCols];
+  __shared__ uint32_t range[2][32];
+  const int groups = 256 / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  const int here = Few ? 1 : groups;  // rows of this workgroup
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * here;
+  if (threadIdx.x < here) {
+    const int64_t r = r0 + threadIdx.x;
+    const int64_t at = r < rows ? r % groups_of_rows * per_group + r / groups_of_rows : 0;
+    range[0][threadIdx.x] = r < rows ? rowptr[at] : 0;
+    range[1][threadIdx.x] = r < rows ? rowptr[at + 1] : 0;
+  }
+  __syncthreads();
+  auto items = [](int64_t s, int64_t e) {  // loads of a lane that sums the range alone
+    const int64_t c_lo = (s + kEmbChunk - 1) / kEmbChunk, c_hi = e / kEmbChunk;
+    return c_lo < c_hi ? e - s - (c_hi - c_lo) * (kEmbChunk - 1) : e - s;
+  };
+  auto put = [&](int64_t r, int c0, float(&acc)[kCols][V]) {
 #pragma unroll
     for (int u = 0; u < kCols; ++u) {
 #pragma unroll
       for (int t = 0; t < V; ++t) acc[u][t] *= scale;
       store_chunk(out + r * dim, c0 + (lane + u * lanes) * V, dim, acc[u]);
+    }
+  };
+  if (!Few && r0 + group < rows) {
+    const int64_t s = range[0][group], e = range[1][group];
+    if (items(s, e) <= kAlone) {
+      for (int c0 = 0; c0 < dim; c0 += lanes * V * kCols) {
+        float acc[kCols][V] = {};
+        sum_range<T, kCols>(g, g_stride, pos, partial, pstride, s, e, dim, c0, lane, lanes, 0, 1, acc);
+        put(r0 + group, c0, acc);
+      }
+    }
+  }
+  for (int q = 0; q < here; ++q) {
+    const int64_t s = range[0][q], e = range[1][q];
+    if (items(s, e) <= kAlone) continue;  // the same for the whole workgroup
+    for (int c0 = 0; c0 < dim; c0 += lanes * V * kCols) {
+      float acc[kCols][V] = {};
+      sum_range<T, kCols>(g, g_stride, pos, partial, pstride, s, e, dim, c0, lane, lanes, group, groups, acc);
+#pragma unroll
+      for (int u = 0; u < kCols; ++u)
+#pragma unroll
+        for (int t = 0; t < V; ++t) acc_lds[(u * V + t) * 256 + threadIdx.x] = acc[u][t];
+      __syncthreads();
+      if (group == 0) {
+        for (int k = 1; k < groups; ++k)
+#pragma unroll
+          for (int u = 0; u < kCols; ++u)
+#pragma unroll
+            for (int t = 0; t < V; ++t) acc[u][t] += acc_lds[(u * V + t) * 256 + k * lanes + lane];
+        put(r0 + q, c0, acc);
+      }
+      __syncthreads();
     }
   }
 }
@@ -522,39 +643,36 @@ int embedding_bwd_launch(const EmbeddingArgs& a) {
   float* partial = reinterpret_cast<float*>(ws + p.partial);
   const Index* tokens = static_cast<const Index*>(a.tokens);
   int last = 0;
-  if (p.blocks == 1) {
-    hipLaunchKernelGGL((embedding_sort_kernel<Index, true, kEmbSortAlone / 1024>), dim3(1), dim3(1024), 0, st, tokens, nullptr, nullptr, a.rows, a.n, 0, p.passes,
-                       p.digit_bits, nullptr, int64_t{1}, key[0], pos[0]);
+  if (p.groups > 1) {
+    int bits = 0;
+    while ((1 << bits) < p.per_group) ++bits;
+    hipLaunchKernelGGL((embedding_order_kernel<Index>), dim3(kEmbGroups), dim3(1024), 0, st, tokens, a.rows,
+                       static_cast<int>(a.n), static_cast<int>(p.per_group), bits, key[0], pos[0], rowptr);
   } else {
-    for (int q = 0; q < p.passes; ++q) {
+    for (int q = 0; q < p.passes && p.blocks; ++q) {
       const uint32_t* kin = q ? key[last] : nullptr;
       const uint32_t* pin = q ? pos[last] : nullptr;
       const int to = q ? 1 - last : 0;
       hipLaunchKernelGGL((embedding_hist_kernel<Index>), dim3(static_cast<unsigned>(p.blocks)), dim3(1024), 0, st,
                          tokens, kin, a.rows, a.n, q * p.digit_bits, p.digit_bits, hist);
-      hipLaunchKernelGGL((embedding_sort_kernel<Index, false, kEmbSortBlock / 1024>), dim3(static_cast<unsigned>(p.blocks)), dim3(1024), 0,
-                         st, tokens, kin, pin, a.rows, a.n, q, p.passes, p.digit_bits, hist, p.blocks, key[to],
+      hipLaunchKernelGGL((embedding_sort_kernel<Index>), dim3(static_cast<unsigned>(p.blocks)), dim3(1024), 0, st,
+                         tokens, kin, pin, a.rows, a.n, q * p.digit_bits, p.digit_bits, hist, p.blocks, key[to],
                          pos[to]);
       last = to;
     }
   }
   const int lanes = row_lanes<T>(a.dim);
-  const int64_t range_blocks = (a.rows + 1 + 255) / 256;
-  hipLaunchKernelGGL((embedding_chunk_kernel<T>), dim3(static_cast<unsigned>(range_blocks + p.chunks)), dim3(256), 0,
-                     st, static_cast<const T*>(a.grad), a.grad_stride, key[last], pos[last], a.rows, a.dim, a.n,
-                     range_blocks, lanes, rowptr, partial, round_up(a.dim, 8));
-  // few rows: each is long, so a workgroup shares one; many: a group of at most a wave each
-  const int dim = static_cast<int>(a.dim);
-  if (a.rows < 2048) {
-    hipLaunchKernelGGL((embedding_rows_kernel<T, true>), dim3(static_cast<unsigned>(a.rows)), dim3(256), 0, st,
-                       static_cast<const T*>(a.grad), a.grad_stride, pos[last], rowptr, partial,
-                       round_up(a.dim, 8), a.rows, dim, a.scale, lanes, static_cast<T*>(a.out));
-  } else {
-    const int narrow = row_lanes<T>(a.dim, 64), each = 256 / narrow;
-    hipLaunchKernelGGL((embedding_rows_kernel<T, false>), dim3(static_cast<unsigned>((a.rows + each - 1) / each)),
-                       dim3(256), 0, st, static_cast<const T*>(a.grad), a.grad_stride, pos[last], rowptr, partial,
-                       round_up(a.dim, 8), a.rows, dim, a.scale, narrow, static_cast<T*>(a.out));
-  }
+  const int64_t range_blocks = p.groups > 1 ? 0 : (a.rows + 1 + 255) / 256;
+  if (range_blocks + p.chunks > 0)
+    hipLaunchKernelGGL((embedding_chunk_kernel<T>), dim3(static_cast<unsigned>(range_blocks + p.chunks)), dim3(256), 0,
+                       st, static_cast<const T*>(a.grad), a.grad_stride, key[last], pos[last], p.keys, a.dim, a.n,
+                       range_blocks, lanes, rowptr, partial, round_up(a.dim, 8));
+  const int narrow = row_lanes<T>(a.dim, 64), each = 256 / narrow;
+  const bool few = a.rows < 2048;
+  auto* sum = few ? embedding_rows_kernel<T, true> : embedding_rows_kernel<T, false>;
+  hipLaunchKernelGGL(sum, dim3(static_cast<unsigned>(few ? a.rows : (a.rows + each - 1) / each)), dim3(256), 0, st,
+                     static_cast<const T*>(a.grad), a.grad_stride, pos[last], rowptr, partial, round_up(a.dim, 8),
+                     a.rows, p.groups, p.per_group, static_cast<int>(a.dim), a.scale, narrow, static_cast<T*>(a.out));
   return static_cast<int>(hipGetLastError());
 }
 
