@@ -311,7 +311,7 @@ embedding_sort_kernel(const Index* __restrict__ tokens, const uint32_t* __restri
 // order, counts those of the groups before w, which is where its ranges
 // start, and sorts what it kept by r / kEmbGroups as above.  Every workgroup
 // reads the same tokens, at most 256 KB, from its L2.  16384 tokens into 32768
-// rows on one MI355X: @@ us; as two radix passes of two launches each 29 us.
+// rows on one MI355X: 16 us; as two radix passes of two launches each 29 us.
 template <typename Index>
 __global__ void __launch_bounds__(1024)
 embedding_order_kernel(const Index* __restrict__ tokens, int64_t rows, int n, int per_group, int bits,
@@ -525,11 +525,16 @@ __device__ __forceinline__ void sum_range(const T* __restrict__ g, int64_t g_str
   }
 }
 
-// A workgroup takes 256 / lanes table rows (`lanes` at most a wave).  A group
-// of lanes sums a short range alone, zeros for an empty one; a range of more
-// than kAlone items is shared out over all groups, whose sums are added in
-// order: the few frequent tokens would otherwise be the kernel's last groups.
-// Few: one row per workgroup, where a table's rows would not fill the chip.
+// A workgroup takes 1024 / lanes table rows (`lanes` at most a wave), every
+// gridDim.x-th: frequent tokens are often neighbours.  It
+// writes zeros for its empty ranges, all threads together: most rows of a large
+// table have no token, and the dependent loads of the others' sums take longer
+// than all the zeros.  Then a group of lanes sums a short range alone; a range
+// of more than kAlone items is shared out over all groups, whose sums are
+// added in order: the few frequent tokens would otherwise be the kernel's last
+// groups.  Few: one row per workgroup, where a table's rows would not fill
+// the chip.  32768 x 1024 bf16, 16384 tokens: 24 us, 4.2 TB/s (one row per
+// 64 lanes, empty or not: 41 us).
 template <typename T, bool Few>
 __global__ void __launch_bounds__(256)
 embedding_rows_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t* __restrict__ pos,
@@ -538,12 +543,12 @@ embedding_rows_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t*
                       T* __restrict__ out) {
   constexpr int V = Chunk<T>::kN, kCols = 2, kAlone = Few ? -1 : 8;
   __shared__ float acc_lds[256 * V * kCols];
-  __shared__ uint32_t range[2][32];
+  __shared__ uint32_t range[2][128];
   const int groups = 256 / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-  const int here = Few ? 1 : groups;  // rows of this workgroup
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * here;
+  const int here = Few ? 1 : 4 * groups;  // rows of this workgroup
+  auto row_of = [](int q) { return blockIdx.x + static_cast<int64_t>(q) * gridDim.x; };
   if (threadIdx.x < here) {
-    const int64_t r = r0 + threadIdx.x;
+    const int64_t r = row_of(threadIdx.x);
     const int64_t at = r < rows ? r % groups_of_rows * per_group + r / groups_of_rows : 0;
     range[0][threadIdx.x] = r < rows ? rowptr[at] : 0;
     range[1][threadIdx.x] = r < rows ? rowptr[at + 1] : 0;
@@ -561,13 +566,21 @@ embedding_rows_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t*
       store_chunk(out + r * dim, c0 + (lane + u * lanes) * V, dim, acc[u]);
     }
   };
-  if (!Few && r0 + group < rows) {
-    const int64_t s = range[0][group], e = range[1][group];
-    if (items(s, e) <= kAlone) {
+  if constexpr (!Few) {
+    const int chunks = (dim + V - 1) / V;
+    for (int i = threadIdx.x; i < here * chunks; i += 256) {
+      const int q = i / chunks;
+      constexpr float zero[V] = {};
+      if (row_of(q) < rows && range[0][q] == range[1][q])
+        store_chunk(out + row_of(q) * dim, i % chunks * V, dim, zero);
+    }
+    for (int q = group; q < here; q += groups) {
+      const int64_t s = range[0][q], e = range[1][q];
+      if (s == e || items(s, e) > kAlone) continue;
       for (int c0 = 0; c0 < dim; c0 += lanes * V * kCols) {
         float acc[kCols][V] = {};
         sum_range<T, kCols>(g, g_stride, pos, partial, pstride, s, e, dim, c0, lane, lanes, 0, 1, acc);
-        put(r0 + group, c0, acc);
+        put(row_of(q), c0, acc);
       }
     }
   }
@@ -588,7 +601,7 @@ embedding_rows_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t*
           for (int u = 0; u < kCols; ++u)
 #pragma unroll
             for (int t = 0; t < V; ++t) acc[u][t] += acc_lds[(u * V + t) * 256 + k * lanes + lane];
-        put(r0 + q, c0, acc);
+        put(row_of(q), c0, acc);
       }
       __syncthreads();
     }
@@ -667,7 +680,7 @@ int embedding_bwd_launch(const EmbeddingArgs& a) {
     hipLaunchKernelGGL((embedding_chunk_kernel<T>), dim3(static_cast<unsigned>(range_blocks + p.chunks)), dim3(256), 0,
                        st, static_cast<const T*>(a.grad), a.grad_stride, key[last], pos[last], p.keys, a.dim, a.n,
                        range_blocks, lanes, rowptr, partial, round_up(a.dim, 8));
-  const int narrow = row_lanes<T>(a.dim, 64), each = 256 / narrow;
+  const int narrow = row_lanes<T>(a.dim, 64), each = 1024 / narrow;
   const bool few = a.rows < 2048;
   auto* sum = few ? embedding_rows_kernel<T, true> : embedding_rows_kernel<T, false>;
   hipLaunchKernelGGL(sum, dim3(static_cast<unsigned>(few ? a.rows : (a.rows + each - 1) / each)), dim3(256), 0, st,
