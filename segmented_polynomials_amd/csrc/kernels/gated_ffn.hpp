@@ -124,7 +124,7 @@ int gemm_launch(GemmArgs& g, hipStream_t st) {
   if constexpr (Dt::kPlanes == 1) {
     constexpr bool kTwoAcross = AAcross && BAcross, kBwd = Epi == kEpiGatedBwd;
     const double large = kTwoAcross || kBwd ? cost(256, 128, kBwd ? 1 : 2, 1.0) : cost(256, 256, 1, 1.0);
-    const double c128 = cost(128, 128, 2, 0.8), c64 = cost(64, 64, 2, 0.45);
+    const double c128 = cost(128, 128, 2, 0.8), c64 = cost(64, 64, 3, 0.45);
     if (large <= c128 && large <= c64) {
       if constexpr (kTwoAcross)
         return gemm_launch_tile<Dt, 256, 128, 2, 2, 32, 3, AAcross, BAcross, Epi>(g, st);
@@ -134,7 +134,7 @@ int gemm_launch(GemmArgs& g, hipStream_t st) {
         return gemm_launch_tile<Dt, 256, 256, 2, 4, 64, 2, AAcross, BAcross, Epi>(g, st);
     }
     if (c128 <= c64) return gemm_launch_tile<Dt, 128, 128, 2, 2, 64, 2, AAcross, BAcross, Epi>(g, st);
-    return gemm_launch_tile<Dt, 64, 64, 2, 2, 64, 4, AAcross, BAcross, Epi>(g, st);
+    return gemm_launch_tile<Dt, 64, 64, 2, 2, 64, 3, AAcross, BAcross, Epi>(g, st);
   } else {
     // 20000 rows of 128 x 512: paired 52 us with 128 x 128 tiles, 48 us with 64 x 64, three workgroups a unit
     if (cost(128, 128, 1, 0.9) <= cost(64, 64, 3, 0.9))
