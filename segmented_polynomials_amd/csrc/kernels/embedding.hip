@@ -544,20 +544,26 @@ embedding_rows_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t*
   constexpr int V = Chunk<T>::kN, kCols = 2, kAlone = Few ? -1 : 8;
   __shared__ float acc_lds[256 * V * kCols];
   __shared__ uint32_t range[2][128];
+  __shared__ int long_rows[128], long_count;
   const int groups = 256 / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
   const int here = Few ? 1 : 4 * groups;  // rows of this workgroup
   auto row_of = [](int q) { return blockIdx.x + static_cast<int64_t>(q) * gridDim.x; };
-  if (threadIdx.x < here) {
-    const int64_t r = row_of(threadIdx.x);
-    const int64_t at = r < rows ? r % groups_of_rows * per_group + r / groups_of_rows : 0;
-    range[0][threadIdx.x] = r < rows ? rowptr[at] : 0;
-    range[1][threadIdx.x] = r < rows ? rowptr[at + 1] : 0;
-  }
-  __syncthreads();
   auto items = [](int64_t s, int64_t e) {  // loads of a lane that sums the range alone
     const int64_t c_lo = (s + kEmbChunk - 1) / kEmbChunk, c_hi = e / kEmbChunk;
     return c_lo < c_hi ? e - s - (c_hi - c_lo) * (kEmbChunk - 1) : e - s;
   };
+  if (threadIdx.x == 0) long_count = 0;
+  __syncthreads();
+  if (threadIdx.x < here) {
+    const int64_t r = row_of(threadIdx.x);
+    const int64_t at = r < rows ? r % groups_of_rows * per_group + r / groups_of_rows : 0;
+    const uint32_t s = r < rows ? rowptr[at] : 0, e = r < rows ? rowptr[at + 1] : 0;
+    range[0][threadIdx.x] = s;
+    range[1][threadIdx.x] = e;
+    // the order of the list does not matter: its rows are independent
+    if (r < rows && items(s, e) > kAlone) long_rows[atomicAdd(&long_count, 1)] = threadIdx.x;
+  }
+  __syncthreads();
   auto put = [&](int64_t r, int c0, float(&acc)[kCols][V]) {
 #pragma unroll
     for (int u = 0; u < kCols; ++u) {
@@ -584,9 +590,9 @@ embedding_rows_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t*
       }
     }
   }
-  for (int q = 0; q < here; ++q) {
+  for (int k = 0; k < long_count; ++k) {
+    const int q = long_rows[k];
     const int64_t s = range[0][q], e = range[1][q];
-    if (items(s, e) <= kAlone) continue;  // the same for the whole workgroup
     for (int c0 = 0; c0 < dim; c0 += lanes * V * kCols) {
       float acc[kCols][V] = {};
       sum_range<T, kCols>(g, g_stride, pos, partial, pstride, s, e, dim, c0, lane, lanes, group, groups, acc);
@@ -596,11 +602,11 @@ embedding_rows_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t*
         for (int t = 0; t < V; ++t) acc_lds[(u * V + t) * 256 + threadIdx.x] = acc[u][t];
       __syncthreads();
       if (group == 0) {
-        for (int k = 1; k < groups; ++k)
+        for (int o = 1; o < groups; ++o)
 #pragma unroll
           for (int u = 0; u < kCols; ++u)
 #pragma unroll
-            for (int t = 0; t < V; ++t) acc[u][t] += acc_lds[(u * V + t) * 256 + k * lanes + lane];
+            for (int t = 0; t < V; ++t) acc[u][t] += acc_lds[(u * V + t) * 256 + o * lanes + lane];
         put(row_of(q), c0, acc);
       }
       __syncthreads();

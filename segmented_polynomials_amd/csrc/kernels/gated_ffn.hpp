@@ -97,8 +97,64 @@ int gemm_launch_tile(GemmArgs& g, hipStream_t st) {
     tiles += g.tiles_m[z] * g.tiles_n[z];
   }
   if (tiles == 0) return 0;  // no rows
+  if (g.splits < 1) g.splits = 1;
   hipLaunchKernelGGL((gemm_tile_kernel<Dt, BM, BN, WM, WN, KS, S, AAcross, BAcross, Epi>),
-                     dim3(static_cast<unsigned>(tiles)), dim3(WM * WN * 64), 0, st, g);
+                     dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(g.splits)), dim3(WM * WN * 64), 0, st, g);
+  return static_cast<int>(hipGetLastError());
+}
+
+// Shares of the sum over k of a product with few tiles.  A card holds 768
+// workgroups of the 64 x 64 tile; a product that fills less than half of them
+// and has a long sum gives each tile several, of at least sixteen steps, whose
+// float32 sums a second kernel adds.  One MI355X, 63 rows of 1352 x 5603 x 272
+// float32, backward: 158 us, 385 us without; shares of eight steps cost 1357
+// rows of 322 x 853 x 257 f16, whose sums have 22 to 28, 6 us of 44.
+struct Split {
+  int splits = 1;
+  int64_t elements = 0;  // of one share
+};
+template <typename Dt>
+Split plan_split(const GemmArgs& g) {
+  constexpr int64_t kStep = Dt::kPlanes == 1 ? 64 : 32;
+  Split p;
+  int64_t tiles = 0;
+  for (int z = 0; z < g.batch; ++z) {
+    tiles += round_up(g.m[z], 64) / 64 * (round_up(g.n[z], 64) / 64);
+    p.elements += g.m[z] * round_up(g.n[z], 4);
+  }
+  const int64_t steps = (g.k + kStep - 1) / kStep * g.phases;
+  if (tiles > 0 && tiles < 384)
+    p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(768 / tiles, steps / 16)));
+  return p;
+}
+
+template <typename Dt, bool AAcross, bool BAcross, int Epi>
+int gemm_launch(GemmArgs& g, hipStream_t st);
+
+// A product with a plain epilogue, split if that pays; `sums` is the space that
+// split_bytes reserved for it.
+template <typename Dt, bool AAcross, bool BAcross, int Epi>
+int gemm_launch_split(GemmArgs& g, float* sums, hipStream_t st) {
+  using T = std::conditional_t<Epi == kEpiStoreF32, float, typename Dt::T>;
+  const Split p = plan_split<Dt>(g);
+  if (p.splits == 1) return gemm_launch<Dt, AAcross, BAcross, Epi>(g, st);
+  SplitSumArgs q{};
+  int64_t at = 0, most = 0;
+  for (int z = 0; z < g.batch; ++z) {
+    q.m[z] = g.m[z], q.n[z] = g.n[z], q.ld[z] = round_up(g.n[z], 4), q.ldc[z] = g.ldc[z], q.to[z] = g.c[z];
+    q.from[z] = sums + at;
+    g.c[z] = sums + at, g.ldc[z] = q.ld[z];
+    at += q.m[z] * q.ld[z];
+    most = std::max(most, q.m[z] * q.ld[z] / 4);
+  }
+  q.split_stride = g.split_stride = p.elements;
+  q.splits = g.splits = p.splits;
+  q.batch = g.batch;
+  constexpr int kK = Dt::kPlanes == 1 ? 64 : 32, kS = Dt::kPlanes == 1 ? 3 : 2;
+  const int rc = gemm_launch_tile<Dt, 64, 64, 2, 2, kK, kS, AAcross, BAcross, kEpiStoreF32>(g, st);
+  if (rc || most == 0) return rc;
+  hipLaunchKernelGGL(split_sum_kernel<T>, dim3(static_cast<unsigned>(std::min<int64_t>((most + 255) / 256, 2048)), q.batch),
+                     dim3(256), 0, st, q);
   return static_cast<int>(hipGetLastError());
 }
 
@@ -200,9 +256,40 @@ struct FfnPlan {
   }
 };
 
+// the sums' space of the largest of a call's split products
+template <typename Dt>
+struct SplitSpace {
+  int64_t most = 0;
+  void add(const GemmArgs& g) {
+    const Split p = plan_split<Dt>(g);
+    if (p.splits > 1) most = std::max(most, p.splits * p.elements);
+  }
+};
+
+template <typename Dt>
+GemmArgs product(int64_t m, int64_t n, int64_t k, const Operand& a, const Operand& b, void* c, int64_t ldc) {
+  GemmArgs g{};
+  add_phase<Dt>(g, g.phases, a, b);
+  g.batch = 1, g.m[0] = m, g.n[0] = n, g.k = k, g.lda[0] = a.ld, g.ldb[0] = b.ld, g.c[0] = c, g.ldc[0] = ldc;
+  return g;
+}
+
+// x Wg^T and x Wu^T; the caller adds what the epilogue writes
+template <typename Dt>
+GemmArgs paired_product(const GatedFfnArgs& a, const Operand& x, const Operand& wg, const Operand& wu,
+                        const Operand& h) {
+  GemmArgs g{};
+  // the two weights share a row stride: packing decides for both alike but for their alignment
+  add_phase<Dt>(g, g.phases, x, wg, &wu);
+  g.batch = 1, g.m[0] = a.n, g.n[0] = a.hidden, g.k = a.d_in, g.lda[0] = x.ld, g.ldb[0] = wg.ld;
+  g.h = const_cast<uint16_t*>(h.plane[0]), g.ldh = h.ld, g.plane_stride = a.n * h.ld, g.act = a.act;
+  return g;
+}
+
 template <typename Dt>
 int ffn_fwd(const GatedFfnArgs& a, size_t* bytes) {
   const bool worst = bytes != nullptr;
+  const hipStream_t st = static_cast<hipStream_t>(a.stream);
   if (a.n <= kFewRows) {
     Arena arena{static_cast<char*>(a.workspace)};
     const int64_t ldh = round_up(a.hidden, 8);
@@ -211,7 +298,6 @@ int ffn_fwd(const GatedFfnArgs& a, size_t* bytes) {
       *bytes = arena.at;
       return 0;
     }
-    const hipStream_t st = static_cast<hipStream_t>(a.stream);
     const int rc = gemm_rows<Dt, true>({a.x, a.w_gate, a.w_up, h, a.n, a.hidden, a.d_in, a.x_stride, ldh, a.act}, st);
     return rc ? rc : gemm_rows<Dt, false>({h, a.w_down, nullptr, a.out, a.n, a.d_out, a.hidden, ldh, a.out_stride, 0}, st);
   }
@@ -221,30 +307,25 @@ int ffn_fwd(const GatedFfnArgs& a, size_t* bytes) {
   const Operand wu = plan.use(a.w_up, a.hidden, a.d_in, a.d_in, worst);
   const Operand wd = plan.use(a.w_down, a.d_out, a.hidden, a.hidden, worst);
   const Operand h = plan.hidden(a.n, a.hidden);
+  GemmArgs g = paired_product<Dt>(a, x, wg, wu, h);
+  GemmArgs d = product<Dt>(a.n, a.d_out, a.hidden, h, wd, a.out, a.out_stride);
+  SplitSpace<Dt> space;
+  space.add(d);
+  float* sums = plan.arena.template take<float>(space.most);
   if (worst) {
     *bytes = plan.arena.at;
     return 0;
   }
-  const hipStream_t st = static_cast<hipStream_t>(a.stream);
   int rc = plan.run_pack(st);
-  if (rc) return rc;
-  // the two weights of the paired product share a row stride: pack decides for both alike but for their alignment
-  GemmArgs g{};
-  add_phase<Dt>(g, g.phases, x, wg, &wu);
-  g.batch = 1, g.m[0] = a.n, g.n[0] = a.hidden, g.k = a.d_in, g.lda[0] = x.ld, g.ldb[0] = wg.ld;
-  g.h = const_cast<uint16_t*>(h.plane[0]), g.ldh = h.ld, g.plane_stride = a.n * h.ld, g.act = a.act;
-  rc = gemm_launch<Dt, false, false, kEpiGated>(g, st);
-  if (rc) return rc;
-  GemmArgs d{};
-  add_phase<Dt>(d, d.phases, h, wd);
-  d.batch = 1, d.m[0] = a.n, d.n[0] = a.d_out, d.k = a.hidden, d.lda[0] = h.ld, d.ldb[0] = wd.ld, d.c[0] = a.out;
-  d.ldc[0] = a.out_stride;
-  return gemm_launch<Dt, false, false, kEpiStore>(d, st);
+  if (!rc) rc = gemm_launch<Dt, false, false, kEpiGated>(g, st);
+  if (!rc) rc = gemm_launch_split<Dt, false, false, kEpiStore>(d, sums, st);
+  return rc;
 }
 
 template <typename Dt>
 int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
   const bool worst = bytes != nullptr;
+  const hipStream_t st = static_cast<hipStream_t>(a.stream);
   FfnPlan<Dt> plan(a.workspace);
   const Operand x = plan.use(a.x, a.n, a.d_in, a.x_stride, worst);
   const Operand wg = plan.use(a.w_gate, a.hidden, a.d_in, a.d_in, worst);
@@ -253,61 +334,45 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
   const Operand go = plan.use(a.gout, a.n, a.d_out, a.gout_stride, worst);
   const Operand h = plan.hidden(a.n, a.hidden), dg = plan.hidden(a.n, a.hidden), du = plan.hidden(a.n, a.hidden);
   float* dh = plan.arena.template take<float>(a.n * h.ld);
+  GemmArgs first = product<Dt>(a.n, a.hidden, a.d_out, go, wd, dh, h.ld);
+  GemmArgs pair = paired_product<Dt>(a, x, wg, wu, h);
+  pair.dg = const_cast<uint16_t*>(dg.plane[0]), pair.du = const_cast<uint16_t*>(du.plane[0]), pair.dh = dh;
+  GemmArgs dx = product<Dt>(a.n, a.d_in, a.hidden, dg, wg, a.gx, a.d_in);
+  add_phase<Dt>(dx, dx.phases, du, wu);
+  GemmArgs dw = product<Dt>(a.hidden, a.d_in, a.n, dg, x, a.gw_gate, a.d_in);
+  GemmArgs down = product<Dt>(a.d_out, a.hidden, a.n, go, h, a.gw_down, a.hidden);
+  int at = 1;
+  add_phase<Dt>(dw, at, du, x);
+  dw.batch = 2;
+  dw.m[1] = dw.m[0], dw.n[1] = dw.n[0], dw.lda[1] = dw.lda[0], dw.ldb[1] = dw.ldb[0], dw.ldc[1] = dw.ldc[0];
+  dw.c[1] = a.gw_up;
+  // Products that do not fill the card share a launch (1357 rows of 322 x 853 x 257: 10 + 9 us apart);
+  // large ones are chosen tiles for each (8192 x 2048 x 5632: 329 + 192 us apart, 578 us together).
+  const int64_t tiles = round_up(a.hidden, 64) / 64 * (round_up(a.d_in, 64) / 64 * 2 + round_up(a.d_out, 64) / 64);
+  const bool apart = tiles > 1024;
+  if (!apart) {
+    add_phase<Dt>(dw, at, go, h);
+    dw.batch = 3;
+    dw.m[2] = down.m[0], dw.n[2] = down.n[0], dw.lda[2] = down.lda[0], dw.ldb[2] = down.ldb[0];
+    dw.ldc[2] = down.ldc[0], dw.c[2] = down.c[0];
+  }
+  SplitSpace<Dt> space;  // sized for every gradient, asked for or not
+  space.add(first);
+  space.add(dx);
+  space.add(dw);
+  if (apart) space.add(down);
+  float* sums = plan.arena.template take<float>(space.most);
   if (worst) {
     *bytes = plan.arena.at;
     return 0;
   }
-  const hipStream_t st = static_cast<hipStream_t>(a.stream);
   int rc = plan.run_pack(st);
-  if (rc) return rc;
-  GemmArgs g{};
-  add_phase<Dt>(g, g.phases, go, wd);
-  g.batch = 1, g.m[0] = a.n, g.n[0] = a.hidden, g.k = a.d_out, g.lda[0] = go.ld, g.ldb[0] = wd.ld, g.c[0] = dh;
-  g.ldc[0] = h.ld;
-  rc = gemm_launch<Dt, false, true, kEpiStoreF32>(g, st);
-  if (rc) return rc;
-  g = GemmArgs{};
-  add_phase<Dt>(g, g.phases, x, wg, &wu);
-  g.batch = 1, g.m[0] = a.n, g.n[0] = a.hidden, g.k = a.d_in, g.lda[0] = x.ld, g.ldb[0] = wg.ld;
-  g.h = const_cast<uint16_t*>(h.plane[0]), g.dg = const_cast<uint16_t*>(dg.plane[0]);
-  g.du = const_cast<uint16_t*>(du.plane[0]), g.dh = dh;
-  g.ldh = h.ld, g.plane_stride = a.n * h.ld, g.act = a.act;
-  rc = gemm_launch<Dt, false, false, kEpiGatedBwd>(g, st);
-  if (rc) return rc;
-  if (a.gx) {
-    g = GemmArgs{};
-    add_phase<Dt>(g, g.phases, dg, wg);
-    add_phase<Dt>(g, g.phases, du, wu);
-    g.batch = 1, g.m[0] = a.n, g.n[0] = a.d_in, g.k = a.hidden, g.lda[0] = dg.ld, g.ldb[0] = wg.ld, g.c[0] = a.gx;
-    g.ldc[0] = a.d_in;
-    rc = gemm_launch<Dt, false, true, kEpiStore>(g, st);
-    if (rc) return rc;
-  }
-  if (a.gw_gate) {
-    g = GemmArgs{};
-    int at = 0;
-    add_phase<Dt>(g, at, dg, x);
-    g.phases = at;
-    add_phase<Dt>(g, at, du, x);
-    add_phase<Dt>(g, at, go, h);
-    g.batch = 3, g.k = a.n;
-    for (int z = 0; z < 2; ++z)
-      g.m[z] = a.hidden, g.n[z] = a.d_in, g.lda[z] = dg.ld, g.ldb[z] = x.ld, g.ldc[z] = a.d_in;
-    g.m[2] = a.d_out, g.n[2] = a.hidden, g.lda[2] = go.ld, g.ldb[2] = h.ld, g.ldc[2] = a.hidden;
-    g.c[0] = a.gw_gate, g.c[1] = a.gw_up, g.c[2] = a.gw_down;
-    // Products that do not fill the card share a launch (1357 rows of 322 x 853 x 257: 10 + 9 us apart);
-    // large ones are chosen tiles for each (8192 x 2048 x 5632: 329 + 192 us apart, 578 us together).
-    const int64_t tiles = round_up(a.hidden, 64) / 64 * (round_up(a.d_in, 64) / 64 * 2 + round_up(a.d_out, 64) / 64);
-    if (tiles > 1024) {
-      GemmArgs d{};
-      add_phase<Dt>(d, d.phases, go, h);
-      d.batch = 1, d.k = a.n, d.m[0] = g.m[2], d.n[0] = g.n[2], d.lda[0] = go.ld, d.ldb[0] = h.ld;
-      d.c[0] = a.gw_down, d.ldc[0] = a.hidden;
-      rc = gemm_launch<Dt, true, true, kEpiStore>(d, st);
-      if (rc) return rc;
-      g.batch = 2;
-    }
-    rc = gemm_launch<Dt, true, true, kEpiStore>(g, st);
+  if (!rc) rc = gemm_launch_split<Dt, false, true, kEpiStoreF32>(first, sums, st);
+  if (!rc) rc = gemm_launch<Dt, false, false, kEpiGatedBwd>(pair, st);
+  if (!rc && a.gx) rc = gemm_launch_split<Dt, false, true, kEpiStore>(dx, sums, st);
+  if (!rc && a.gw_gate) {
+    rc = gemm_launch_split<Dt, true, true, kEpiStore>(dw, sums, st);
+    if (!rc && apart) rc = gemm_launch_split<Dt, true, true, kEpiStore>(down, sums, st);
   }
   return rc;
 }

@@ -86,7 +86,7 @@ gemm_rows_kernel(RowsArgs g) {
   for (int j = 0; j < W; ++j)
 #pragma unroll
     for (int i = 0; i < M16; ++i) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
+#pragma unroll(P == 1 && M16 == 1 ? 4 : 2)
   for (int k0 = wave * 64; k0 < k; k0 += waves * 64) {
     RowChunk<Dt> rw[2][W], rx[2][M16];
 #pragma unroll

@@ -46,6 +46,10 @@ struct GemmArgs {
   int64_t m[kMaxBatch], n[kMaxBatch], lda[kMaxBatch], ldb[kMaxBatch], ldc[kMaxBatch];
   void* c[kMaxBatch];
   int64_t tiles_m[kMaxBatch], tiles_n[kMaxBatch];
+  // workgroups (x, y) take the y-th share of the steps of a tile and store their
+  // float32 sums split_stride elements apart
+  int splits;
+  int64_t split_stride;
   // epilogue of paired products
   uint16_t *h, *dg, *du;  // planes of [m][ldh], plane_stride apart
   const float* dh;        // [m][ldh]
@@ -277,6 +281,12 @@ gemm_tile_kernel(GemmArgs g) {
   const int step_a = static_cast<int>(AAcross ? KS * lda * 2 : KS * 2);  // bytes
   const int step_b = static_cast<int>(BAcross ? KS * ldb * 2 : KS * 2);
 
+  // this workgroup's share of the steps of all phases
+  const int64_t steps = (g.k + KS - 1) / KS;
+  const int64_t s0 = kPair ? 0 : steps * g.phases * blockIdx.y / g.splits;
+  int left = static_cast<int>((kPair ? steps : steps * g.phases * (blockIdx.y + 1) / g.splits) - s0);
+  int to_load = left;  // none: a gradient over no rows is zero
+
   // the next step to load: its k left, its corners and the bytes from there to the operands' ends
   int phase = 0, k_left = 0;
   int64_t left_a = 0, left_b = 0;
@@ -293,8 +303,22 @@ gemm_tile_kernel(GemmArgs g) {
     left_a = left_a0;
     left_b = left_b0;
   };
-  matrices();
-  if (g.k == 0) left_a = left_b = 0;
+  if (left > 0) {
+    phase = static_cast<int>(s0 / steps);
+    matrices();
+    const int64_t skip = s0 % steps;
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      pa[q] += skip * step_a;
+      pb[q] += skip * step_b;
+    }
+    left_a -= skip * step_a;
+    left_b -= skip * step_b;
+    k_left -= static_cast<int>(skip * KS);
+  } else {
+    matrices();
+    left_a = left_b = 0;
+  }
   // Loads are issued for exactly S - 1 steps past the last one too (of nothing:
   // the range is empty), so that the count of those outstanding is the same in
   // every step, for the wait below and for the compiler's own.
@@ -323,11 +347,11 @@ gemm_tile_kernel(GemmArgs g) {
     left_a -= step_a;
     left_b -= step_b;
     k_left -= KS;
-    if (k_left <= 0) {
-      if (++phase < g.phases)
-        matrices();
-      else
-        left_a = left_b = 0;
+    if (--to_load <= 0) {
+      left_a = left_b = 0;
+    } else if (k_left <= 0) {
+      ++phase;
+      matrices();
     }
   };
 
@@ -391,7 +415,6 @@ gemm_tile_kernel(GemmArgs g) {
   if constexpr (S > 3) issue(a2, b2);
   // whole turns of the buffers, then what is left: a loop with exits between
   // the steps would have the compiler wait for loads that are not due
-  int left = (static_cast<int>(g.k) + KS - 1) / KS * g.phases;  // none: a gradient over no rows is zero
   for (; left >= S; left -= S) {
     first();
     step(a1, b1, a0, b0);
@@ -414,7 +437,7 @@ gemm_tile_kernel(GemmArgs g) {
     for (int i = 0; i < FM; ++i) {
       const int64_t m = m0 + wm * (BM / WM) + i * 16 + lane % 16;
       if (m >= gm) continue;
-      T* row = static_cast<T*>(g.c[z]) + m * g.ldc[z];
+      T* row = static_cast<T*>(g.c[z]) + (Epi == kEpiStoreF32 ? g.split_stride * blockIdx.y : 0) + m * g.ldc[z];
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const int64_t n = n0 + wn * (BN / WN) + j * 16 + lane / 16 * 4;
@@ -528,6 +551,38 @@ gemm_tile_kernel(GemmArgs g) {
         store(g.dg + p * g.plane_stride, [&](int i, int j, int q) { return plane(acc[i][j][q], p); });
         store(g.du + p * g.plane_stride, [&](int i, int j, int q) { return plane(acc[i][j + FN / 2][q], p); });
       }
+    }
+  }
+}
+
+// The sum of the shares, in order, in the output's type: four columns a lane.
+struct SplitSumArgs {
+  const float* from[kMaxBatch];
+  void* to[kMaxBatch];
+  int64_t m[kMaxBatch], n[kMaxBatch], ld[kMaxBatch], ldc[kMaxBatch], split_stride;
+  int batch, splits;
+};
+template <typename T>
+__global__ void __launch_bounds__(256)
+split_sum_kernel(SplitSumArgs g) {
+  const int z = blockIdx.y;
+  const int64_t quads = g.ld[z] / 4, total = g.m[z] * quads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = i / quads;
+    const int c = static_cast<int>(i % quads * 4);
+    const float* from = g.from[z] + r * g.ld[z] + c;
+    v4f s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int k = 0; k < g.splits; ++k) s += *reinterpret_cast<const v4f*>(from + k * g.split_stride);
+    T* to = static_cast<T*>(g.to[z]) + r * g.ldc[z] + c;
+    const T v[4] = {static_cast<T>(s[0]), static_cast<T>(s[1]), static_cast<T>(s[2]), static_cast<T>(s[3])};
+    if (c + 4 <= g.n[z]) {
+      __builtin_memcpy(to, v, sizeof(v));
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c + q < g.n[z]) to[q] = v[q];
     }
   }
 }

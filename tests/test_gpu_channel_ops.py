@@ -514,3 +514,20 @@ def test_gated_ffn_few_rows(n, di, F, do, dtype):
     assert torch.equal(to[:, 4:4 + do], got) and bool((to[:, :4] == 5).all()) and bool((to[:, 4 + do:] == 5).all())
     one = sp.gated_ffn_fwd(x[:1].expand(n, di), wg, wu, wd, act="gelu")
     assert torch.equal(one, got[:1].expand(n, do))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,di,F,do", [(70, 200, 3001, 65), (66, 1030, 2052, 30), (5000, 65, 70, 33), (9, 64, 4000, 700),
+                                       (300, 20, 8000, 640)])
+def test_gated_ffn_long_sums(n, di, F, do, dtype):
+    """Products of few tiles whose long sums are shared out and added."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"gated ffn, long sums n={n} d_in={di} hidden={F} d_out={do} {dtype}")
+    x, wg, wu, wd, gy = ffn_case(n, di, F, do, dtype, n + F)
+    (out, eout), grads = ffn_reference(x, wg, wu, wd, gy, "silu", dtype)
+    check(sp.gated_ffn_fwd(x, wg, wu, wd), out, eout, dtype, "out")
+    got = sp.gated_ffn_bwd(x, wg, wu, wd, gy)
+    for name, a, (r, e) in zip(("grad_x", "grad_w_gate", "grad_w_up", "grad_w_down"), got, grads):
+        check(a, r, e, dtype, name)
+    assert all(torch.equal(p, q) for p, q in zip(got, sp.gated_ffn_bwd(x, wg, wu, wd, gy)))
