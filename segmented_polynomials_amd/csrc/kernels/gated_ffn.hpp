@@ -8,8 +8,8 @@
 //             dx = dg Wg + du Wu             one product of two phases
 //             dWg = dg^T x, dWu = du^T x, dWd = g^T h     one launch of the three
 // Between the products h, dg and du are held in the operands' type: they are
-// operands of matrix instructions, each rounding is at most a relative 2^-9
-// (bf16) or 2^-12 (f16) of one term of a long sum, the size of the inputs' own
+// operands of matrix instructions, each rounding is at most a relative 2^-8
+// (bf16) or 2^-11 (f16) of one term of a long sum, the size of the inputs' own
 // rounding.  float32 keeps them as three bf16 planes (24 bits).  dh is no
 // operand and stays float32: rounded as well, it would add half again to the
 // error of dx, dWg and dWu.

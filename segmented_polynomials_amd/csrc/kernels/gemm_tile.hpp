@@ -6,8 +6,8 @@
 // gradient product needs a transposed copy.  float32 operands come as three
 // bf16 planes x = x1 + x2 + x3 (each the bf16 rounding of what is left: 24
 // bits, the whole significand), and a product is the six plane pairs down to
-// 2^-16 of the first, the smallest first; what is left out is below 2^-24 of
-// it.  A step loads the three planes once for its six products.
+// 2^-16 of the first, the smallest first; what is left out is at most 2^-23
+// of it.  A step loads the three planes once for its six products.
 //
 // One workgroup computes a BM x BN tile in steps of KS k.  The operand tiles
 // go from global memory to LDS directly (16 bytes a lane) into S buffers in
