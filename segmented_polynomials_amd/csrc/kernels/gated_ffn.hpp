@@ -116,7 +116,7 @@ struct Split {
 template <typename Dt>
 Split plan_split(const GemmArgs& g) {
   constexpr int64_t kStep = Dt::kPlanes == 1 ? 64 : 32;
-  Split p;
+    Split p;
   int64_t tiles = 0;
   for (int z = 0; z < g.batch; ++z) {
     tiles += round_up(g.m[z], 64) / 64 * (round_up(g.n[z], 64) / 64);
@@ -128,34 +128,90 @@ Split plan_split(const GemmArgs& g) {
   return p;
 }
 
+// Directs the product's shares into `sums` and notes what adds them up; the
+// elements of `sums` that it takes.
+inline int64_t split_into(GemmArgs& g, const Split& p, float* sums, SplitSumArgs& q) {
+  int64_t at = 0;
+  for (int z = 0; z < g.batch; ++z) {
+    const int k = q.batch++;
+    q.m[k] = g.m[z], q.n[k] = g.n[z], q.ld[k] = round_up(g.n[z], 4), q.ldc[k] = g.ldc[z], q.to[k] = g.c[z];
+    q.from[k] = sums + at, q.split_stride[k] = p.elements, q.splits[k] = p.splits;
+    g.c[z] = sums + at, g.ldc[z] = q.ld[k];
+    at += q.m[k] * q.ld[k];
+  }
+  g.split_stride = p.elements;
+  g.splits = p.splits;
+  return p.splits * p.elements;
+}
+
+template <typename T>
+int split_sum_launch(const SplitSumArgs& q, hipStream_t st) {
+  int64_t most = 0;
+  for (int k = 0; k < q.batch; ++k) most = std::max(most, q.m[k] * q.ld[k] / 4);
+  if (most == 0) return 0;
+  hipLaunchKernelGGL(split_sum_kernel<T>, dim3(static_cast<unsigned>(std::min<int64_t>((most + 255) / 256, 2048)), q.batch),
+                     dim3(256), 0, st, q);
+  return static_cast<int>(hipGetLastError());
+}
+
 template <typename Dt, bool AAcross, bool BAcross, int Epi>
 int gemm_launch(GemmArgs& g, hipStream_t st);
 
+// A step of 64 x 64 tiles, and the buffers: three workgroups share a compute unit.
+template <typename Dt>
+constexpr int kSmallK = Dt::kPlanes == 1 ? 64 : 32;
+template <typename Dt>
+constexpr int kSmallS = Dt::kPlanes == 1 ? 3 : 2;
+
 // A product with a plain epilogue, split if that pays; `sums` is the space that
-// split_bytes reserved for it.
+// SplitSpace found for it.
 template <typename Dt, bool AAcross, bool BAcross, int Epi>
 int gemm_launch_split(GemmArgs& g, float* sums, hipStream_t st) {
   using T = std::conditional_t<Epi == kEpiStoreF32, float, typename Dt::T>;
   const Split p = plan_split<Dt>(g);
   if (p.splits == 1) return gemm_launch<Dt, AAcross, BAcross, Epi>(g, st);
   SplitSumArgs q{};
-  int64_t at = 0, most = 0;
-  for (int z = 0; z < g.batch; ++z) {
-    q.m[z] = g.m[z], q.n[z] = g.n[z], q.ld[z] = round_up(g.n[z], 4), q.ldc[z] = g.ldc[z], q.to[z] = g.c[z];
-    q.from[z] = sums + at;
-    g.c[z] = sums + at, g.ldc[z] = q.ld[z];
-    at += q.m[z] * q.ld[z];
-    most = std::max(most, q.m[z] * q.ld[z] / 4);
+  split_into(g, p, sums, q);
+  const int rc =
+      gemm_launch_tile<Dt, 64, 64, 2, 2, kSmallK<Dt>, kSmallS<Dt>, AAcross, BAcross, kEpiStoreF32>(g, st);
+  return rc ? rc : split_sum_launch<T>(q, st);
+}
+
+template <typename Dt, int EpiX, int EpiW>
+int gemm_launch_two(GemmArgs& x, GemmArgs& w, hipStream_t st) {
+  int64_t tiles[2] = {0, 0};
+  GemmArgs* g[2] = {&x, &w};
+  for (int k = 0; k < 2; ++k) {
+    if (g[k]->splits < 1) g[k]->splits = 1;
+    for (int z = 0; z < g[k]->batch; ++z) {
+      g[k]->tiles_m[z] = (g[k]->m[z] + 63) / 64;
+      g[k]->tiles_n[z] = (g[k]->n[z] + 63) / 64;
+      tiles[k] += g[k]->tiles_m[z] * g[k]->tiles_n[z];
+    }
   }
-  q.split_stride = g.split_stride = p.elements;
-  q.splits = g.splits = p.splits;
-  q.batch = g.batch;
-  constexpr int kK = Dt::kPlanes == 1 ? 64 : 32, kS = Dt::kPlanes == 1 ? 3 : 2;
-  const int rc = gemm_launch_tile<Dt, 64, 64, 2, 2, kK, kS, AAcross, BAcross, kEpiStoreF32>(g, st);
-  if (rc || most == 0) return rc;
-  hipLaunchKernelGGL(split_sum_kernel<T>, dim3(static_cast<unsigned>(std::min<int64_t>((most + 255) / 256, 2048)), q.batch),
-                     dim3(256), 0, st, q);
+  const int64_t blocks = tiles[0] * x.splits + tiles[1] * w.splits;
+  if (blocks == 0) return 0;
+  hipLaunchKernelGGL((gemm_two_kernel<Dt, kSmallK<Dt>, kSmallS<Dt>, EpiX, EpiW>), dim3(static_cast<unsigned>(blocks)),
+                     dim3(256), 0, st, x, w, tiles[0], tiles[1]);
   return static_cast<int>(hipGetLastError());
+}
+
+// The two together, each split if that pays.
+template <typename Dt>
+int gemm_launch_two_split(GemmArgs& x, GemmArgs& w, float* sums, hipStream_t st) {
+  const Split px = plan_split<Dt>(x), pw = plan_split<Dt>(w);
+  SplitSumArgs q{};
+  int64_t at = 0;
+  if (px.splits > 1) at += split_into(x, px, sums, q);
+  if (pw.splits > 1) split_into(w, pw, sums + at, q);
+  int rc;
+  if (px.splits > 1)
+    rc = pw.splits > 1 ? gemm_launch_two<Dt, kEpiStoreF32, kEpiStoreF32>(x, w, st)
+                       : gemm_launch_two<Dt, kEpiStoreF32, kEpiStore>(x, w, st);
+  else
+    rc = pw.splits > 1 ? gemm_launch_two<Dt, kEpiStore, kEpiStoreF32>(x, w, st)
+                       : gemm_launch_two<Dt, kEpiStore, kEpiStore>(x, w, st);
+  return rc ? rc : split_sum_launch<typename Dt::T>(q, st);
 }
 
 // The tile with the least estimated time.  `each` workgroups of a tile share a
@@ -190,12 +246,12 @@ int gemm_launch(GemmArgs& g, hipStream_t st) {
         return gemm_launch_tile<Dt, 256, 256, 2, 4, 64, 2, AAcross, BAcross, Epi>(g, st);
     }
     if (c128 <= c64) return gemm_launch_tile<Dt, 128, 128, 2, 2, 64, 2, AAcross, BAcross, Epi>(g, st);
-    return gemm_launch_tile<Dt, 64, 64, 2, 2, 64, 3, AAcross, BAcross, Epi>(g, st);
+    return gemm_launch_tile<Dt, 64, 64, 2, 2, kSmallK<Dt>, kSmallS<Dt>, AAcross, BAcross, Epi>(g, st);
   } else {
     // 20000 rows of 128 x 512: paired 52 us with 128 x 128 tiles, 48 us with 64 x 64, three workgroups a unit
     if (cost(128, 128, 1, 0.9) <= cost(64, 64, 3, 0.9))
       return gemm_launch_tile<Dt, 128, 128, 2, 4, 32, 2, AAcross, BAcross, Epi>(g, st);
-    return gemm_launch_tile<Dt, 64, 64, 2, 2, 32, 2, AAcross, BAcross, Epi>(g, st);
+    return gemm_launch_tile<Dt, 64, 64, 2, 2, kSmallK<Dt>, kSmallS<Dt>, AAcross, BAcross, Epi>(g, st);
   }
 }
 
@@ -260,10 +316,11 @@ struct FfnPlan {
 template <typename Dt>
 struct SplitSpace {
   int64_t most = 0;
-  void add(const GemmArgs& g) {
+  static int64_t of(const GemmArgs& g) {
     const Split p = plan_split<Dt>(g);
-    if (p.splits > 1) most = std::max(most, p.splits * p.elements);
+    return p.splits > 1 ? p.splits * p.elements : 0;
   }
+  void add(int64_t elements) { most = std::max(most, elements); }
 };
 
 template <typename Dt>
@@ -310,7 +367,7 @@ int ffn_fwd(const GatedFfnArgs& a, size_t* bytes) {
   GemmArgs g = paired_product<Dt>(a, x, wg, wu, h);
   GemmArgs d = product<Dt>(a.n, a.d_out, a.hidden, h, wd, a.out, a.out_stride);
   SplitSpace<Dt> space;
-  space.add(d);
+  space.add(space.of(d));
   float* sums = plan.arena.template take<float>(space.most);
   if (worst) {
     *bytes = plan.arena.at;
@@ -357,10 +414,9 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
     dw.ldc[2] = down.ldc[0], dw.c[2] = down.c[0];
   }
   SplitSpace<Dt> space;  // sized for every gradient, asked for or not
-  space.add(first);
-  space.add(dx);
-  space.add(dw);
-  if (apart) space.add(down);
+  space.add(space.of(first));
+  space.add(space.of(dx) + space.of(dw));
+  space.add(space.of(down));
   float* sums = plan.arena.template take<float>(space.most);
   if (worst) {
     *bytes = plan.arena.at;
@@ -369,6 +425,10 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
   int rc = plan.run_pack(st);
   if (!rc) rc = gemm_launch_split<Dt, false, true, kEpiStoreF32>(first, sums, st);
   if (!rc) rc = gemm_launch<Dt, false, false, kEpiGatedBwd>(pair, st);
+  // Nor do dx and the weights' gradients wait for each other: one round of the card together (the
+  // case above 16 us, 12 + 11 us in two launches).
+  if (!rc && a.gx && a.gw_gate && tiles + round_up(a.n, 64) / 64 * (round_up(a.d_in, 64) / 64) <= 768)
+    return gemm_launch_two_split<Dt>(dx, dw, sums, st);
   if (!rc && a.gx) rc = gemm_launch_split<Dt, false, true, kEpiStore>(dx, sums, st);
   if (!rc && a.gw_gate) {
     rc = gemm_launch_split<Dt, true, true, kEpiStore>(dw, sums, st);

@@ -226,31 +226,40 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("" ::: "memory");
 }
 
+// The buffers of a tile, declared by the kernel: one object per operand and
+// buffer, so that the compiler has a fragment read wait for direct loads into
+// its own object only.
+template <typename Dt, int BM, int BN, int KS, int S>
+struct TileLds {
+  static constexpr int kA = Dt::kPlanes * BM * KS, kB = Dt::kPlanes * BN * KS;
+  static constexpr int kA2 = S > 2 ? kA : 8, kB2 = S > 2 ? kB : 8, kA3 = S > 3 ? kA : 8, kB3 = S > 3 ? kB : 8;
+};
+#define SEGPOLY_TILE_LDS(L)                                        \
+  __shared__ __attribute__((aligned(16))) uint16_t a0[L::kA];      \
+  __shared__ __attribute__((aligned(16))) uint16_t b0[L::kB];      \
+  __shared__ __attribute__((aligned(16))) uint16_t a1[L::kA];      \
+  __shared__ __attribute__((aligned(16))) uint16_t b1[L::kB];      \
+  __shared__ __attribute__((aligned(16))) uint16_t a2[L::kA2];     \
+  __shared__ __attribute__((aligned(16))) uint16_t b2[L::kB2];     \
+  __shared__ __attribute__((aligned(16))) uint16_t a3[L::kA3];     \
+  __shared__ __attribute__((aligned(16))) uint16_t b3[L::kB3]
+
+// Tile `id` of the batches' tiles, share `share` of its steps.
 template <typename Dt, int BM, int BN, int WM, int WN, int KS, int S, bool AAcross, bool BAcross, int Epi>
-__global__ void __launch_bounds__(WM * WN * 64, 2)
-gemm_tile_kernel(GemmArgs g) {
+__device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int share, uint16_t* a0, uint16_t* b0,
+                                          uint16_t* a1, uint16_t* b1, uint16_t* a2, uint16_t* b2, uint16_t* a3,
+                                          uint16_t* b3) {
   using E = typename Dt::E;
   constexpr bool kPair = Epi == kEpiGated || Epi == kEpiGatedBwd;
   constexpr int kWaves = WM * WN, P = Dt::kPlanes;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // fragments per wave
   constexpr int kStageA = P * BM * KS, kStageB = P * BN * KS;
   static_assert(S >= 2 && S <= 4, "buffers");
-  // one object per operand and buffer: the compiler then has a fragment read
-  // wait for direct loads into its own object only
-  __shared__ __attribute__((aligned(16))) uint16_t a0[kStageA];
-  __shared__ __attribute__((aligned(16))) uint16_t b0[kStageB];
-  __shared__ __attribute__((aligned(16))) uint16_t a1[kStageA];
-  __shared__ __attribute__((aligned(16))) uint16_t b1[kStageB];
-  __shared__ __attribute__((aligned(16))) uint16_t a2[S > 2 ? kStageA : 8];
-  __shared__ __attribute__((aligned(16))) uint16_t b2[S > 2 ? kStageB : 8];
-  __shared__ __attribute__((aligned(16))) uint16_t a3[S > 3 ? kStageA : 8];
-  __shared__ __attribute__((aligned(16))) uint16_t b3[S > 3 ? kStageB : 8];
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wm = wave / WN, wn = wave % WN;
 
   int z = 0;
-  int64_t id = blockIdx.x;
   if constexpr (!kPair) {
     while (z + 1 < g.batch && id >= g.tiles_m[z] * g.tiles_n[z]) id -= g.tiles_m[z] * g.tiles_n[z], ++z;
   }
@@ -283,8 +292,8 @@ gemm_tile_kernel(GemmArgs g) {
 
   // this workgroup's share of the steps of all phases
   const int64_t steps = (g.k + KS - 1) / KS;
-  const int64_t s0 = kPair ? 0 : steps * g.phases * blockIdx.y / g.splits;
-  int left = static_cast<int>((kPair ? steps : steps * g.phases * (blockIdx.y + 1) / g.splits) - s0);
+  const int64_t s0 = kPair ? 0 : steps * g.phases * share / g.splits;
+  int left = static_cast<int>((kPair ? steps : steps * g.phases * (share + 1) / g.splits) - s0);
   int to_load = left;  // none: a gradient over no rows is zero
 
   // the next step to load: its k left, its corners and the bytes from there to the operands' ends
@@ -437,7 +446,7 @@ gemm_tile_kernel(GemmArgs g) {
     for (int i = 0; i < FM; ++i) {
       const int64_t m = m0 + wm * (BM / WM) + i * 16 + lane % 16;
       if (m >= gm) continue;
-      T* row = static_cast<T*>(g.c[z]) + (Epi == kEpiStoreF32 ? g.split_stride * blockIdx.y : 0) + m * g.ldc[z];
+      T* row = static_cast<T*>(g.c[z]) + (Epi == kEpiStoreF32 ? g.split_stride * share : 0) + m * g.ldc[z];
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const int64_t n = n0 + wn * (BN / WN) + j * 16 + lane / 16 * 4;
@@ -555,12 +564,40 @@ gemm_tile_kernel(GemmArgs g) {
   }
 }
 
+template <typename Dt, int BM, int BN, int WM, int WN, int KS, int S, bool AAcross, bool BAcross, int Epi>
+__global__ void __launch_bounds__(WM * WN * 64, 2)
+gemm_tile_kernel(GemmArgs g) {
+  using L = TileLds<Dt, BM, BN, KS, S>;
+  SEGPOLY_TILE_LDS(L);
+  gemm_tile<Dt, BM, BN, WM, WN, KS, S, AAcross, BAcross, Epi>(g, blockIdx.x, blockIdx.y, a0, b0, a1, b1, a2, b2, a3, b3);
+}
+
+// Two independent products in one launch, of 64 x 64 tiles: x with one operand
+// across k, w with both; x has the first x_blocks workgroups, its shares side
+// by side.
+template <typename Dt, int KS, int S, int EpiX, int EpiW>
+__global__ void __launch_bounds__(256, 2)
+gemm_two_kernel(GemmArgs x, GemmArgs w, int64_t x_tiles, int64_t w_tiles) {
+  using L = TileLds<Dt, 64, 64, KS, S>;
+  SEGPOLY_TILE_LDS(L);
+  const int64_t x_blocks = x_tiles * x.splits;
+  if (blockIdx.x < x_blocks) {
+    gemm_tile<Dt, 64, 64, 2, 2, KS, S, false, true, EpiX>(x, blockIdx.x % x_tiles, static_cast<int>(blockIdx.x / x_tiles),
+                                                          a0, b0, a1, b1, a2, b2, a3, b3);
+  } else {
+    const int64_t id = blockIdx.x - x_blocks;
+    gemm_tile<Dt, 64, 64, 2, 2, KS, S, true, true, EpiW>(w, id % w_tiles, static_cast<int>(id / w_tiles), a0, b0, a1, b1,
+                                                         a2, b2, a3, b3);
+  }
+}
+
 // The sum of the shares, in order, in the output's type: four columns a lane.
 struct SplitSumArgs {
-  const float* from[kMaxBatch];
-  void* to[kMaxBatch];
-  int64_t m[kMaxBatch], n[kMaxBatch], ld[kMaxBatch], ldc[kMaxBatch], split_stride;
-  int batch, splits;
+  static constexpr int kMax = kMaxBatch + 1;
+  const float* from[kMax];
+  void* to[kMax];
+  int64_t m[kMax], n[kMax], ld[kMax], ldc[kMax], split_stride[kMax];
+  int splits[kMax], batch;
 };
 template <typename T>
 __global__ void __launch_bounds__(256)
@@ -574,7 +611,7 @@ split_sum_kernel(SplitSumArgs g) {
     const float* from = g.from[z] + r * g.ld[z] + c;
     v4f s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-    for (int k = 0; k < g.splits; ++k) s += *reinterpret_cast<const v4f*>(from + k * g.split_stride);
+    for (int k = 0; k < g.splits[z]; ++k) s += *reinterpret_cast<const v4f*>(from + k * g.split_stride[z]);
     T* to = static_cast<T*>(g.to[z]) + r * g.ldc[z] + c;
     const T v[4] = {static_cast<T>(s[0]), static_cast<T>(s[1]), static_cast<T>(s[2]), static_cast<T>(s[3])};
     if (c + 4 <= g.n[z]) {
