@@ -29,7 +29,7 @@ LIB = os.path.join(OUT, "libsegpoly_san.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
 HOST_SOURCES = ["irreps.cpp", "cg.cpp", "tp_descriptor.cpp", "symcon_descriptor.cpp", "capi.cpp", "capi_linear.cpp",
-                "capi_sh.cpp", "capi_fctp.cpp", "capi_edge.cpp"]
+                "capi_sh.cpp", "capi_fctp.cpp", "capi_edge.cpp", "capi_channel.cpp"]
 SAN = ["-fsanitize=address,undefined", "-fno-omit-frame-pointer", "-fno-sanitize-recover=undefined"]
 
 
@@ -63,7 +63,8 @@ def run_tests():
                ASAN_OPTIONS="detect_leaks=0:abort_on_error=1:halt_on_error=1",
                UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1")
     _run([sys.executable, "-m", "pytest", "-x", "-q", "-p", "no:cacheprovider",
-          os.path.join(ROOT, "tests", "test_capi_host.py")], env=env)
+          os.path.join(ROOT, "tests", "test_capi_host.py"),
+          os.path.join(ROOT, "tests", "test_capi_channel_host.py")], env=env)
 
 
 if __name__ == "__main__":
