@@ -365,10 +365,16 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
   };
 
   v4f acc[FM][FN];
+  // the five small products of float32 planes are summed apart: added to the
+  // large sum one by one they would round it six times as often
+  v4f small[P > 1 ? FM : 1][P > 1 ? FN : 1];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < FN; ++j) {
+      acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      if constexpr (P > 1) small[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
 
   // paired: the wave's first FN/2 fragments are of B, the others of B2
   auto b_row = [&](int j) {
@@ -398,8 +404,14 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
-          for (int j = 0; j < FN; ++j)
-            acc[i][j] = mma16(E{}, fb[P == 1 ? 0 : kPairs3[t][1]][j], fa[P == 1 ? 0 : kPairs3[t][0]][i], acc[i][j]);
+          for (int j = 0; j < FN; ++j) {
+            if constexpr (P == 1) {
+              acc[i][j] = mma16(E{}, fb[0][j], fa[0][i], acc[i][j]);
+            } else {
+              v4f& c = t < kProducts - 1 ? small[i][j] : acc[i][j];
+              c = mma16(E{}, fb[kPairs3[t][1]][j], fa[kPairs3[t][0]][i], c);
+            }
+          }
     }
   };
 
@@ -438,6 +450,12 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
     }
   }
   __builtin_amdgcn_s_waitcnt(0x0f70);  // no load into LDS outlives the workgroup
+  if constexpr (P > 1) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] += small[i][j];
+  }
 
   // ---------------------------------------------------------- epilogue
   if constexpr (!kPair) {
