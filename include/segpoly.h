@@ -727,7 +727,8 @@ int embedding_fwd(int dtype, const void* table, int64_t rows, int64_t dim, const
 
 /* embedding_bwd_workspace: bytes embedding_bwd needs (sorted tokens and
  * their positions, row ranges, float32 sums of 16 positions; for at most 16
- * rows the float32 sums of up to 512 segments of the positions). */
+ * rows the float32 sums of up to 512 segments of the positions, fewer for
+ * rows of more than 1024 columns). */
 int embedding_bwd_workspace(int64_t n, int64_t rows, int64_t dim, size_t* bytes);
 
 /*

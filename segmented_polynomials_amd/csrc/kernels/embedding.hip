@@ -26,7 +26,8 @@ namespace segpoly {
 EmbeddingPlan embedding_plan(int64_t n, int64_t rows, int64_t dim) {
   EmbeddingPlan p{};
   if (rows <= kEmbDirectRows) {
-    p.segments = std::max<int64_t>(1, std::min<int64_t>((n + 63) / 64, 512));
+    // 512 workgroups over the segments and the tiles of 1024 columns
+    p.segments = std::max<int64_t>(1, std::min<int64_t>((n + 63) / 64, 512 / std::max<int64_t>(1, (dim + 1023) / 1024)));
     p.bytes = round_up(4 * p.segments * rows * dim, 256);
     return p;
   }

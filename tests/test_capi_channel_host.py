@@ -140,3 +140,11 @@ def test_binding_checks_host_tensors():
         sp.gated_ffn_fwd(t, t, t, t)
     with pytest.raises(ValueError):
         sp.gated_ffn_fwd(t, t, t, t, act="tanh")
+
+
+def test_embedding_workspace_of_small_tables():
+    """Tables summed in LDS: the sums of the segments, bounded for wide rows."""
+    assert sp.embedding_bwd_workspace(50000, 10, 128) == 4 * 512 * 10 * 128
+    assert sp.embedding_bwd_workspace(1, 10, 128) == 4 * 10 * 128
+    assert sp.embedding_bwd_workspace(1 << 30, 16, 1 << 21) == 4 * 16 << 21
+    assert sp.embedding_bwd_workspace(1 << 30, 16, 8192) == 4 * 64 * 16 * 8192
