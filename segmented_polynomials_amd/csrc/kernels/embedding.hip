@@ -27,7 +27,7 @@ EmbeddingPlan embedding_plan(int64_t n, int64_t rows, int64_t dim) {
   EmbeddingPlan p{};
   if (rows <= kEmbDirectRows) {
     // 512 workgroups over the segments and the tiles of 1024 columns
-    p.segments = std::max<int64_t>(1, std::min<int64_t>((n + 63) / 64, 512 / std::max<int64_t>(1, (dim + 1023) / 1024)));
+    p.segments = std::max<int64_t>(1, std::min<int64_t>((n + 15) / 16, 512 / std::max<int64_t>(1, (dim + 1023) / 1024)));
     p.bytes = round_up(4 * p.segments * rows * dim, 256);
     return p;
   }
@@ -141,12 +141,13 @@ embedding_direct_kernel(const T* __restrict__ g, int64_t g_stride, const Index* 
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * tile; i += kThreads) {
-    const int col = static_cast<int>(blockIdx.y) * tile + i % tile;
-    if (col >= dim) continue;
+  const int tile_bits = __builtin_ctz(tile);  // a power of two, as the lanes are
+#pragma unroll 4
+  for (int i = threadIdx.x; i < rows << tile_bits; i += kThreads) {
+    const int r = i >> tile_bits, col = static_cast<int>(blockIdx.y) * tile + (i & (tile - 1));
     float s = 0.f;
-    for (int q = 0; q < groups; ++q) s += acc[q * rows * tile + i];
-    partial[(static_cast<int64_t>(blockIdx.x) * rows + i / tile) * dim + col] = s;
+    for (int q = 0; q < groups; ++q) s += acc[((q * rows) << tile_bits) + i];
+    if (col < dim) partial[(static_cast<int64_t>(blockIdx.x) * rows + r) * dim + col] = s;
   }
 }
 
@@ -529,8 +530,9 @@ __device__ __forceinline__ void sum_range(const T* __restrict__ g, int64_t g_str
   }
 }
 
-// A workgroup takes 1024 / lanes table rows (`lanes` at most a wave), every
-// gridDim.x-th: frequent tokens are often neighbours.  It
+// A workgroup takes 16 table rows, or one for each of its groups of `lanes`
+// lanes (at most a wave), every gridDim.x-th: frequent tokens are often
+// neighbours.  It
 // writes zeros for its empty ranges, all threads together: most rows of a large
 // table have no token, and the dependent loads of the others' sums take longer
 // than all the zeros.  Then a group of lanes sums a short range alone; a range
@@ -547,10 +549,10 @@ embedding_rows_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t*
                       T* __restrict__ out) {
   constexpr int V = Chunk<T>::kN, kCols = 2, kAlone = Few ? -1 : 8;
   __shared__ float acc_lds[256 * V * kCols];
-  __shared__ uint32_t range[2][128];
-  __shared__ int long_rows[128], long_count;
+  __shared__ uint32_t range[2][32];
+  __shared__ int long_rows[32], long_count;
   const int groups = 256 / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-  const int here = Few ? 1 : 4 * groups;  // rows of this workgroup
+  const int here = Few ? 1 : groups > 16 ? groups : 16;  // rows of this workgroup
   auto row_of = [](int q) { return blockIdx.x + static_cast<int64_t>(q) * gridDim.x; };
   auto items = [](int64_t s, int64_t e) {  // loads of a lane that sums the range alone
     const int64_t c_lo = (s + kEmbChunk - 1) / kEmbChunk, c_hi = e / kEmbChunk;
@@ -690,7 +692,7 @@ int embedding_bwd_launch(const EmbeddingArgs& a) {
     hipLaunchKernelGGL((embedding_chunk_kernel<T>), dim3(static_cast<unsigned>(range_blocks + p.chunks)), dim3(256), 0,
                        st, static_cast<const T*>(a.grad), a.grad_stride, key[last], pos[last], p.keys, a.dim, a.n,
                        range_blocks, lanes, rowptr, partial, round_up(a.dim, 8));
-  const int narrow = row_lanes<T>(a.dim, 64), each = 1024 / narrow;
+  const int narrow = row_lanes<T>(a.dim, 64), each = std::max(256 / narrow, 16);
   const bool few = a.rows < 2048;
   auto* sum = few ? embedding_rows_kernel<T, true> : embedding_rows_kernel<T, false>;
   hipLaunchKernelGGL(sum, dim3(static_cast<unsigned>(few ? a.rows : (a.rows + each - 1) / each)), dim3(256), 0, st,
