@@ -290,7 +290,9 @@ block_norm_bwd_kernel(BlockNormArgs a) {
     }
     row_sum<G, 3>(s2, lds, half);
     {
-      const float ryv = next ? rsqrtf(s2[1] * inv + a.eps) : 0.f;  // eps may be zero
+      // zero without a row or a second norm: with eps = 0 the root of their zeros is
+      // infinite, and its product with them NaN in the column sums of all rows
+      const float ryv = next && d ? rsqrtf(s2[1] * inv + a.eps) : 0.f;
       const float k = s2[2] * inv * ryv * ryv;
 #pragma unroll
       for (int i = 0; i < E; ++i) {
@@ -300,7 +302,7 @@ block_norm_bwd_kernel(BlockNormArgs a) {
     }
     Map::store(static_cast<T*>(a.gx) + at, d, dy);
     if constexpr (Layer) Map::centre(dy, 0.f, d);  // the means reached past the row's end
-    const float rstd = rsqrtf(s2[0] * inv + a.eps);
+    const float rstd = d ? rsqrtf(s2[0] * inv + a.eps) : 0.f;
     float c[E];
     param_at(0, c);
     float s3[3] = {0.f, 0.f, 0.f};  // sums of p = dy c gate, p f, dy c norm(f)

@@ -1,0 +1,53 @@
+"""GPU tests of the invariant-channel operators at the ends of their ranges:
+eps of zero, empty calls, single rows of any stride, values outside the element
+type's range between products, infinities and NaN, the limits of the embedding
+gradient's ordering, and the accuracy that the forms promise.  Tolerances as in
+``test_gpu_channel_ops``, whose references are used where they fit."""
+
+import pytest
+import torch
+
+from tests._gpu import announce, need_gpu
+from tests.test_gpu_channel_ops import HALF, NORM_F32, T, check, gen, norm64, nvjp64, nvjp_abs, rnd
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ block norm
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("gate", ["none", "row", "element"])
+@pytest.mark.parametrize("n,dim,nxt", [(1, 64, True), (3, 33, True), (37, 64, False), (37, 200, True), (5, 511, True),
+                                       (37, 1000, True), (1, 1000, False)])
+def test_block_norm_without_eps(n, dim, nxt, gate, kind, dtype):
+    """eps = 0, numbers of rows that are no multiple of a workgroup's: what
+    stands past the last row takes no part in the parameters' gradients."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"block norm, eps 0, n={n} dim={dim} {kind} gate={gate} next={nxt} {dtype}")
+    g = gen(n + dim)
+    x, f, gy, gh = (rnd(g, n, dim, dtype=dtype) for _ in range(4))
+    gt = None if gate == "none" else rnd(g, n, 1 if gate == "row" else dim, dtype=dtype)
+    wp, rs = 1 + rnd(g, dim, std=0.1), 0.5 + rnd(g, dim, std=0.1)
+    wn = 1 + rnd(g, dim, std=0.1) if nxt else None
+    kw = dict(f=f, gate=gt, w_post=wp, res_scale=rs, w_pre=wn, kind=kind, eps=0.0)
+    nf, rf, nfa = norm64(f.double(), kind, 0.0)
+    s = rs.double()
+    G = torch.ones(n, 1, dtype=torch.float64, device="cuda") if gt is None else gt.double()
+    v, va = nf * wp.double(), nfa * wp.double().abs()
+    y, _ = sp.block_norm_fwd(x, **kw)
+    check(y, x.double() + s * G * v, NORM_F32 * (x.double().abs() + (s * G).abs() * va), dtype, "y")
+    Y, dy, dya = y.double(), gy.double(), gy.double().abs()
+    if nxt:
+        ny, ry, nya = norm64(Y, kind, 0.0)
+        q = gh.double() * wn.double()
+        dy, dya = dy + nvjp64(q, ny, ry, kind), dya + nvjp_abs(q.abs(), nya, ry, kind)
+    got = sp.block_norm_bwd(y, gy, gh if nxt else None, **kw)
+    p, pa = dy * s * G * wp.double(), dya * (s * G).abs() * wp.double().abs()
+    check(got[0], dy, NORM_F32 * dya, dtype, "grad_x")
+    check(got[1], nvjp64(p, nf, rf, kind), NORM_F32 * nvjp_abs(pa, nfa, rf, kind), dtype, "grad_f")
+    check(got[3], (dy * s * G * nf).sum(0), NORM_F32 * (dya * (s * G).abs() * nfa).sum(0), "f32", "grad_w_post")
+    check(got[4], (dy * G * v).sum(0), NORM_F32 * (dya * G.abs() * va).sum(0), "f32", "grad_res_scale")
+    if nxt:
+        check(got[5], (gh.double() * ny).sum(0), NORM_F32 * (gh.double().abs() * nya).sum(0), "f32", "grad_w_pre")
