@@ -812,7 +812,8 @@ int gated_ffn_fwd(int dtype, int act, const void* x, int64_t x_stride, const voi
  * gated_ffn_bwd: vector-Jacobian product of gated_ffn_fwd for grad_out
  * [n, d_out]; the hidden rows are computed again.  grad_x [n, d_in] or NULL;
  * the three weight gradients, shaped as the weights, or all NULL.  With
- * n == 0 the weight gradients are zero.
+ * n == 0 the weight gradients are zero, and no input or workspace is read
+ * (all may be NULL).
  */
 int gated_ffn_bwd(int dtype, int act, const void* x, int64_t x_stride, const void* w_gate, const void* w_up,
                   const void* w_down, const void* grad_out, int64_t grad_out_stride, int64_t n, int64_t d_in,

@@ -182,7 +182,7 @@ int gated_ffn_workspace(int dtype, int64_t n, int64_t d_in, int64_t hidden, int6
   if (!bytes) return fail(SEGPOLY_E_INVALID, "null bytes");
   int rc = check_ffn(dtype, SEGPOLY_ACT_SILU, n, d_in, hidden, d_out);
   if (rc) return rc;
-  *bytes = n == 0 && !backward ? 0 : gated_ffn_workspace_bytes(dtype, n, d_in, hidden, d_out, backward != 0);
+  *bytes = gated_ffn_workspace_bytes(dtype, n, d_in, hidden, d_out, backward != 0);
   return ok();
 }
 

@@ -86,7 +86,7 @@ struct GatedFfnArgs {
   void* workspace;
   void* stream;
 };
-// workspace bytes for any strides and alignments of these sizes
+// workspace bytes for any strides and alignments of these sizes; none for no rows
 size_t gated_ffn_workspace_bytes(int dtype, int64_t n, int64_t d_in, int64_t hidden, int64_t d_out, bool backward);
 int launch_gated_ffn_fwd(const GatedFfnArgs& a);
 int launch_gated_ffn_bwd(const GatedFfnArgs& a);

@@ -290,11 +290,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
   const int step_a = static_cast<int>(AAcross ? KS * lda * 2 : KS * 2);  // bytes
   const int step_b = static_cast<int>(BAcross ? KS * ldb * 2 : KS * 2);
 
-  // this workgroup's share of the steps of all phases
+  // this workgroup's share of the steps of all phases, one at least
   const int64_t steps = (g.k + KS - 1) / KS;
   const int64_t s0 = kPair ? 0 : steps * g.phases * share / g.splits;
   int left = static_cast<int>((kPair ? steps : steps * g.phases * (share + 1) / g.splits) - s0);
-  int to_load = left;  // none: a gradient over no rows is zero
+  int to_load = left;
 
   // the next step to load: its k left, its corners and the bytes from there to the operands' ends
   int phase = 0, k_left = 0;
@@ -312,22 +312,17 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
     left_a = left_a0;
     left_b = left_b0;
   };
-  if (left > 0) {
-    phase = static_cast<int>(s0 / steps);
-    matrices();
-    const int64_t skip = s0 % steps;
+  phase = static_cast<int>(s0 / steps);
+  matrices();
+  const int64_t skip = s0 % steps;
 #pragma unroll
-    for (int q = 0; q < P; ++q) {
-      pa[q] += skip * step_a;
-      pb[q] += skip * step_b;
-    }
-    left_a -= skip * step_a;
-    left_b -= skip * step_b;
-    k_left -= static_cast<int>(skip * KS);
-  } else {
-    matrices();
-    left_a = left_b = 0;
+  for (int q = 0; q < P; ++q) {
+    pa[q] += skip * step_a;
+    pb[q] += skip * step_b;
   }
+  left_a -= skip * step_a;
+  left_b -= skip * step_b;
+  k_left -= static_cast<int>(skip * KS);
   // Loads are issued for exactly S - 1 steps past the last one too (of nothing:
   // the range is empty), so that the count of those outstanding is the same in
   // every step, for the wait below and for the compiler's own.

@@ -51,3 +51,23 @@ def test_block_norm_without_eps(n, dim, nxt, gate, kind, dtype):
     check(got[4], (dy * G * v).sum(0), NORM_F32 * (dya * G.abs() * va).sum(0), "f32", "grad_res_scale")
     if nxt:
         check(got[5], (gh.double() * ny).sum(0), NORM_F32 * (gh.double().abs() * nya).sum(0), "f32", "grad_w_pre")
+
+
+# ------------------------------------------------------------------ gated feed-forward
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("di,F,do", [(8, 16, 8), (33, 70, 5), (1000, 1200, 900)])
+def test_gated_ffn_bwd_of_no_rows(di, F, do, dtype):
+    """The weight gradients over no rows are zeros and their neighbours
+    untouched; weights, rows and workspace may be null."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"gated ffn backward of no rows, null inputs, {di} x {F} x {do} {dtype}")
+    bufs = [torch.full((k + 2,), 7.0, dtype=T[dtype], device="cuda") for k in (F * di, F * di, do * F)]
+    to = [b.data_ptr() + b.element_size() for b in bufs]
+    code = {"f32": sp.F32, "bf16": sp.BF16, "f16": sp.F16}[dtype]
+    rc = sp.lib.gated_ffn_bwd(code, 0, None, di, None, None, None, None, do, 0, di, F, do, None, *to, None, 0,
+                              torch.cuda.current_stream().cuda_stream)
+    assert rc == sp.OK
+    for b in bufs:
+        assert not b[1:-1].any() and b[0] == 7 and b[-1] == 7
