@@ -800,6 +800,8 @@ int gated_ffn_workspace(int dtype, int64_t n, int64_t d_in, int64_t hidden, int6
  * gated_ffn_fwd: out = (act(x w_gate^T) * (x w_up^T)) w_down^T.
  *   x [n, d_in], w_gate, w_up [hidden, d_in], w_down [d_out, hidden],
  *   out [n, d_out], all T.
+ * Widths and, of more than one row, row strides are at most 2^21
+ * (E_UNSUPPORTED, E_INVALID above).
  * Products on the matrix cores with float32 sums; the hidden rows are held
  * in T between the two products (float32 in 24 bits).  A float32 infinity
  * gives NaN where the product of its planes meets a zero.

@@ -36,8 +36,12 @@ int check_workspace(const void* ws, size_t have, size_t need) {
   return SEGPOLY_OK;
 }
 
-// the largest width, row stride and table the kernels' 32-bit offsets take
+// the largest width and row stride the kernels' 32-bit offsets take
 constexpr int64_t kMaxWidth = int64_t{1} << 21;
+
+// The row stride of a feed-forward operand: that of a single row, or none, is never
+// used, whatever the tensor it was taken from.
+int64_t row_stride(int64_t n, int64_t stride, int64_t width) { return n <= 1 ? width : stride; }
 
 int check_embedding(int dtype, int idx_dtype, int64_t rows, int64_t dim, int64_t n) {
   int rc = check_dtype(dtype);
@@ -191,6 +195,7 @@ int gated_ffn_fwd(int dtype, int act, const void* x, int64_t x_stride, const voi
                   int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_ffn(dtype, act, n, d_in, hidden, d_out);
   if (rc) return rc;
+  x_stride = row_stride(n, x_stride, d_in);
   if (x_stride < 0 || x_stride > kMaxWidth || out_stride < d_out) return fail(SEGPOLY_E_INVALID, "bad row stride");
   if (n == 0) return ok();
   if (!x || !w_gate || !w_up || !w_down || !out) return fail(SEGPOLY_E_INVALID, "null buffer");
@@ -210,6 +215,8 @@ int gated_ffn_bwd(int dtype, int act, const void* x, int64_t x_stride, const voi
                   void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_ffn(dtype, act, n, d_in, hidden, d_out);
   if (rc) return rc;
+  x_stride = row_stride(n, x_stride, d_in);
+  grad_out_stride = row_stride(n, grad_out_stride, d_out);
   if (x_stride < 0 || x_stride > kMaxWidth || grad_out_stride < 0 || grad_out_stride > kMaxWidth)
     return fail(SEGPOLY_E_INVALID, "bad row stride");
   if (n && (!x || !w_gate || !w_up || !w_down || !grad_out)) return fail(SEGPOLY_E_INVALID, "null buffer");

@@ -28,3 +28,13 @@ def test_gated_ffn_bwd_of_no_rows_needs_no_input(dtype):
                                 None) == sp.E_INVALID
     assert sp.lib.gated_ffn_bwd(dtype, 0, P, 8, P, None, P, P, 8, 3, 8, 16, 8, P, None, None, None, P, 1 << 30,
                                 None) == sp.E_INVALID
+
+
+def test_gated_ffn_row_stride_of_a_single_row():
+    """Never used, so never too large; the call then fails for its workspace."""
+    for n, what in ((1, "null workspace"), (2, "bad row stride")):
+        assert sp.lib.gated_ffn_fwd(sp.BF16, 0, P, 1 << 40, P, P, P, n, 8, 16, 8, P, 8, None, 0, None) == sp.E_INVALID
+        assert what in sp.lib.segpoly_last_error().decode()
+        assert sp.lib.gated_ffn_bwd(sp.BF16, 0, P, 1 << 40, P, P, P, P, 1 << 40, n, 8, 16, 8, P, P, P, P, None, 0,
+                                    None) == sp.E_INVALID
+        assert what in sp.lib.segpoly_last_error().decode()

@@ -71,3 +71,21 @@ def test_gated_ffn_bwd_of_no_rows(di, F, do, dtype):
     assert rc == sp.OK
     for b in bufs:
         assert not b[1:-1].any() and b[0] == 7 and b[-1] == 7
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("d", [1024, 1001])
+def test_gated_ffn_single_row_of_a_long_tensor(d, dtype):
+    """The last position of one sequence: one row, whose stride is never used."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"gated ffn, one row with a row stride above 2^21, d={d} {dtype}")
+    g = gen(d)
+    seq, gseq = rnd(g, 1, 2500, d, dtype=dtype), rnd(g, 1, 2500, d, dtype=dtype)
+    x, gy = seq[:, -1], gseq[:, -1]
+    assert x.stride(0) > 1 << 21
+    wg, wu = (rnd(g, 72, d, std=d ** -0.5, dtype=dtype) for _ in range(2))
+    wd = rnd(g, d, 72, std=0.1, dtype=dtype)
+    assert torch.equal(sp.gated_ffn_fwd(x, wg, wu, wd), sp.gated_ffn_fwd(x.clone(), wg, wu, wd))
+    a, b = sp.gated_ffn_bwd(x, wg, wu, wd, gy), sp.gated_ffn_bwd(x.clone(), wg, wu, wd, gy.clone())
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
