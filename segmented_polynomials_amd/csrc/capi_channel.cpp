@@ -2,6 +2,7 @@
 // gated feed-forward, each with its backward.  Host code.
 #include <hip/hip_runtime_api.h>
 
+#include <initializer_list>
 #include <string>
 
 #include "capi_util.hpp"
@@ -26,6 +27,14 @@ int check_dtype(int dtype) {
 }
 
 bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// every buffer at a multiple of its element's size
+int check_aligned(int64_t bytes, std::initializer_list<const void*> buffers) {
+  for (const void* p : buffers)
+    if (!aligned(p, bytes)) return fail(SEGPOLY_E_INVALID, "misaligned buffer");
+  return SEGPOLY_OK;
+}
+int64_t index_bytes(int idx_dtype) { return idx_dtype == SEGPOLY_I32 ? 4 : 8; }
 
 int check_workspace(const void* ws, size_t have, size_t need) {
   if (need == 0) return SEGPOLY_OK;
@@ -89,8 +98,8 @@ int embedding_fwd(int dtype, const void* table, int64_t rows, int64_t dim, const
   if (out_stride < dim) return fail(SEGPOLY_E_INVALID, "out_stride below dim");
   if (n == 0 || dim == 0) return ok();
   if ((rows && !table) || !tokens || !out) return fail(SEGPOLY_E_INVALID, "null buffer");
-  if (!aligned(table, channel_dtype_bytes(dtype)) || !aligned(out, channel_dtype_bytes(dtype)))
-    return fail(SEGPOLY_E_INVALID, "misaligned buffer");
+  if ((rc = check_aligned(channel_dtype_bytes(dtype), {table, out}))) return rc;
+  if ((rc = check_aligned(index_bytes(idx_dtype), {tokens}))) return rc;
   EmbeddingArgs a{};
   a.table = table, a.tokens = tokens, a.out = out, a.rows = rows, a.dim = dim, a.n = n, a.out_stride = out_stride;
   a.scale = static_cast<float>(scale), a.dtype = dtype, a.idx = idx_dtype, a.stream = stream;
@@ -113,8 +122,8 @@ int embedding_bwd(int dtype, const void* grad_out, int64_t grad_stride, const vo
   if (grad_stride < 0) return fail(SEGPOLY_E_INVALID, "negative stride");
   if (rows == 0 || dim == 0) return ok();
   if (!grad_table || (n && (!grad_out || !tokens))) return fail(SEGPOLY_E_INVALID, "null buffer");
-  if (!aligned(grad_table, channel_dtype_bytes(dtype)) || !aligned(grad_out, channel_dtype_bytes(dtype)))
-    return fail(SEGPOLY_E_INVALID, "misaligned buffer");
+  if ((rc = check_aligned(channel_dtype_bytes(dtype), {grad_table, grad_out}))) return rc;
+  if ((rc = check_aligned(index_bytes(idx_dtype), {tokens}))) return rc;
   rc = check_workspace(workspace, workspace_bytes, embedding_plan(n, rows, dim).bytes);
   if (rc) return rc;
   EmbeddingArgs a{};
@@ -134,6 +143,8 @@ int block_norm_fwd(int dtype, int kind, int gate_mode, int gate_act, const void*
   if (!x || !f || !w_post || !y || (gate_mode != SEGPOLY_GATE_NONE && !gate))
     return fail(SEGPOLY_E_INVALID, "null buffer");
   if ((w_pre != nullptr) != (h != nullptr)) return fail(SEGPOLY_E_INVALID, "w_pre and h come together");
+  if ((rc = check_aligned(channel_dtype_bytes(dtype), {x, f, gate, y, h}))) return rc;
+  if ((rc = check_aligned(4, {w_post, res_scale, w_pre}))) return rc;
   BlockNormArgs a{};
   a.x = x, a.f = f, a.gate = gate, a.w_post = static_cast<const float*>(w_post);
   a.res_scale = static_cast<const float*>(res_scale), a.w_pre = static_cast<const float*>(w_pre), a.y = y, a.h = h;
@@ -166,6 +177,8 @@ int block_norm_bwd(int dtype, int kind, int gate_mode, int gate_act, const void*
   if (n && (!grad_y || !f || !grad_x || !grad_f || (gate_mode != SEGPOLY_GATE_NONE && (!gate || !grad_gate)) ||
             (w_pre && (!y || !grad_h))))
     return fail(SEGPOLY_E_INVALID, "null buffer");
+  if ((rc = check_aligned(channel_dtype_bytes(dtype), {y, grad_y, grad_h, f, gate, grad_x, grad_f, grad_gate}))) return rc;
+  if ((rc = check_aligned(4, {w_post, res_scale, w_pre, grad_w_post, grad_res_scale, grad_w_pre}))) return rc;
   const int64_t parts = block_norm_parts(n, dim);
   rc = check_workspace(workspace, workspace_bytes, static_cast<size_t>(parts) * 2 * dim * 4);
   if (rc) return rc;
@@ -199,6 +212,7 @@ int gated_ffn_fwd(int dtype, int act, const void* x, int64_t x_stride, const voi
   if (x_stride < 0 || x_stride > kMaxWidth || out_stride < d_out) return fail(SEGPOLY_E_INVALID, "bad row stride");
   if (n == 0) return ok();
   if (!x || !w_gate || !w_up || !w_down || !out) return fail(SEGPOLY_E_INVALID, "null buffer");
+  if ((rc = check_aligned(channel_dtype_bytes(dtype), {x, w_gate, w_up, w_down, out}))) return rc;
   rc = check_workspace(workspace, workspace_bytes,
                        gated_ffn_workspace_bytes(dtype, n, d_in, hidden, d_out, false));
   if (rc) return rc;
@@ -223,6 +237,9 @@ int gated_ffn_bwd(int dtype, int act, const void* x, int64_t x_stride, const voi
   const int weights = (grad_w_gate != nullptr) + (grad_w_up != nullptr) + (grad_w_down != nullptr);
   if (weights != 0 && weights != 3) return fail(SEGPOLY_E_INVALID, "the three weight gradients come together");
   if (!weights && !grad_x) return fail(SEGPOLY_E_INVALID, "no gradient requested");
+  if ((rc = check_aligned(channel_dtype_bytes(dtype), {x, w_gate, w_up, w_down, grad_out, grad_x, grad_w_gate, grad_w_up,
+                                                       grad_w_down})))
+    return rc;
   rc = check_workspace(workspace, workspace_bytes, gated_ffn_workspace_bytes(dtype, n, d_in, hidden, d_out, true));
   if (rc) return rc;
   GatedFfnArgs a{};

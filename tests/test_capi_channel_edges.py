@@ -38,3 +38,32 @@ def test_gated_ffn_row_stride_of_a_single_row():
         assert sp.lib.gated_ffn_bwd(sp.BF16, 0, P, 1 << 40, P, P, P, P, 1 << 40, n, 8, 16, 8, P, P, P, P, None, 0,
                                     None) == sp.E_INVALID
         assert what in sp.lib.segpoly_last_error().decode()
+
+
+def misaligned(fn, args, at, by):
+    a = list(args)
+    a[at] = P + by
+    return fn(*a) == sp.E_INVALID and "misaligned" in sp.lib.segpoly_last_error().decode()
+
+
+@pytest.mark.parametrize("dtype,off", [(sp.F32, 2), (sp.BF16, 1), (sp.F16, 1)])
+def test_buffers_off_their_elements_are_refused(dtype, off):
+    """Buffers of the rows' type by half an element, parameters and tokens by
+    two bytes; no other argument is at fault, and none is launched."""
+    small = 0  # of the workspace: refused afterwards, were the alignment not
+    emb = (dtype, P, 5, 8, P, sp.I64, 3, 1.0, P, 8, None)
+    assert all(misaligned(sp.lib.embedding_fwd, emb, i, off) for i in (1, 8))
+    assert misaligned(sp.lib.embedding_fwd, emb, 4, 4)
+    emb = (dtype, P, 8, P, sp.I32, 3, 5, 8, 1.0, P, P, small, None)
+    assert all(misaligned(sp.lib.embedding_bwd, emb, i, off) for i in (1, 9))
+    assert misaligned(sp.lib.embedding_bwd, emb, 3, 2)
+    norm = (dtype, 0, 2, 0, P, 8, P, 8, P, 8, P, P, P, 1e-6, 3, 8, P, P, None)
+    assert all(misaligned(sp.lib.block_norm_fwd, norm, i, off) for i in (4, 6, 8, 16, 17))
+    assert all(misaligned(sp.lib.block_norm_fwd, norm, i, 2) for i in (10, 11, 12))
+    norm = (dtype, 0, 2, 0, P, 8, P, 8, P, 8, P, 8, P, 8, P, P, P, 1e-6, 3, 8, P, P, P, P, P, P, P, small, None)
+    assert all(misaligned(sp.lib.block_norm_bwd, norm, i, off) for i in (4, 6, 8, 10, 12, 20, 21, 22))
+    assert all(misaligned(sp.lib.block_norm_bwd, norm, i, 2) for i in (14, 15, 16, 23, 24, 25))
+    ffn = (dtype, 0, P, 8, P, P, P, 3, 8, 16, 8, P, 8, P, small, None)
+    assert all(misaligned(sp.lib.gated_ffn_fwd, ffn, i, off) for i in (2, 4, 5, 6, 11))
+    ffn = (dtype, 0, P, 8, P, P, P, P, 8, 3, 8, 16, 8, P, P, P, P, P, small, None)
+    assert all(misaligned(sp.lib.gated_ffn_bwd, ffn, i, off) for i in (2, 4, 5, 6, 7, 13, 14, 15, 16))
