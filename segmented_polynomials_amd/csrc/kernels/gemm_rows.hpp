@@ -1,5 +1,5 @@
 // Products of a few rows with a weight matrix, out[m, o] = sum over k of
-// x[m, k] w[o, k] for m < 64: bound by reading the weights once.  A workgroup
+// x[m, k] w[o, k] for at most 64 rows: bound by reading the weights once.  A workgroup
 // takes 16 weight rows (paired: of both matrices) and its waves share out the
 // sum over k, 64 k at a time; weights and rows go from memory straight into
 // the matrix instructions' registers, with no staging and no barrier before
@@ -82,10 +82,26 @@ gemm_rows_kernel(RowsArgs g) {
     x[i] = static_cast<const T*>(g.x) + (m < g.m ? m : g.m - 1) * g.ldx;
   }
   v4f acc[W][M16];
+  // the small products of several planes are summed apart, as in gemm_tile
+  v4f small[P > 1 ? W : 1][P > 1 ? M16 : 1];
 #pragma unroll
   for (int j = 0; j < W; ++j)
 #pragma unroll
-    for (int i = 0; i < M16; ++i) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < M16; ++i) {
+      acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
+      if constexpr (P > 1) small[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+  auto add = [&](int j, int i, const u16x8(&pw)[P], const u16x8(&px)[P]) {
+    if constexpr (P == 1) {
+      acc[j][i] = mma16(typename Dt::E{}, pw[0], px[0], acc[j][i]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 6; ++t) {
+        v4f& c = t < 5 ? small[j][i] : acc[j][i];
+        c = mma16(typename Dt::E{}, pw[kPairs3[t][1]], px[kPairs3[t][0]], c);
+      }
+    }
+  };
 #pragma unroll(P == 1 && M16 == 1 ? 4 : 2)
   for (int k0 = wave * 64; k0 < k; k0 += waves * 64) {
     RowChunk<Dt> rw[2][W], rx[2][M16];
@@ -100,20 +116,26 @@ gemm_rows_kernel(RowsArgs g) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int c = k0 + h * 32 + lane / 16 * 8;
-      u16x8 pw[W][P];
-#pragma unroll
-      for (int j = 0; j < W; ++j) rw[h][j].planes(c, k, pw[j]);
-#pragma unroll
-      for (int i = 0; i < M16; ++i) {
+      if constexpr (M16 == 1) {  // one weight's planes at a time: sixteen waves have 128 registers each
         u16x8 px[P];
-        rx[h][i].planes(c, k, px);
-        constexpr int kProducts = P == 1 ? 1 : 6;
+        rx[h][0].planes(c, k, px);
 #pragma unroll
-        for (int t = 0; t < kProducts; ++t)
+        for (int j = 0; j < W; ++j) {
+          u16x8 pw[P];
+          rw[h][j].planes(c, k, pw);
+          add(j, 0, pw, px);
+        }
+      } else {
+        u16x8 pw[W][P];
 #pragma unroll
-          for (int j = 0; j < W; ++j)
-            acc[j][i] = mma16(typename Dt::E{}, pw[j][P == 1 ? 0 : kPairs3[t][1]], px[P == 1 ? 0 : kPairs3[t][0]],
-                              acc[j][i]);
+        for (int j = 0; j < W; ++j) rw[h][j].planes(c, k, pw[j]);
+#pragma unroll
+        for (int i = 0; i < M16; ++i) {
+          u16x8 px[P];
+          rx[h][i].planes(c, k, px);
+#pragma unroll
+          for (int j = 0; j < W; ++j) add(j, i, pw[j], px);
+        }
       }
     }
   }
@@ -122,7 +144,10 @@ gemm_rows_kernel(RowsArgs g) {
   for (int i = 0; i < M16; ++i) {
     if (i) __syncthreads();
 #pragma unroll
-    for (int j = 0; j < W; ++j) sums[wave][j][lane] = acc[j][i];
+    for (int j = 0; j < W; ++j) {
+      if constexpr (P > 1) acc[j][i] += small[j][i];
+      sums[wave][j][lane] = acc[j][i];
+    }
     __syncthreads();
     if (threadIdx.x < 256) {
       const int l = threadIdx.x / 16 + threadIdx.x % 16 / 4 * 16, q = threadIdx.x % 4;
