@@ -803,8 +803,8 @@ int gated_ffn_workspace(int dtype, int64_t n, int64_t d_in, int64_t hidden, int6
  * Widths and, of more than one row, row strides are at most 2^21
  * (E_UNSUPPORTED, E_INVALID above).
  * Products on the matrix cores with float32 sums; the hidden rows are held
- * in T between the two products (float32 in 24 bits).  A float32 infinity
- * gives NaN where the product of its planes meets a zero.
+ * in T between the two products (float32 in 24 bits).  Infinities and NaN
+ * go through as the formula has them.
  */
 int gated_ffn_fwd(int dtype, int act, const void* x, int64_t x_stride, const void* w_gate, const void* w_up,
                   const void* w_down, int64_t n, int64_t d_in, int64_t hidden, int64_t d_out, void* out,

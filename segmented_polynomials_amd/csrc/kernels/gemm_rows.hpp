@@ -145,7 +145,7 @@ gemm_rows_kernel(RowsArgs g) {
     if (i) __syncthreads();
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      if constexpr (P > 1) acc[j][i] += small[j][i];
+      if constexpr (P > 1) acc[j][i] = add_small(acc[j][i], small[j][i]);
       sums[wave][j][lane] = acc[j][i];
     }
     __syncthreads();

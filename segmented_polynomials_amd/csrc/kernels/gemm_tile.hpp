@@ -96,6 +96,17 @@ __device__ __forceinline__ void split3(float x, bf16 (&p)[3]) {
   p[2] = static_cast<bf16>(r);
 }
 
+// The sum of the large products of planes and of the small ones.  An infinite
+// or NaN operand is in a first plane, whose large products carry it; in the
+// small ones it meets the zeros and either signs of other planes, which make
+// NaN of an infinity, so they do not count then.
+__device__ __forceinline__ v4f add_small(v4f large, v4f small) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (__builtin_fabsf(large[q]) < __builtin_inff()) large[q] += small[q];
+  return large;
+}
+
 // The normal distribution function: half the complementary error function of
 // |g| / sqrt(2), by the Chebyshev fit t exp(-x^2 + p(t)), t = 1 / (1 + x / 2), of
 // Press et al., Numerical Recipes, whose relative error is below 1.2e-7 on the
@@ -449,7 +460,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) acc[i][j] += small[i][j];
+      for (int j = 0; j < FN; ++j) acc[i][j] = add_small(acc[i][j], small[i][j]);
   }
 
   // ---------------------------------------------------------- epilogue

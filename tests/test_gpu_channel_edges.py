@@ -108,3 +108,120 @@ def test_gated_ffn_few_rows_as_accurate_as_many(di, F, do):
                  for t in (sp.gated_ffn_fwd(x[:64], wg, wu, wd), sp.gated_ffn_fwd(x, wg, wu, wd)))
     print(f"[parity] rms error: few rows {few:.3e}, many {many:.3e}", flush=True)
     assert few <= 1.25 * many
+
+
+def same_kind(got, ref, what):
+    """Infinite where the reference is, of its sign, NaN where it is, else finite."""
+    ref = ref.to(got.dtype)
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)), f"{what}: NaN"
+    inf = torch.isinf(ref)
+    assert torch.equal(torch.isinf(got), inf) and torch.equal(got[inf], ref[inf]), f"{what}: infinities"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("act", ["relu", "sigmoid"])
+@pytest.mark.parametrize("n,di,F,do", [(5, 40, 72, 24), (64, 64, 136, 48), (90, 33, 70, 31), (700, 256, 520, 256)])
+def test_gated_ffn_infinities_and_nan(n, di, F, do, act, dtype):
+    """An infinity and a NaN in x, in w_down and in grad_out: what they reach is
+    infinite or NaN as the formula has it, everything else as without them."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"gated ffn, infinities and NaN, n={n} {di} x {F} x {do} {act} {dtype}")
+    x, wg, wu, wd, gy = ffn_case(n, di, F, do, dtype, n + 1)
+    inf, nan = float("inf"), float("nan")
+
+    def forward(x, wd):
+        X, G, U, D = (t.double() for t in (x, wg, wu, wd))
+        return (act64(X @ G.T, act)[0] * (X @ U.T)) @ D.T
+
+    plain = sp.gated_ffn_fwd(x, wg, wu, wd, act=act)
+    bad = x.clone()
+    bad[1, 3], bad[2, 4], bad[n - 1, di - 1] = inf, nan, -inf
+    out = sp.gated_ffn_fwd(bad, wg, wu, wd, act=act)
+    same_kind(out, forward(bad, wd), "out of x")
+    keep = torch.ones(n, dtype=torch.bool)
+    keep[[1, 2, n - 1]] = False
+    assert torch.equal(out[keep], plain[keep])
+    badw = wd.clone()
+    badw[2, 5], badw[do - 1, 0] = inf, nan
+    out = sp.gated_ffn_fwd(x, wg, wu, badw, act=act)
+    # relu's zero times an infinity is NaN; the sign of a value that is nearly zero is not asked for
+    h = act64(x.double() @ wg.double().T, act)[0][:, 5] * (x.double() @ wu.double().T)[:, 5]
+    clear = (h == 0) | (h.abs() > 1e-3)
+    same_kind(out[clear], forward(x, badw)[clear], "out of w_down")
+    keep = torch.ones(do, dtype=torch.bool)
+    keep[[2, do - 1]] = False
+    assert torch.equal(out[:, keep], plain[:, keep])
+    # grad_out: one row of grad_x, one row of grad_w_down
+    full = sp.gated_ffn_bwd(x, wg, wu, wd, gy, act=act)
+    badg = gy.clone()
+    badg[3, 7] = inf
+    got = sp.gated_ffn_bwd(x, wg, wu, wd, badg, act=act)
+    keep = torch.ones(n, dtype=torch.bool)
+    keep[3] = False
+    assert torch.equal(got[0][keep], full[0][keep]) and not torch.isfinite(got[0][3]).any()
+    h = act64(x.double() @ wg.double().T, act)[0][3] * (x.double() @ wu.double().T)[3]
+    clear = (h == 0) | (h.abs() > 1e-3)
+    same_kind(got[3][7][clear], (inf * h)[clear], "grad_w_down")
+    keep = torch.ones(do, dtype=torch.bool)
+    keep[7] = False
+    assert torch.equal(got[3][keep], full[3][keep])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_embedding_infinities_and_nan(dtype):
+    """Of tokens out of range they reach nothing, of others their column only."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"embedding, infinities and NaN {dtype}")
+    g = gen(8)
+    for n, rows, dim in ((700, 10, 33), (700, 300, 40), (40000, 5000, 24)):
+        tok = torch.randint(0, rows, (n,), generator=g, device="cuda", dtype=torch.int32)
+        grad = rnd(g, n, dim, dtype=dtype)
+        tok[5], tok[6] = -1, rows
+        full = sp.embedding_bwd(grad, tok, rows)
+        grad[5], grad[6, 2], grad[n - 1, 3], grad[8, 4] = float("nan"), float("inf"), float("inf"), float("nan")
+        got = sp.embedding_bwd(grad, tok, rows)
+        want = full.clone()
+        want[tok[n - 1].long(), 3], want[tok[8].long(), 4] = float("inf"), float("nan")
+        assert torch.equal(got.nan_to_num(7.0, 9.0, 11.0), want.nan_to_num(7.0, 9.0, 11.0))
+        table = rnd(g, rows, dim, dtype=dtype)
+        table[tok[0].long(), 1] = float("-inf")
+        out = sp.embedding_fwd(table, tok)
+        at = tok.long().clamp(0, rows - 1)
+        ok = (tok >= 0) & (tok < rows)
+        assert torch.equal(out, torch.where(ok[:, None], table[at], torch.zeros_like(table[at])))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,dim,kind", [(37, 64, "layer"), (9, 1000, "rms"), (5, 8192, "layer")])
+def test_block_norm_infinities_and_nan(n, dim, kind, dtype):
+    """A row with an infinity or a NaN spoils itself and the column sums, and
+    no other row; the sums stay whole in the columns of a finite row's NaN gate."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"block norm, infinities and NaN, n={n} dim={dim} {kind} {dtype}")
+    g = gen(n)
+    x, f, gy, gh = (rnd(g, n, dim, dtype=dtype) for _ in range(4))
+    gt = rnd(g, n, dim, dtype=dtype)
+    w = 1 + rnd(g, dim, std=0.1)
+    kw = dict(w_post=w, res_scale=w, w_pre=w, kind=kind)
+    y0, h0 = sp.block_norm_fwd(x, f, gate=gt, **kw)
+    b0 = sp.block_norm_bwd(y0, gy, gh, f, gate=gt, **kw)
+    keep = torch.ones(n, dtype=torch.bool)
+    keep[[1, n - 1]] = False
+    bad = f.clone()
+    bad[1, 3], bad[n - 1, dim - 1] = float("inf"), float("nan")
+    y, h = sp.block_norm_fwd(x, bad, gate=gt, **kw)
+    assert torch.equal(y[keep], y0[keep]) and torch.equal(h[keep], h0[keep])
+    assert not torch.isfinite(y[n - 1]).any() and not torch.isfinite(y[1, 3])
+    got = sp.block_norm_bwd(y0, gy, gh, bad, gate=gt, **kw)
+    assert torch.equal(got[0], b0[0]) and all(torch.equal(p[keep], q[keep]) for p, q in zip(got[:3], b0[:3]))
+    badg = gt.clone()
+    badg[1, 3] = float("nan")
+    got = sp.block_norm_bwd(y0, gy, gh, f, gate=badg, **kw)
+    cols = torch.ones(dim, dtype=torch.bool)
+    cols[3] = False
+    for p, q in zip(got[3:5], b0[3:5]):
+        assert torch.equal(p[cols], q[cols]) and torch.isnan(p[3])
+    assert torch.equal(got[5], b0[5]) and torch.equal(got[0], b0[0])
