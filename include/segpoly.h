@@ -803,8 +803,9 @@ int gated_ffn_workspace(int dtype, int64_t n, int64_t d_in, int64_t hidden, int6
  * Widths and, of more than one row, row strides are at most 2^21
  * (E_UNSUPPORTED, E_INVALID above).
  * Products on the matrix cores with float32 sums; the hidden rows are held
- * in T between the two products (float32 in 24 bits).  Infinities and NaN
- * go through as the formula has them.
+ * in T's precision between the two products (float32: 24 bits, float16: with a
+ * power of two for blocks of them that its range does not hold).  Infinities
+ * and NaN go through as the formula has them.
  */
 int gated_ffn_fwd(int dtype, int act, const void* x, int64_t x_stride, const void* w_gate, const void* w_up,
                   const void* w_down, int64_t n, int64_t d_in, int64_t hidden, int64_t d_out, void* out,
@@ -812,7 +813,8 @@ int gated_ffn_fwd(int dtype, int act, const void* x, int64_t x_stride, const voi
 
 /*
  * gated_ffn_bwd: vector-Jacobian product of gated_ffn_fwd for grad_out
- * [n, d_out]; the hidden rows are computed again.  grad_x [n, d_in] or NULL;
+ * [n, d_out]; the hidden rows are computed again, and they and their gradients
+ * held as in the forward.  grad_x [n, d_in] or NULL;
  * the three weight gradients, shaped as the weights, or all NULL.  With
  * n == 0 the weight gradients are zero, and no input or workspace is read
  * (all may be NULL).

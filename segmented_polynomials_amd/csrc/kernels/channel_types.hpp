@@ -150,6 +150,28 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
+// The largest over aligned groups of W = 16 or 64 lanes, in every lane.
+template <int Ctrl>
+__device__ __forceinline__ float dpp_max(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), Ctrl, 0xf, 0xf, true);
+  return __builtin_fmaxf(v, __builtin_bit_cast(float, o));
+}
+// over the lanes l, l ^ 16, l ^ 32 and l ^ 48
+__device__ __forceinline__ float max_over_rows(float v) {
+  float w = v;
+  asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(v), "+v"(w));
+  v = __builtin_fmaxf(v, w);
+  w = v;
+  asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(v), "+v"(w));
+  return __builtin_fmaxf(v, w);
+}
+template <int W>
+__device__ __forceinline__ float lane_max(float v) {
+  v = dpp_max<0x140>(dpp_max<0x141>(dpp_max<0x4e>(dpp_max<0xb1>(v))));
+  if constexpr (W == 64) v = max_over_rows(v);
+  return v;
+}
+
 // 1 / (1 + e^-v); the reciprocal is the hardware's, within one unit of the last place
 __device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
 

@@ -10,9 +10,16 @@
 // Between the products h, dg and du are held in the operands' type: they are
 // operands of matrix instructions, each rounding is at most a relative 2^-8
 // (bf16) or 2^-11 (f16) of one term of a long sum, the size of the inputs' own
-// rounding.  float32 keeps them as three bf16 planes (24 bits).  dh is no
-// operand and stays float32: rounded as well, it would add half again to the
-// error of dx, dWg and dWu.
+// rounding; outputs are off by about 1.4 times what their one rounding alone
+// would leave.  As two planes they would cost every product of theirs a second
+// matrix instruction, a third more of a forward's and five eighths more of a
+// backward's (few rows, measured: 13.5 -> 15 us for 3 rows, 34 -> 49 us for 64, of
+// 1024 x 4096 x 1024 bf16).  float16's range does not hold what lies between
+// inputs and results, so it holds them in scaled blocks (gemm_tile.hpp,
+// gemm_rows.hpp); that costs 2 % of large calls and 1 to 4 us of small ones
+// (8192 x 2048 x 5632 backward 1505 -> 1530 us, 100 x 1024 x 4096 x 1024 48.7 -> 52.7).
+// float32 keeps three bf16 planes (24 bits).  dh is no operand and stays float32: rounded as
+// well, it would add half again to the error of dx, dWg and dWu.
 #pragma once
 #include <algorithm>
 #include <cmath>
@@ -29,6 +36,8 @@ namespace kern {
 struct Operand {
   const uint16_t* plane[3];
   int64_t ld;
+  int* exponents = nullptr;  // of scaled blocks of 64 rows and 32 columns
+  int64_t exponents_ld = 0;
 };
 
 constexpr int kMaxPack = 5;
@@ -84,6 +93,9 @@ void add_phase(GemmArgs& g, int& at, const Operand& a, const Operand& b, const O
     g.b[i] = b.plane[p];
     if (b2) g.b2[i] = b2->plane[p];
   }
+  g.ea[at] = a.exponents;
+  g.eb[at] = b.exponents;
+  g.e_ld = std::max(a.exponents_ld, b.exponents_ld);
   ++at;
 }
 
@@ -302,6 +314,10 @@ struct FfnPlan {
     uint16_t* p = arena.take<uint16_t>(P * n * o.ld);
     if (p)
       for (int k = 0; k < P; ++k) o.plane[k] = p + k * n * o.ld;
+    if constexpr (Dt::kScaled) {
+      o.exponents_ld = (hidden + 31) / 32;
+      o.exponents = arena.take<int>((n + 63) / 64 * o.exponents_ld);
+    }
     return o;
   }
   int run_pack(hipStream_t st) {
@@ -340,6 +356,7 @@ GemmArgs paired_product(const GatedFfnArgs& a, const Operand& x, const Operand& 
   add_phase<Dt>(g, g.phases, x, wg, &wu);
   g.batch = 1, g.m[0] = a.n, g.n[0] = a.hidden, g.k = a.d_in, g.lda[0] = x.ld, g.ldb[0] = wg.ld;
   g.h = const_cast<uint16_t*>(h.plane[0]), g.ldh = h.ld, g.plane_stride = a.n * h.ld, g.act = a.act;
+  g.e_h = h.exponents, g.e_ld = h.exponents_ld;
   return g;
 }
 
@@ -351,12 +368,22 @@ int ffn_fwd(const GatedFfnArgs& a, size_t* bytes) {
     Arena arena{static_cast<char*>(a.workspace)};
     const int64_t ldh = round_up(a.hidden, 8);
     void* h = arena.take<typename Dt::T>(a.n * ldh);
+    int8_t* e = nullptr;
+    uint32_t* odd = nullptr;
+    if constexpr (Dt::kScaled) {
+      const int64_t groups = (a.hidden + 15) / 16;
+      e = arena.take<int8_t>(a.n * groups);
+      odd = arena.take<uint32_t>(round_up(groups, 4));
+    }
     if (worst) {
       *bytes = arena.at;
       return 0;
     }
-    const int rc = gemm_rows<Dt, true>({a.x, a.w_gate, a.w_up, h, a.n, a.hidden, a.d_in, a.x_stride, ldh, a.act}, st);
-    return rc ? rc : gemm_rows<Dt, false>({h, a.w_down, nullptr, a.out, a.n, a.d_out, a.hidden, ldh, a.out_stride, 0}, st);
+    const int rc =
+        gemm_rows<Dt, true>({a.x, a.w_gate, a.w_up, h, e, odd, a.n, a.hidden, a.d_in, a.x_stride, ldh, a.act}, st);
+    return rc ? rc
+              : gemm_rows<Dt, false>({h, a.w_down, nullptr, a.out, e, odd, a.n, a.d_out, a.hidden, ldh, a.out_stride, 0},
+                                     st);
   }
   FfnPlan<Dt> plan(a.workspace);
   const Operand x = plan.use(a.x, a.n, a.d_in, a.x_stride, worst);
@@ -393,6 +420,7 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
   float* dh = plan.arena.template take<float>(a.n * h.ld);
   GemmArgs first = product<Dt>(a.n, a.hidden, a.d_out, go, wd, dh, h.ld);
   GemmArgs pair = paired_product<Dt>(a, x, wg, wu, h);
+  pair.e_dg = dg.exponents, pair.e_du = du.exponents;
   pair.dg = const_cast<uint16_t*>(dg.plane[0]), pair.du = const_cast<uint16_t*>(du.plane[0]), pair.dh = dh;
   GemmArgs dx = product<Dt>(a.n, a.d_in, a.hidden, dg, wg, a.gx, a.d_in);
   add_phase<Dt>(dx, dx.phases, du, wu);

@@ -8,6 +8,8 @@
 // waves of 4 KB each 64 workgroups already ask for the whole of 8 MB.  Loads
 // are of 16 bytes at any alignment, float32 is split into its planes in
 // registers: no operand is copied first.
+// float16 hidden rows go from the paired product to the second in scaled blocks
+// (gemm_tile.hpp), here of sixteen columns of one row.
 // One MI355X, 3 rows, 1024 x 4096 bf16: gate, up and down take 6 + 8 us, as tiles of
 // 64 x 64 (gemm_tile.hpp) 8 + 18 us.
 #pragma once
@@ -24,6 +26,8 @@ constexpr int64_t kFewRows = 64;
 struct RowsArgs {
   const void *x, *w, *w2;  // [m][k] with row stride ldx, [n][k] dense; w2 of a paired product
   void* out;               // [m][ldo]
+  int8_t* exponents;       // float16: of 16 columns of a hidden row, [m][hidden / 16]
+  uint32_t* odd;           // and whether any row's is not zero, [hidden / 16], a byte a wave
   int64_t m, n, k, ldx, ldo;
   int act;
 };
@@ -91,8 +95,30 @@ gemm_rows_kernel(RowsArgs g) {
       acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
       if constexpr (P > 1) small[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
     }
-  auto add = [&](int j, int i, const u16x8(&pw)[P], const u16x8(&px)[P]) {
-    if constexpr (P == 1) {
+  // float16: where any exponent is not zero the sum is made a second time, with
+  // them.  Row i's is then in units of the present ones (lane % 16 has it), as in
+  // gemm_tile, and the two sixteens of a step are added apart.
+  constexpr bool kUnits = Dt::kScaled && !Pair;
+  int unit[M16], top[M16];
+  const int groups = (k + 15) / 16;
+  u32x4 odd = {0, 0, 0, 0};
+  if constexpr (kUnits)
+    if (lane * 4 < groups) odd = *reinterpret_cast<const u32x4*>(g.odd + lane * 4);
+  auto add = [&](auto units, int j, int i, const u16x8(&pw)[P], const u16x8(&px)[P], int e) {
+    if constexpr (units) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const bool mine = lane / 32 == s;
+        const int es = static_cast<int>(max_over_rows(static_cast<float>(mine ? e : kNoValue)));
+        top[i] = es > top[i] ? es : top[i];
+        const int to = es == kNoValue ? unit[i] : es > top[i] - kReach ? es : top[i] - kReach;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[j][i][q] = __builtin_ldexpf(acc[j][i][q], unit[i] - to);
+        unit[i] = to;
+        const u16x8 part = es < to && es != kNoValue ? lower(px[0], es - to) : px[0];
+        acc[j][i] = mma16(typename Dt::E{}, mine ? pw[0] : u16x8{}, mine ? part : u16x8{}, acc[j][i]);
+      }
+    } else if constexpr (P == 1) {
       acc[j][i] = mma16(typename Dt::E{}, pw[0], px[0], acc[j][i]);
     } else {
 #pragma unroll
@@ -102,43 +128,73 @@ gemm_rows_kernel(RowsArgs g) {
       }
     }
   };
-#pragma unroll(P == 1 && M16 == 1 ? 4 : 2)
-  for (int k0 = wave * 64; k0 < k; k0 += waves * 64) {
-    RowChunk<Dt> rw[2][W], rx[2][M16];
+  auto run = [&](auto units) {
+    constexpr int kUnroll = units ? 1 : P == 1 && M16 == 1 ? 4 : 2;
+#pragma unroll(kUnroll)
+    for (int k0 = wave * 64; k0 < k; k0 += waves * 64) {
+      RowChunk<Dt> rw[2][W], rx[2][M16];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = k0 + h * 32 + lane / 16 * 8;
+      for (int h = 0; h < 2; ++h) {
+        const int c = k0 + h * 32 + lane / 16 * 8;
 #pragma unroll
-      for (int j = 0; j < W; ++j) rw[h][j].load(w[j], c, k);
+        for (int j = 0; j < W; ++j) rw[h][j].load(w[j], c, k);
 #pragma unroll
-      for (int i = 0; i < M16; ++i) rx[h][i].load(x[i], c, k);
-    }
+        for (int i = 0; i < M16; ++i) rx[h][i].load(x[i], c, k);
+      }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = k0 + h * 32 + lane / 16 * 8;
-      if constexpr (M16 == 1) {  // one weight's planes at a time: sixteen waves have 128 registers each
-        u16x8 px[P];
-        rx[h][0].planes(c, k, px);
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          u16x8 pw[P];
-          rw[h][j].planes(c, k, pw);
-          add(j, 0, pw, px);
-        }
-      } else {
-        u16x8 pw[W][P];
-#pragma unroll
-        for (int j = 0; j < W; ++j) rw[h][j].planes(c, k, pw[j]);
-#pragma unroll
-        for (int i = 0; i < M16; ++i) {
+      for (int h = 0; h < 2; ++h) {
+        const int c = k0 + h * 32 + lane / 16 * 8;
+        auto exponent = [&](int i) -> int {
+          if constexpr (units) {
+            const int64_t m = i * 16 + lane % 16;
+            return c < k ? g.exponents[(m < g.m ? m : g.m - 1) * groups + c / 16] : kNoValue;
+          }
+          return 0;
+        };
+        if constexpr (M16 == 1) {  // one weight's planes at a time: sixteen waves have 128 registers each
           u16x8 px[P];
-          rx[h][i].planes(c, k, px);
+          rx[h][0].planes(c, k, px);
 #pragma unroll
-          for (int j = 0; j < W; ++j) add(j, i, pw[j], px);
+          for (int j = 0; j < W; ++j) {
+            u16x8 pw[P];
+            rw[h][j].planes(c, k, pw);
+            add(units, j, 0, pw, px, exponent(0));
+          }
+        } else {
+          u16x8 pw[W][P];
+#pragma unroll
+          for (int j = 0; j < W; ++j) rw[h][j].planes(c, k, pw[j]);
+#pragma unroll
+          for (int i = 0; i < M16; ++i) {
+            u16x8 px[P];
+            rx[h][i].planes(c, k, px);
+#pragma unroll
+            for (int j = 0; j < W; ++j) add(units, j, i, pw[j], px, exponent(i));
+          }
         }
       }
     }
+  };
+  run(std::false_type{});
+  if constexpr (kUnits) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) any |= lane * 4 + q < groups ? odd[q] : 0;
+    for (int t = 256 + lane; t < groups; t += 64) any |= g.odd[t];
+    if (__ballot(any != 0)) {
+#pragma unroll
+      for (int i = 0; i < M16; ++i) {
+        acc[0][i] = v4f{0.f, 0.f, 0.f, 0.f};
+        unit[i] = top[i] = kNoValue;
+      }
+      run(std::true_type{});
+#pragma unroll
+      for (int i = 0; i < M16; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[0][i][q] = __builtin_ldexpf(acc[0][i][q], unit[i]);
+    }
   }
+  bool not_zero = false;  // an exponent of this thread's
   // lane l of a fragment holds weight rows l / 16 * 4 + q of row l % 16
 #pragma unroll
   for (int i = 0; i < M16; ++i) {
@@ -158,10 +214,22 @@ gemm_rows_kernel(RowsArgs g) {
         for (int s = 0; s < waves; ++s) v[j] += sums[s][j][l][q];
       }
       const int64_t m = i * 16 + l % 16, n = static_cast<int64_t>(blockIdx.x) * 16 + l / 16 * 4 + q;
+      if constexpr (Pair) v[0] = act_value(v[0], g.act) * v[1];
+      if constexpr (Pair && Dt::kScaled) {  // sixteen lanes have a row's sixteen columns
+        const int e = block_exponent(lane_max<16>(finite_abs(v[0])));
+        v[0] *= block_scale(e);
+        not_zero |= e != 0 && e != kNoValue;
+        if (m < g.m && l / 16 + q == 0) g.exponents[m * ((g.n + 15) / 16) + blockIdx.x] = static_cast<int8_t>(e);
+      }
       if (m < g.m && n < g.n) {
-        if constexpr (Pair) v[0] = act_value(v[0], g.act) * v[1];
         static_cast<T*>(g.out)[m * g.ldo + n] = static_cast<T>(v[0]);
       }
+    }
+  }
+  if constexpr (Pair && Dt::kScaled) {
+    if (threadIdx.x < 256) {
+      const bool any = __ballot(not_zero) != 0;
+      if (lane == 0) reinterpret_cast<uint8_t*>(g.odd + blockIdx.x)[wave] = any;
     }
   }
 }

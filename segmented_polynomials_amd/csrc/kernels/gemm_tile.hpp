@@ -55,14 +55,43 @@ struct GemmArgs {
   const float* dh;        // [m][ldh]
   int64_t ldh, plane_stride;
   int act;
+  // float16: exponents of blocks (scaled, below), [m / 64][e_ld] by n / 32; the
+  // paired product's outputs, and of A and B at [z * phases + p], null: not scaled
+  int *e_h, *e_dg, *e_du;
+  const int *ea[kMaxBatch], *eb[kMaxBatch];
+  int64_t e_ld;
 };
 
 enum { kEpiStore = 0, kEpiStoreF32 = 1, kEpiGated = 2, kEpiGatedBwd = 3 };
 
-// io type T, matrix type E, planes per operand
-struct DtBF16 { using T = bf16; using E = bf16; static constexpr int kPlanes = 1; };
-struct DtF16 { using T = f16; using E = f16; static constexpr int kPlanes = 1; };
-struct DtF32 { using T = float; using E = bf16; static constexpr int kPlanes = 3; };
+// io type T, matrix type E, planes per operand, products held in scaled blocks
+struct DtBF16 { using T = bf16; using E = bf16; static constexpr int kPlanes = 1; static constexpr bool kScaled = false; };
+struct DtF16 { using T = f16; using E = f16; static constexpr int kPlanes = 1; static constexpr bool kScaled = true; };
+struct DtF32 { using T = float; using E = bf16; static constexpr int kPlanes = 3; static constexpr bool kScaled = false; };
+
+// float16 reaches from 2^-24 to 2^16.  A value that is held in it between two
+// products can pass both ends where the inputs and the result do not, so its
+// block is held times 2^-E: E = 0 while the block's largest finite value is
+// between 2^-9 and 2^15, else a multiple of 8 that brings it between 2^7 and
+// 2^15.  What a block's small values lose is then below 2^-16 of its largest, a
+// sixteenth of what the largest loses in its own rounding.
+constexpr int kReach = 64;      // below the largest exponent of a sum, values no longer count
+constexpr int kNoValue = -128;  // the exponent of a block of zeros, infinities and NaN
+__device__ __forceinline__ int block_exponent(float largest) {
+  if (largest == 0.f) return kNoValue;
+  const int e = static_cast<int>(__builtin_bit_cast(uint32_t, largest) >> 23) - 127;
+  if (e >= -9 && e <= 14) return 0;
+  const int scaled = (e - 14 + 7) >> 3 << 3;
+  return scaled > -112 ? scaled : -112;
+}
+__device__ __forceinline__ float power_of_two(int e) {  // -126 .. 127
+  return __builtin_bit_cast(float, (127 + e) << 23);
+}
+__device__ __forceinline__ float block_scale(int e) { return e == kNoValue ? 1.f : power_of_two(-e); }
+__device__ __forceinline__ float finite_abs(float v) {
+  v = __builtin_fabsf(v);
+  return v < __builtin_inff() ? v : 0.f;
+}
 
 // Plane pairs of a float32 product, the smallest first.
 constexpr int kPairs3[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
@@ -151,6 +180,15 @@ __device__ __forceinline__ void act_both(float g, int act, float& a, float& da) 
     a = sigmoid(g);
     da = a * (1.f - a);
   }
+}
+
+// a fragment times 2^d, d <= 0: in two steps, for one that takes all of float16's
+// values to zero is itself below it, and would make NaN of an infinity
+__device__ __forceinline__ u16x8 lower(u16x8 v, int d) {
+  using F8 = f16 __attribute__((ext_vector_type(8)));
+  const int d1 = d > -24 ? d : -24, d2 = d - d1 > -24 ? d - d1 : -24;
+  const F8 f = __builtin_bit_cast(F8, v) * static_cast<f16>(power_of_two(d1));
+  return __builtin_bit_cast(u16x8, f * static_cast<f16>(power_of_two(d2)));
 }
 
 // ------------------------------------------------------------ operand tiles
@@ -382,6 +420,95 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
       if constexpr (P > 1) small[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
     }
 
+  // Scaled blocks of this wave's rows of A, or B: a group of fragments per block
+  // across the sum.  A group's sum is in units of its present block's exponent
+  // and changes them with it (but not by more than kReach from the largest, for
+  // float32's range).  Ordinary values have exponents of zero everywhere, which
+  // one look over them before the first step shows, while its loads are on their
+  // way.
+  constexpr int GA = (BM / WM) / (AAcross ? 32 : 64) > 1 ? (BM / WM) / (AAcross ? 32 : 64) : 1;
+  constexpr int GB = BN / WN / 32 > 1 ? BN / WN / 32 : 1;
+  constexpr bool kScaledB = AAcross && BAcross;  // the other products' B is a weight
+  int unit_a[GA] = {}, unit_b[GB] = {}, least_a[GA] = {}, least_b[GB] = {};
+  bool mixed = false, in_units = false;
+  int64_t now = s0;  // the step that compute works on
+  // exponents of one group along the sum: first, distance and number; the last
+  // step's second half can be past the last, and a group past the last row (not
+  // stored) has the last one's
+  struct Along {
+    const int* e;
+    int64_t step;
+    int count;
+    __device__ __forceinline__ int at(int t) const { return e[(t < count ? t : count - 1) * step]; }
+  };
+  auto along = [&](const int* e, int64_t r, int64_t rows, bool across) {
+    r = r < rows ? r : rows - 1;
+    return across ? Along{e + r / 32, g.e_ld, static_cast<int>((g.k + 63) / 64)}
+                  : Along{e + r / 64 * g.e_ld, 1, static_cast<int>((g.k + 31) / 32)};
+  };
+  auto along_a = [&](int p, int q) {
+    return along(g.ea[z * g.phases + p], m0 + wm * (BM / WM) + q * (AAcross ? 32 : 64), gm, AAcross);
+  };
+  auto along_b = [&](int p, int q) {
+    return along(g.eb[z * g.phases + p], n0 + wn * (BN / WN) + q * 32, gn, true);
+  };
+  // the first look: 256 exponents of each group and phase (one or two), loaded
+  // before the first step's operands and waited for after them
+  int seen_a[2][GA][4] = {}, seen_b[2][GB][4] = {};
+  auto load_seen = [&](auto&& group, auto& seen) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int q = 0; q < static_cast<int>(sizeof(seen[0]) / 16); ++q)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) seen[p][q][u] = group(p < g.phases ? p : 0, q).at(u * 64 + lane);
+  };
+  auto look = [&](auto&& group, auto& seen, auto& unit, auto& least) {
+    constexpr int G = sizeof(unit) / sizeof(int);
+    bool other = false;
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int q = 0; q < G; ++q)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) other |= seen[p][q][u] != 0 && seen[p][q][u] != kNoValue;
+    for (int p = 0; p < g.phases; ++p)
+      for (int t = 256 + lane; t < group(p, 0).count; t += 64)
+#pragma unroll
+        for (int q = 0; q < G; ++q) {
+          const int e = group(p, q).at(t);
+          other |= e != 0 && e != kNoValue;
+        }
+    if (__ballot(other) == 0) return;
+#pragma unroll
+    for (int q = 0; q < G; ++q) {
+      float hi = kNoValue, lo = -kNoValue;
+      for (int p = 0; p < g.phases; ++p)
+        for (int t = lane; t < group(p, q).count; t += 64) {
+          const int e = group(p, q).at(t);
+          if (e == kNoValue) continue;
+          hi = __builtin_fmaxf(hi, static_cast<float>(e));
+          lo = __builtin_fminf(lo, static_cast<float>(e));
+        }
+      const int top = __builtin_amdgcn_readfirstlane(static_cast<int>(lane_max<64>(hi + 128.f))) - 128;
+      const int low = 128 - __builtin_amdgcn_readfirstlane(static_cast<int>(lane_max<64>(128.f - lo)));
+      if (top == kNoValue) continue;
+      unit[q] = top;
+      least[q] = top - kReach;
+      mixed |= low != top;
+      in_units |= mixed || top != 0;
+    }
+  };
+  // exponent e comes next in a group: its sum changes units, or its fragments are
+  // lowered to them where the exponent is out of reach
+  auto enter = [&](int e, int& unit, int least, auto&& sums, auto&& fragments) {
+    if (e == kNoValue) return;
+    const int to = e > least ? e : least;
+    if (to != unit) sums(power_of_two(unit - to));
+    unit = to;
+    if (e < to) fragments(e - to);
+  };
+
   // paired: the wave's first FN/2 fragments are of B, the others of B2
   auto b_row = [&](int j) {
     if constexpr (kPair)
@@ -389,7 +516,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
     else
       return wn * (BN / WN) + j * 16;
   };
-  auto compute = [&](const uint16_t* at_a, const uint16_t* at_b) {
+  auto compute = [&](auto units, const uint16_t* at_a, const uint16_t* at_b) {
 #pragma unroll
     for (int kk = 0; kk < KS / 32; ++kk) {
       // the transposing reads of two halves at once do not fit in the registers beside a large tile
@@ -403,6 +530,41 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
 #pragma unroll
         for (int i = 0; i < FM; ++i)
           fa[q][i] = read_fragment<BM, KS, AAcross>(at_a + q * BM * KS, wm * (BM / WM) + i * 16, kk, lane);
+      }
+      if constexpr (units) {
+        const int p = static_cast<int>(now / steps);
+        const int at = static_cast<int>(now % steps) * KS + kk * 32;
+        constexpr int NA = FM / GA, NB = FN / GB;
+#pragma unroll
+        for (int q = 0; q < GA; ++q) {
+          if (!g.ea[z * g.phases]) continue;
+          auto sums = [&](float f) {
+#pragma unroll
+            for (int i = q * NA; i < (q + 1) * NA; ++i)
+#pragma unroll
+              for (int j = 0; j < FN; ++j) acc[i][j] *= f;
+          };
+          auto fragments = [&](int d) {
+#pragma unroll
+            for (int i = q * NA; i < (q + 1) * NA; ++i) fa[0][i] = lower(fa[0][i], d);
+          };
+          enter(along_a(p, q).at(at / (AAcross ? 64 : 32)), unit_a[q], least_a[q], sums, fragments);
+        }
+#pragma unroll
+        for (int q = 0; q < (kScaledB ? GB : 0); ++q) {
+          if (!g.eb[z * g.phases]) continue;
+          auto sums = [&](float f) {
+#pragma unroll
+            for (int j = q * NB; j < (q + 1) * NB; ++j)
+#pragma unroll
+              for (int i = 0; i < FM; ++i) acc[i][j] *= f;
+          };
+          auto fragments = [&](int d) {
+#pragma unroll
+            for (int j = q * NB; j < (q + 1) * NB; ++j) fb[0][j] = lower(fb[0][j], d);
+          };
+          enter(along_b(p, q).at(at / 64), unit_b[q], least_b[q], sums, fragments);
+        }
       }
       constexpr int kProducts = P == 1 ? 1 : 6;
 #pragma unroll
@@ -424,36 +586,56 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
   constexpr int kLoads = P * (la.kInstr + lb.kInstr);  // of a wave in a step
   // One step: its own loads have landed (those of the S - 2 steps after it may
   // not have) and the buffer read a step ago is free for the one S - 1 ahead.
-  auto step = [&](uint16_t* now_a, uint16_t* now_b, uint16_t* ahead_a, uint16_t* ahead_b) {
+  auto step = [&](auto units, uint16_t* now_a, uint16_t* now_b, uint16_t* ahead_a, uint16_t* ahead_b) {
     wait_and_meet<(S - 2) * kLoads>();
     issue(ahead_a, ahead_b);
-    compute(now_a, now_b);
+    compute(units, now_a, now_b);
+    if constexpr (units) ++now;
   };
-  auto first = [&] {
+  auto first = [&](auto units) {
     if constexpr (S == 2)
-      step(a0, b0, a1, b1);
+      step(units, a0, b0, a1, b1);
     else if constexpr (S == 3)
-      step(a0, b0, a2, b2);
+      step(units, a0, b0, a2, b2);
     else
-      step(a0, b0, a3, b3);
+      step(units, a0, b0, a3, b3);
   };
+  // whole turns of the buffers, then what is left: a loop with exits between
+  // the steps would have the compiler wait for loads that are not due
+  auto run = [&](auto units) {
+    for (; left >= S; left -= S) {
+      first(units);
+      step(units, a1, b1, a0, b0);
+      if constexpr (S > 2) step(units, a2, b2, a1, b1);
+      if constexpr (S > 3) step(units, a3, b3, a2, b2);
+    }
+    if (left > 0) {
+      first(units);
+      if (S > 2 && left > 1) {
+        step(units, a1, b1, a0, b0);
+        if (S > 3 && left > 2) step(units, a2, b2, a1, b1);
+      }
+    }
+  };
+  if constexpr (Dt::kScaled && !kPair) {
+    if (g.ea[z * g.phases]) load_seen(along_a, seen_a);
+    if constexpr (kScaledB)
+      if (g.eb[z * g.phases]) load_seen(along_b, seen_b);
+  }
   issue(a0, b0);
   if constexpr (S > 2) issue(a1, b1);
   if constexpr (S > 3) issue(a2, b2);
-  // whole turns of the buffers, then what is left: a loop with exits between
-  // the steps would have the compiler wait for loads that are not due
-  for (; left >= S; left -= S) {
-    first();
-    step(a1, b1, a0, b0);
-    if constexpr (S > 2) step(a2, b2, a1, b1);
-    if constexpr (S > 3) step(a3, b3, a2, b2);
-  }
-  if (left > 0) {
-    first();
-    if (S > 2 && left > 1) {
-      step(a1, b1, a0, b0);
-      if (S > 3 && left > 2) step(a2, b2, a1, b1);
-    }
+  if constexpr (Dt::kScaled && !kPair) {
+    if (g.ea[z * g.phases]) look(along_a, seen_a, unit_a, least_a);
+    if constexpr (kScaledB)
+      if (g.eb[z * g.phases]) look(along_b, seen_b, unit_b, least_b);
+    // a loop of its own where units change: waves of a workgroup in either meet at the same barriers
+    if (mixed)
+      run(std::true_type{});
+    else
+      run(std::false_type{});
+  } else {
+    run(std::false_type{});
   }
   __builtin_amdgcn_s_waitcnt(0x0f70);  // no load into LDS outlives the workgroup
   if constexpr (P > 1) {
@@ -465,6 +647,15 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
 
   // ---------------------------------------------------------- epilogue
   if constexpr (!kPair) {
+    if constexpr (Dt::kScaled) {
+      if (in_units) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] *= power_of_two(unit_a[i / (FM / GA)]) * power_of_two(unit_b[j / (FN / GB)]);
+      }
+    }
     using T = std::conditional_t<Epi == kEpiStoreF32, float, typename Dt::T>;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -540,6 +731,82 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
       }
     };
     wait_and_meet<0>();  // every wave has read its last fragments
+    // dh of the wave's fragments
+    constexpr int kD = Epi == kEpiGatedBwd ? 1 : 0;
+    v4f d[kD ? FM : 1][kD ? FN / 2 : 1];
+    auto load_dh = [&](int i, int j) {
+      const int64_t m = m0 + row0 + i * 16, n = n0 + col0 + j * 16;
+      v4f v = {0.f, 0.f, 0.f, 0.f};
+      if (m < gm && n < width) __builtin_memcpy(&v, g.dh + m * g.ldh + n, sizeof(v));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = n + q < gn ? v[q] : 0.f;
+      return v;
+    };
+    // Scaled blocks: the exponents come of bounds of the block's largest values,
+    // |h| <= max |g| max |u|, |dg| <= 1.13 max |dh| max |u| (1.13 bounds every
+    // activation's derivative), |du| <= max |dh| max |g| (1 for |g| with a
+    // sigmoid), a few times the values themselves, which are not known before the
+    // activations are.
+    constexpr int kBlocks = BM / WM > 64 ? BM / WM / 64 : 1, kPer = FM / kBlocks;
+    float scale_h[kBlocks], scale_dg[kBlocks], scale_du[kBlocks];
+    if constexpr (Dt::kScaled) {
+      static_assert(BM == 64 ? BN == 64 : BM / WM % 64 == 0 && BN / 2 / WN == 32, "a wave holds whole blocks");
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        float top[3];
+        auto largest = [&](auto&& magnitude) {
+          top[0] = top[1] = top[2] = 0.f;
+#pragma unroll
+          for (int i = b * kPer; i < (b + 1) * kPer; ++i)
+#pragma unroll
+            for (int j = 0; j < FN / 2; ++j)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                top[0] = __builtin_fmaxf(top[0], magnitude(acc[i][j][q]));
+                top[1] = __builtin_fmaxf(top[1], magnitude(acc[i][j + FN / 2][q]));
+                if constexpr (kD) top[2] = __builtin_fmaxf(top[2], magnitude(d[i][j][q]));
+              }
+#pragma unroll
+          for (int t = 0; t < 2 + kD; ++t) top[t] = lane_max<64>(top[t]);
+        };
+        if constexpr (kD)
+#pragma unroll
+          for (int i = b * kPer; i < (b + 1) * kPer; ++i)
+#pragma unroll
+            for (int j = 0; j < FN / 2; ++j) d[i][j] = load_dh(i, j);
+        largest([](float v) { return __builtin_fabsf(v); });  // the largest passes over NaN
+        if (!(__builtin_fmaxf(top[0], __builtin_fmaxf(top[1], top[2])) < __builtin_inff()))
+          largest([](float v) { return finite_abs(v); });
+        if constexpr (BM == 64) {  // one block, the workgroup's
+          float* shared = reinterpret_cast<float*>(b0);
+          if (lane == 0)
+#pragma unroll
+            for (int t = 0; t < 3; ++t) shared[t * kWaves + wave] = top[t];
+          wait_and_meet<63>();
+#pragma unroll
+          for (int t = 0; t < 3; ++t)
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) top[t] = __builtin_fmaxf(top[t], shared[t * kWaves + w]);
+        }
+        const float value = g.act == kActSigmoid ? 1.f : top[0];
+        const int eh = block_exponent(value * top[1]), eg = block_exponent(1.13f * top[2] * top[1]),
+                  eu = block_exponent(top[2] * value);
+        scale_h[b] = block_scale(eh), scale_dg[b] = block_scale(eg), scale_du[b] = block_scale(eu);
+        const int64_t m = m0 + (BM == 64 ? 0 : wm * (BM / WM) + b * 64), n = n0 + (BM == 64 ? 0 : wn * 32);
+        if (m < gm && n < gn && (BM == 64 ? threadIdx.x == 0 : lane == 0)) {
+          const int64_t at = m / 64 * g.e_ld + n / 32;
+          g.e_h[at] = eh;
+          if constexpr (kD) g.e_dg[at] = eg, g.e_du[at] = eu;
+        }
+      }
+    }
+    // element v of fragment row i, of the values with these scales
+    auto held = [&](float v, const float(&scale)[kBlocks], int i) {
+      if constexpr (Dt::kScaled)
+        return v * scale[i / kPer];
+      else
+        return v;
+    };
     if constexpr (Epi == kEpiGated || P > 1) {
       v4f h[FM][FN / 2];
 #pragma unroll
@@ -550,25 +817,24 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
           for (int q = 0; q < 4; ++q) h[i][j][q] = act_value(acc[i][j][q], g.act) * acc[i][j + FN / 2][q];
 #pragma unroll
       for (int p = 0; p < P; ++p)
-        store(g.h + p * g.plane_stride, [&](int i, int j, int q) { return plane(h[i][j][q], p); });
+        store(g.h + p * g.plane_stride, [&](int i, int j, int q) { return plane(held(h[i][j][q], scale_h, i), p); });
     }
     if constexpr (Epi == kEpiGatedBwd) {
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN / 2; ++j) {
-          const int64_t m = m0 + row0 + i * 16, n = n0 + col0 + j * 16;
-          float d[4] = {0.f, 0.f, 0.f, 0.f}, h[4];
-          if (m < gm && n < width) __builtin_memcpy(d, g.dh + m * g.ldh + n, sizeof(d));
+          if constexpr (!Dt::kScaled) d[i][j] = load_dh(i, j);
+          float h[4];
           // the gradients replace the two products
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float u = acc[i][j + FN / 2][q], dh = n + q < gn ? d[q] : 0.f;
+            const float u = acc[i][j + FN / 2][q], dh = d[i][j][q];
             float v, dv;
             act_both(acc[i][j][q], g.act, v, dv);
-            h[q] = v * u;
-            acc[i][j][q] = dh * u * dv;
-            acc[i][j + FN / 2][q] = dh * v;
+            h[q] = held(v * u, scale_h, i);
+            acc[i][j][q] = held(dh * u * dv, scale_dg, i);
+            acc[i][j + FN / 2][q] = held(dh * v, scale_du, i);
           }
           if constexpr (P == 1) {
             const E e[4] = {static_cast<E>(h[0]), static_cast<E>(h[1]), static_cast<E>(h[2]), static_cast<E>(h[3])};

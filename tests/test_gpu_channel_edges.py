@@ -8,7 +8,8 @@ import pytest
 import torch
 
 from tests._gpu import announce, need_gpu
-from tests.test_gpu_channel_ops import NORM_F32, T, act64, check, ffn_case, gen, norm64, nvjp64, nvjp_abs, rnd
+from tests.test_gpu_channel_ops import (NORM_F32, T, act64, check, ffn_case, ffn_reference, gen, norm64, nvjp64,
+                                        nvjp_abs, rnd)
 
 pytestmark = pytest.mark.gpu
 
@@ -225,3 +226,82 @@ def test_block_norm_infinities_and_nan(n, dim, kind, dtype):
     for p, q in zip(got[3:5], b0[3:5]):
         assert torch.equal(p[cols], q[cols]) and torch.isnan(p[3])
     assert torch.equal(got[5], b0[5]) and torch.equal(got[0], b0[0])
+
+
+def wide_range(n, di, F, do, how, seed):
+    """float16 inputs of the feed-forward block whose hidden values leave
+    float16's range and whose results do not.  "big": hidden values far past
+    65504.  "small": gradients of a few 2^-24, of which the sums over many rows
+    are ordinary numbers.  "mixed": runs of rows and of hidden columns of
+    magnitudes from 2^-12 to 2^12 of the others."""
+    x, wg, wu, wd, gy = ffn_case(n, di, F, do, "f16", seed)
+    if how == "big":
+        return (x * 1000).half(), wg, wu, (wd / 4096).half(), (gy / 1024).half()
+    if how == "small":
+        return (x * 32).half(), (wg / 32).half(), (wu / 32).half(), wd, (gy * 1.5e-7).half()
+    g = gen(seed + 1)
+    rows = 2.0 ** torch.randint(-3, 4, ((n + 49) // 50,), generator=g, device="cuda").repeat_interleave(50)[:n]
+    cols = 2.0 ** torch.randint(-6, 7, ((F + 39) // 40,), generator=g, device="cuda").repeat_interleave(40)[:F]
+    return (x * rows[:, None] * 16).half(), wg, (wu * cols[:, None] * 8).half(), (wd / 4096).half(), \
+        (gy * rows.flip(0)[:, None] / 1024).half()
+
+
+def wide_reference(x, wg, wu, wd, gy, act):
+    """As ``ffn_reference``, of gradients times 2^40 (all are linear in grad_out), so
+    that its allowance for the smallest float16 does not count, but with what a
+    block loses of its small values: 2^-16 of the bounds that give its exponent,
+    here over all blocks."""
+    up = 2.0 ** 40
+    (out, eout), grads = ffn_reference(x, wg, wu, wd, gy.double() * up, act, "f16")
+    X, G, U, D, Y = (t.double() for t in (x, wg, wu, wd, gy))
+    mg, mu, md = (t.abs().max().item() for t in (X @ G.T, X @ U.T, Y @ D))
+    mg = 1.0 if act == "sigmoid" else mg
+    n, F = x.shape[0], wg.shape[0]
+    fh, fg, fu = (2.0 ** -16 * t for t in (mg * mu, 1.13 * md * mu, md * mg))
+    one = torch.ones(n, F, dtype=torch.float64, device="cuda")
+    more = (fg * (one @ G.abs()) + fu * (one @ U.abs()), fg * (one.T @ X.abs()), fu * (one.T @ X.abs()),
+            fh * (Y.abs().T @ one))
+    return (out, eout + fh * D.abs().sum(1)), [(r / up, e / up + m) for (r, e), m in zip(grads, more)]
+
+
+@pytest.mark.parametrize("how", ["big", "small", "mixed"])
+@pytest.mark.parametrize("act", ["relu", "sigmoid"])
+@pytest.mark.parametrize("n,di,F,do", [(1, 64, 200, 40), (20, 64, 200, 40), (40, 33, 1000, 65), (64, 128, 72, 48),
+                                       (65, 64, 200, 40), (700, 64, 300, 40), (130, 322, 853, 257), (70, 200, 3001, 65),
+                                       (5000, 65, 70, 33), (300, 20, 8000, 640), (4100, 1030, 1032, 1100),
+                                       (4096, 72, 2048, 64), (2048, 4096, 136, 4096), (17000, 16, 72, 24),
+                                       (70, 24, 8500, 16), (5, 24, 8500, 40)])
+def test_gated_ffn_float16_range(n, di, F, do, act, how):
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"gated ffn float16, {how} hidden values, n={n} {di} x {F} x {do} {act}")
+    x, wg, wu, wd, gy = wide_range(n, di, F, do, how, n + F)
+    (out, eout), grads = wide_reference(x, wg, wu, wd, gy, act)
+    got = sp.gated_ffn_fwd(x, wg, wu, wd, act=act)
+    check(got, out, eout, "f16", "out")
+    back = sp.gated_ffn_bwd(x, wg, wu, wd, gy, act=act)
+    for name, a, (r, e) in zip(("grad_x", "grad_w_gate", "grad_w_up", "grad_w_down"), back, grads):
+        fits = r.abs() < 60000
+        check(torch.where(fits, a, 0), torch.where(fits, r, 0), torch.where(fits, e, 0), "f16", name)
+    assert torch.equal(got, sp.gated_ffn_fwd(x, wg, wu, wd, act=act))
+    assert all(torch.equal(p, q) for p, q in zip(back, sp.gated_ffn_bwd(x, wg, wu, wd, gy, act=act)))
+
+
+@pytest.mark.parametrize("n", [40, 500])
+def test_gated_ffn_float16_infinities_beside_large_and_small_blocks(n):
+    """An infinity in a block of zeros, and beside finite values that need an exponent."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"gated ffn float16, infinities in scaled blocks, n={n}")
+    x, wg, wu, wd, gy = wide_range(n, 64, 200, 40, "mixed", 3)
+    keep = torch.ones(n, dtype=torch.bool)
+    plain = sp.gated_ffn_fwd(x, wg, wu, wd, act="relu")
+    for rest in (1.0, 0.0):
+        bad = x * rest
+        bad[7, 5] = float("inf")
+        keep[7] = False
+        X, G, U, D = (t.double() for t in (bad, wg, wu, wd))
+        ref = (act64(X @ G.T, "relu")[0] * (X @ U.T)) @ D.T
+        out = sp.gated_ffn_fwd(bad, wg, wu, wd, act="relu")
+        same_kind(out, ref, "out")
+        assert torch.equal(out[keep], plain[keep] * rest)
