@@ -28,6 +28,10 @@ struct EmbeddingArgs {
 constexpr int kEmbChunk = 16;
 // Tokens one workgroup ranks in a sorting pass.
 constexpr int kEmbSortBlock = 4096;
+// Counts of this many sorting workgroups and more are added up by a kernel of their
+// own.  64 columns bf16 of 200000 rows, one MI355X, by each workgroup and by the kernel:
+// 300000 tokens (74 workgroups) 90 and 91 us, 524288 (128) 111 and 105, 2^24 6227 and 2971.
+constexpr int64_t kEmbScanBlocks = 128;
 // Lists up to this many tokens into up to this many rows are ordered in one
 // launch: kEmbGroups workgroups, group w those of the rows r = w modulo kEmbGroups.
 constexpr int kEmbGroups = 256;

@@ -48,7 +48,7 @@ EmbeddingPlan embedding_plan(int64_t n, int64_t rows, int64_t dim) {
     return o;
   };
   for (int i = 0; i < (order ? 1 : 2); ++i) p.key[i] = take(4 * n), p.pos[i] = take(4 * n);
-  p.hist = take((size_t{4} << p.digit_bits) * p.blocks);
+  p.hist = take((size_t{4} << p.digit_bits) * (p.blocks + 1));
   p.rowptr = take(4 * (p.keys + 1));
   p.partial = take(4 * p.chunks * round_up(dim, 8));
   p.bytes = at;
@@ -222,6 +222,35 @@ __device__ __forceinline__ uint32_t scan1024(uint32_t v, uint32_t* wave_sum) {
   return before + s - v;
 }
 
+// Counts of the workgroups before each, and of all, for 64 digits a workgroup: the
+// counts of kEmbScanBlocks workgroups and more, which the sorting workgroups would
+// otherwise each add up alone, in time that grows with their square.
+__global__ void __launch_bounds__(1024)
+embedding_scan_kernel(uint32_t* __restrict__ hist, int64_t blocks, int D) {
+  __shared__ uint32_t sum[16][64];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int d = blockIdx.x * 64 + lane;
+  const bool on = d < D;
+  const int64_t b0 = blocks * wave / 16, b1 = blocks * (wave + 1) / 16;
+  uint32_t own = 0;
+  if (on) {
+#pragma unroll 8
+    for (int64_t b = b0; b < b1; ++b) own += hist[b * D + d];
+  }
+  sum[wave][lane] = own;
+  __syncthreads();
+  uint32_t before = 0;
+  for (int w = 0; w < wave; ++w) before += sum[w][lane];
+  if (!on) return;
+#pragma unroll 8
+  for (int64_t b = b0; b < b1; ++b) {
+    const uint32_t c = hist[b * D + d];
+    hist[b * D + d] = before;
+    before += c;
+  }
+  if (wave == 15) hist[blocks * D + d] = before;
+}
+
 // lanes of the wave that are on and have the same key of `bits` bits, by one ballot per bit
 __device__ __forceinline__ uint64_t equal_lanes(bool on, uint32_t key, int bits) {
   uint64_t peers = __ballot(on);
@@ -290,11 +319,16 @@ embedding_sort_kernel(const Index* __restrict__ tokens, const uint32_t* __restri
       total += c;
     }
     total = 0;
+    if (blocks >= kEmbScanBlocks) {  // added up by embedding_scan_kernel
+      prior = hist[static_cast<int64_t>(blockIdx.x) * D + d0];
+      total = hist[blocks * D + d0];
+    } else {
 #pragma unroll 8
-    for (int64_t b = 0; b < blocks; ++b) {
-      const uint32_t c = hist[b * D + d0];
-      total += c;
-      if (b < static_cast<int64_t>(blockIdx.x)) prior += c;
+      for (int64_t b = 0; b < blocks; ++b) {
+        const uint32_t c = hist[b * D + d0];
+        total += c;
+        if (b < static_cast<int64_t>(blockIdx.x)) prior += c;
+      }
     }
   }
   const uint32_t before = scan1024(total, wave_sum);
@@ -680,6 +714,9 @@ int embedding_bwd_launch(const EmbeddingArgs& a) {
       const int to = q ? 1 - last : 0;
       hipLaunchKernelGGL((embedding_hist_kernel<Index>), dim3(static_cast<unsigned>(p.blocks)), dim3(1024), 0, st,
                          tokens, kin, a.rows, a.n, q * p.digit_bits, p.digit_bits, hist);
+      if (p.blocks >= kEmbScanBlocks)
+        hipLaunchKernelGGL(embedding_scan_kernel, dim3(((1u << p.digit_bits) + 63) / 64), dim3(1024), 0, st, hist,
+                           p.blocks, 1 << p.digit_bits);
       hipLaunchKernelGGL((embedding_sort_kernel<Index>), dim3(static_cast<unsigned>(p.blocks)), dim3(1024), 0, st,
                          tokens, kin, pin, a.rows, a.n, q * p.digit_bits, p.digit_bits, hist, p.blocks, key[to],
                          pos[to]);

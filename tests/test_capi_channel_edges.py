@@ -67,3 +67,16 @@ def test_buffers_off_their_elements_are_refused(dtype, off):
     assert all(misaligned(sp.lib.gated_ffn_fwd, ffn, i, off) for i in (2, 4, 5, 6, 11))
     ffn = (dtype, 0, P, 8, P, P, P, P, 8, 3, 8, 16, 8, P, P, P, P, P, small, None)
     assert all(misaligned(sp.lib.gated_ffn_bwd, ffn, i, off) for i in (2, 4, 5, 6, 7, 13, 14, 15, 16))
+
+
+@pytest.mark.parametrize("n,rows,dim", [(100000, 40000, 70), (32769, 5000, 1), (1 << 20, 1 << 21, 24), (1 << 26, 300, 7)])
+def test_embedding_workspace_holds_every_part(n, rows, dim):
+    """Sorted keys and positions twice, 4096 tokens' counts of the digits and the
+    total, the row ranges, and one float32 row of a multiple of eight columns per
+    16 positions."""
+    digits = rows.bit_length()
+    passes = -(-digits // 10)
+    counts = 1 << -(-digits // passes)
+    need = 16 * n + 4 * counts * (-(-n // 4096) + 1) + 4 * (rows + 1) + 4 * (n // 16) * (-(-dim // 8) * 8)
+    got = size(sp.lib.embedding_bwd_workspace, n, rows, dim)
+    assert got[0] == sp.OK and need <= got[1] <= need + 7 * 256 and got[1] % 256 == 0

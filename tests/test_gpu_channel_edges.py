@@ -8,8 +8,8 @@ import pytest
 import torch
 
 from tests._gpu import announce, need_gpu
-from tests.test_gpu_channel_ops import (NORM_F32, T, act64, check, ffn_case, ffn_reference, gen, norm64, nvjp64,
-                                        nvjp_abs, rnd)
+from tests.test_gpu_channel_ops import (E24, NORM_F32, T, act64, check, ffn_case, ffn_reference, gen, norm64,
+                                        nvjp64, nvjp_abs, rnd, tokens_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -305,3 +305,28 @@ def test_gated_ffn_float16_infinities_beside_large_and_small_blocks(n):
         out = sp.gated_ffn_fwd(bad, wg, wu, wd, act="relu")
         same_kind(out, ref, "out")
         assert torch.equal(out[keep], plain[keep] * rest)
+
+
+# ------------------------------------------------------------------ embedding gradient
+
+@pytest.mark.parametrize("n,rows,dim", [(3, 1 << 20, 5), (524287, 5000, 3), (524288, 5000, 3), (2100000, 17, 2),
+                                        (600001, 300000, 4), (700000, (1 << 20) + 5, 3), (32768, 1 << 17, 9),
+                                        (32769, 1 << 17, 9), (32768, (1 << 17) + 1, 9), (32768, 17, 8)])
+def test_embedding_gradient_at_its_limits(n, rows, dim):
+    """The ends of the one-launch ordering (32768 tokens, 2^17 rows), three
+    passes of the radix sort (2^20 rows), and its workgroups' counts added up by
+    themselves and by a kernel of its own (from 524288 tokens)."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"embedding gradient at its limits, n={n} rows={rows} dim={dim}")
+    g = gen(n + rows)
+    tok, grad = tokens_of(g, n, rows, torch.int32), rnd(g, n, dim)
+    tok[-1], grad[-1] = rows - 1, 1.0
+    ok = (tok >= 0) & (tok < rows)
+    at, src = tok.long().clamp(0, rows - 1), grad.double() * ok[:, None]
+    ref = torch.zeros(rows, dim, dtype=torch.float64, device="cuda").index_add_(0, at, src)
+    mag = torch.zeros(rows, dim, dtype=torch.float64, device="cuda").index_add_(0, at, src.abs())
+    count = torch.zeros(rows, dtype=torch.float64, device="cuda").index_add_(0, at, ok.double())
+    d = sp.embedding_bwd(grad, tok, rows)
+    check(d, ref, (count[:, None] + 2) * E24 * mag, "f32", "grad_table")
+    assert torch.equal(sp.embedding_bwd(grad, tok, rows), d)
