@@ -58,6 +58,9 @@ EmbeddingPlan embedding_plan(int64_t n, int64_t rows, int64_t dim) {
 namespace kern {
 
 constexpr int kRowsInFlight = 4;
+// Workgroups of a launch at most, which has fewer than 2^32 threads: longer lists
+// and larger tables take several.
+constexpr int64_t kMostBlocks = int64_t{1} << 22;
 
 // `lanes` lanes (a power of two) walk one row in 16-byte chunks; each lane keeps
 // kRowsInFlight rows in flight.  32768 rows of 2048 bf16 on one MI355X: 42 us,
@@ -460,7 +463,7 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 embedding_chunk_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t* __restrict__ keys,
                        const uint32_t* __restrict__ pos, int64_t rows, int64_t dim, int64_t n, int64_t range_blocks,
-                       int lanes, uint32_t* __restrict__ rowptr, float* __restrict__ partial, int64_t pstride) {
+                       int64_t chunks, int lanes, uint32_t* __restrict__ rowptr, float* __restrict__ partial, int64_t pstride) {
   constexpr int V = Chunk<T>::kN;
   __shared__ float acc_lds[256 * V];
   if (blockIdx.x < range_blocks) {
@@ -495,33 +498,34 @@ embedding_chunk_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t
     rowptr[r] = static_cast<uint32_t>(lo);
     return;
   }
-  const int64_t chunk = blockIdx.x - range_blocks;
-  const uint32_t k0 = keys[chunk * kEmbChunk];
-  if (k0 != keys[chunk * kEmbChunk + kEmbChunk - 1] || k0 >= rows) return;
   const int groups = 256 / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-  for (int c0 = 0; c0 < dim; c0 += lanes * V) {
-    const int c = c0 + lane * V;
-    float acc[V] = {};
-    if (c < dim) {
+  for (int64_t chunk = blockIdx.x - range_blocks; chunk < chunks; chunk += gridDim.x - range_blocks) {
+    const uint32_t k0 = keys[chunk * kEmbChunk];
+    if (k0 != keys[chunk * kEmbChunk + kEmbChunk - 1] || k0 >= rows) continue;
+    for (int c0 = 0; c0 < dim; c0 += lanes * V) {
+      const int c = c0 + lane * V;
+      float acc[V] = {};
+      if (c < dim) {
 #pragma unroll 4
-      for (int j = group; j < kEmbChunk; j += groups) {
-        float v[V];
-        load_chunk(g + static_cast<int64_t>(pos[chunk * kEmbChunk + j]) * g_stride, c, static_cast<int>(dim), v);
+        for (int j = group; j < kEmbChunk; j += groups) {
+          float v[V];
+          load_chunk(g + static_cast<int64_t>(pos[chunk * kEmbChunk + j]) * g_stride, c, static_cast<int>(dim), v);
 #pragma unroll
-        for (int t = 0; t < V; ++t) acc[t] += v[t];
+          for (int t = 0; t < V; ++t) acc[t] += v[t];
+        }
       }
+#pragma unroll
+      for (int t = 0; t < V; ++t) acc_lds[t * 256 + threadIdx.x] = acc[t];
+      __syncthreads();
+      if (group == 0 && c < dim) {
+        for (int q = 1; q < groups; ++q)
+#pragma unroll
+          for (int t = 0; t < V; ++t) acc[t] += acc_lds[t * 256 + q * lanes + lane];
+#pragma unroll
+        for (int t = 0; t < V; ++t) partial[chunk * pstride + c + t] = acc[t];
+      }
+      __syncthreads();
     }
-#pragma unroll
-    for (int t = 0; t < V; ++t) acc_lds[t * 256 + threadIdx.x] = acc[t];
-    __syncthreads();
-    if (group == 0 && c < dim) {
-      for (int q = 1; q < groups; ++q)
-#pragma unroll
-        for (int t = 0; t < V; ++t) acc[t] += acc_lds[t * 256 + q * lanes + lane];
-#pragma unroll
-      for (int t = 0; t < V; ++t) partial[chunk * pstride + c + t] = acc[t];
-    }
-    __syncthreads();
   }
 }
 
@@ -579,15 +583,15 @@ template <typename T, bool Few>
 __global__ void __launch_bounds__(256)
 embedding_rows_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t* __restrict__ pos,
                       const uint32_t* __restrict__ rowptr, const float* __restrict__ partial, int64_t pstride,
-                      int64_t rows, int groups_of_rows, int64_t per_group, int dim, float scale, int lanes,
-                      T* __restrict__ out) {
+                      int64_t first_row, int64_t rows, int groups_of_rows, int64_t per_group, int dim, float scale,
+                      int lanes, T* __restrict__ out) {
   constexpr int V = Chunk<T>::kN, kCols = 2, kAlone = Few ? -1 : 8;
   __shared__ float acc_lds[256 * V * kCols];
   __shared__ uint32_t range[2][32];
   __shared__ int long_rows[32], long_count;
   const int groups = 256 / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
   const int here = Few ? 1 : groups > 16 ? groups : 16;  // rows of this workgroup
-  auto row_of = [](int q) { return blockIdx.x + static_cast<int64_t>(q) * gridDim.x; };
+  auto row_of = [=](int q) { return first_row + blockIdx.x + static_cast<int64_t>(q) * gridDim.x; };
   auto items = [](int64_t s, int64_t e) {  // loads of a lane that sums the range alone
     const int64_t c_lo = (s + kEmbChunk - 1) / kEmbChunk, c_hi = e / kEmbChunk;
     return c_lo < c_hi ? e - s - (c_hi - c_lo) * (kEmbChunk - 1) : e - s;
@@ -667,11 +671,15 @@ template <typename T, typename Index>
 int embedding_fwd_launch(const EmbeddingArgs& a) {
   const int lanes = row_lanes<T>(a.dim);
   const int64_t per = 256 / lanes * kRowsInFlight;
-  hipLaunchKernelGGL((embedding_fwd_kernel<T, Index>), dim3(static_cast<unsigned>((a.n + per - 1) / per)), dim3(256),
-                     0, static_cast<hipStream_t>(a.stream), static_cast<const T*>(a.table),
-                     static_cast<const Index*>(a.tokens), a.rows, a.dim, a.n, a.scale, static_cast<T*>(a.out),
-                     a.out_stride, lanes);
-  return static_cast<int>(hipGetLastError());
+  for (int64_t first = 0, slice = kMostBlocks * per; first < a.n; first += slice) {
+    const int64_t n = std::min(a.n - first, slice);
+    hipLaunchKernelGGL((embedding_fwd_kernel<T, Index>), dim3(static_cast<unsigned>((n + per - 1) / per)), dim3(256), 0,
+                       static_cast<hipStream_t>(a.stream), static_cast<const T*>(a.table),
+                       static_cast<const Index*>(a.tokens) + first, a.rows, a.dim, n, a.scale,
+                       static_cast<T*>(a.out) + first * a.out_stride, a.out_stride, lanes);
+    if (const int rc = static_cast<int>(hipGetLastError())) return rc;
+  }
+  return 0;
 }
 
 template <typename T, typename Index>
@@ -707,6 +715,7 @@ int embedding_bwd_launch(const EmbeddingArgs& a) {
     while ((1 << bits) < p.per_group) ++bits;
     hipLaunchKernelGGL((embedding_order_kernel<Index>), dim3(kEmbGroups), dim3(1024), 0, st, tokens, a.rows,
                        static_cast<int>(a.n), static_cast<int>(p.per_group), bits, key[0], pos[0], rowptr);
+    if (const int rc = static_cast<int>(hipGetLastError())) return rc;
   } else {
     for (int q = 0; q < p.passes && p.blocks; ++q) {
       const uint32_t* kin = q ? key[last] : nullptr;
@@ -714,28 +723,39 @@ int embedding_bwd_launch(const EmbeddingArgs& a) {
       const int to = q ? 1 - last : 0;
       hipLaunchKernelGGL((embedding_hist_kernel<Index>), dim3(static_cast<unsigned>(p.blocks)), dim3(1024), 0, st,
                          tokens, kin, a.rows, a.n, q * p.digit_bits, p.digit_bits, hist);
-      if (p.blocks >= kEmbScanBlocks)
+      if (const int rc = static_cast<int>(hipGetLastError())) return rc;
+      if (p.blocks >= kEmbScanBlocks) {
         hipLaunchKernelGGL(embedding_scan_kernel, dim3(((1u << p.digit_bits) + 63) / 64), dim3(1024), 0, st, hist,
                            p.blocks, 1 << p.digit_bits);
+        if (const int rc = static_cast<int>(hipGetLastError())) return rc;
+      }
       hipLaunchKernelGGL((embedding_sort_kernel<Index>), dim3(static_cast<unsigned>(p.blocks)), dim3(1024), 0, st,
                          tokens, kin, pin, a.rows, a.n, q * p.digit_bits, p.digit_bits, hist, p.blocks, key[to],
                          pos[to]);
+      if (const int rc = static_cast<int>(hipGetLastError())) return rc;
       last = to;
     }
   }
   const int lanes = row_lanes<T>(a.dim);
   const int64_t range_blocks = p.groups > 1 ? 0 : (a.rows + 1 + 255) / 256;
-  if (range_blocks + p.chunks > 0)
-    hipLaunchKernelGGL((embedding_chunk_kernel<T>), dim3(static_cast<unsigned>(range_blocks + p.chunks)), dim3(256), 0,
-                       st, static_cast<const T*>(a.grad), a.grad_stride, key[last], pos[last], p.keys, a.dim, a.n,
-                       range_blocks, lanes, rowptr, partial, round_up(a.dim, 8));
+  if (range_blocks + p.chunks > 0) {
+    hipLaunchKernelGGL((embedding_chunk_kernel<T>), dim3(static_cast<unsigned>(range_blocks) + static_cast<unsigned>(std::min(p.chunks, kMostBlocks))),
+                       dim3(256), 0, st, static_cast<const T*>(a.grad), a.grad_stride, key[last], pos[last], p.keys,
+                       a.dim, a.n, range_blocks, p.chunks, lanes, rowptr, partial, round_up(a.dim, 8));
+    if (const int rc = static_cast<int>(hipGetLastError())) return rc;
+  }
   const int narrow = row_lanes<T>(a.dim, 64), each = std::max(256 / narrow, 16);
   const bool few = a.rows < 2048;
   auto* sum = few ? embedding_rows_kernel<T, true> : embedding_rows_kernel<T, false>;
-  hipLaunchKernelGGL(sum, dim3(static_cast<unsigned>(few ? a.rows : (a.rows + each - 1) / each)), dim3(256), 0, st,
-                     static_cast<const T*>(a.grad), a.grad_stride, pos[last], rowptr, partial, round_up(a.dim, 8),
-                     a.rows, p.groups, p.per_group, static_cast<int>(a.dim), a.scale, narrow, static_cast<T*>(a.out));
-  return static_cast<int>(hipGetLastError());
+  // as many rows a launch as its workgroups may be
+  for (int64_t first = 0, slice = kMostBlocks * each; first < a.rows; first += slice) {
+    const int64_t end = std::min(a.rows, first + slice), here = end - first;
+    hipLaunchKernelGGL(sum, dim3(static_cast<unsigned>(few ? here : (here + each - 1) / each)), dim3(256), 0, st,
+                       static_cast<const T*>(a.grad), a.grad_stride, pos[last], rowptr, partial, round_up(a.dim, 8), first,
+                       end, p.groups, p.per_group, static_cast<int>(a.dim), a.scale, narrow, static_cast<T*>(a.out));
+    if (const int rc = static_cast<int>(hipGetLastError())) return rc;
+  }
+  return 0;
 }
 
 template <typename T>

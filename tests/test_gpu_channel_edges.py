@@ -330,3 +330,24 @@ def test_embedding_gradient_at_its_limits(n, rows, dim):
     d = sp.embedding_bwd(grad, tok, rows)
     check(d, ref, (count[:, None] + 2) * E24 * mag, "f32", "grad_table")
     assert torch.equal(sp.embedding_bwd(grad, tok, rows), d)
+
+
+def test_embedding_of_more_than_a_launch():
+    """A launch has fewer than 2^32 threads, a list and a table may need more."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    n = (1 << 28) + 5
+    announce(f"embedding gradient of {n} tokens, one gradient row read by all")
+    tok = torch.arange(n, device="cuda", dtype=torch.int32) % 40000
+    d = sp.embedding_bwd(torch.ones(1, 1, device="cuda").expand(n, 1), tok, 40000)
+    want = torch.full((40000, 1), float(n // 40000), device="cuda")  # whole numbers below 2^24 are exact
+    want[:n % 40000] += 1
+    assert torch.equal(d, want)
+    del tok, d
+    rows = (1 << 28) + 3
+    announce(f"embedding gradient into {rows} rows")
+    tok = torch.tensor([0, 5, rows - 1, rows - 1, 1 << 27, (1 << 26) - 1, 1 << 26, rows], device="cuda", dtype=torch.int32)
+    d = sp.embedding_bwd(torch.ones(8, 2, device="cuda", dtype=torch.bfloat16), tok, rows)
+    at = torch.nonzero(d[:, 0])[:, 0].tolist()
+    assert at == [0, 5, (1 << 26) - 1, 1 << 26, 1 << 27, rows - 1] and torch.equal(d[:, 0], d[:, 1])
+    assert d[at, 0].tolist() == [1, 1, 1, 1, 1, 2]
