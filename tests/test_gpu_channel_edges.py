@@ -7,6 +7,7 @@ gradient's ordering, and the accuracy that the forms promise.  Tolerances as in
 import pytest
 import torch
 
+from tests import _ffn_accuracy as acc
 from tests._gpu import announce, need_gpu
 from tests.test_gpu_channel_ops import (E24, NORM_F32, T, act64, check, ffn_case, ffn_reference, gen, norm64,
                                         nvjp64, nvjp_abs, rnd, tokens_of)
@@ -351,3 +352,36 @@ def test_embedding_of_more_than_a_launch():
     at = torch.nonzero(d[:, 0])[:, 0].tolist()
     assert at == [0, 5, (1 << 26) - 1, 1 << 26, 1 << 27, rows - 1] and torch.equal(d[:, 0], d[:, 1])
     assert d[at, 0].tolist() == [1, 1, 1, 1, 1, 2]
+
+
+# ------------------------------------------------------------------ accuracy of the feed-forward block
+
+@pytest.mark.parametrize("shape", acc.SHAPES_F32)
+def test_gated_ffn_float32_accuracy(shape):
+    """All 24 bits of long sums: fewer plane pairs miss this bound (tests/test_ffn_accuracy.py)."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"gated ffn float32 accuracy {shape}")
+    x, wg, wu, wd, gy = acc.inputs(*shape, 1, "cuda")
+    ref = acc.block(*(t.double() for t in (x, wg, wu, wd, gy)))
+    bound = acc.float32_rms(*shape)
+    for name, a, r in zip(acc.NAMES, (sp.gated_ffn_fwd(x, wg, wu, wd), *sp.gated_ffn_bwd(x, wg, wu, wd, gy)), ref):
+        worst = acc.rms_error(a, r) / bound[name]
+        print(f"[parity] {name}: {worst:.3f} of the rms bound", flush=True)
+        assert worst <= 1, name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", acc.SHAPES_16)
+def test_gated_ffn_16_bit_roundings(shape, dtype):
+    """h, dg and du are rounded to 16 bits, nothing else before the outputs (dh is not)."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"gated ffn roundings {shape} {dtype}")
+    t = T[dtype]
+    x, wg, wu, wd, gy = acc.inputs(*shape, 2, "cuda", t)
+    ref = acc.block(*(v.double() for v in (x, wg, wu, wd, gy)), hidden=lambda v: v.to(t).double())
+    for name, a, r in zip(acc.NAMES, (sp.gated_ffn_fwd(x, wg, wu, wd), *sp.gated_ffn_bwd(x, wg, wu, wd, gy)), ref):
+        share = acc.unequal(a, r, t)
+        print(f"[parity] {name}: {share:.4f} of the elements rounded another way", flush=True)
+        assert share <= acc.UNEQUAL, name
