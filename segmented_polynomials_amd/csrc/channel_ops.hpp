@@ -37,7 +37,10 @@ constexpr int64_t kEmbScanBlocks = 128;
 constexpr int kEmbGroups = 256;
 constexpr int64_t kEmbOrderTokens = 32768;
 constexpr int64_t kEmbOrderRows = 512 * kEmbGroups;
-// Tables of at most this many rows are summed in LDS, without a sort.
+// Tables of at most this many rows are summed in LDS, without a sort: as many as
+// have 1024 columns in 64 KB.  16 rows, one MI355X, us in LDS and sorted: 16384 tokens
+// of 64 bf16 11 and 24, of 1024 bf16 45 and 42 (a text's 67); 100000 14 and 39, 120
+// and 118 (283).
 constexpr int kEmbDirectRows = 16;
 
 // Device workspace of the embedding gradient, as byte offsets.

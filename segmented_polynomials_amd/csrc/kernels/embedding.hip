@@ -570,14 +570,14 @@ __device__ __forceinline__ void sum_range(const T* __restrict__ g, int64_t g_str
 
 // A workgroup takes 16 table rows, or one for each of its groups of `lanes`
 // lanes (at most a wave), every gridDim.x-th: frequent tokens are often
-// neighbours.  It
-// writes zeros for its empty ranges, all threads together: most rows of a large
-// table have no token, and the dependent loads of the others' sums take longer
-// than all the zeros.  Then a group of lanes sums a short range alone; a range
-// of more than kAlone items is shared out over all groups, whose sums are
-// added in order: the few frequent tokens would otherwise be the kernel's last
-// groups.  Few: one row per workgroup, where a table's rows would not fill
-// the chip.  32768 x 1024 bf16, 16384 tokens: 24 us, 4.2 TB/s (one row per
+// neighbours.  It writes zeros for its empty ranges, all threads together: most
+// rows of a large table have no token, and the dependent loads of the others'
+// sums take longer than all the zeros.  Then a group of lanes sums a short range
+// alone; a range of more than kAlone items is shared out over all groups, whose
+// sums are added in order: the few frequent tokens would otherwise be the
+// kernel's last groups.  (kAlone 8, 16, 32: 100000 tokens spread evenly over 16000
+// rows of 64 bf16 87, 47, 45 us, a text's 65, 59, 59; 16384 of a text over 50000
+// 28, 28, 31.)  Few: one row per workgroup.  32768 x 1024 bf16, 16384 tokens: 24 us, 4.2 TB/s (one row per
 // 64 lanes, empty or not: 41 us).
 template <typename T, bool Few>
 __global__ void __launch_bounds__(256)
@@ -585,7 +585,7 @@ embedding_rows_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t*
                       const uint32_t* __restrict__ rowptr, const float* __restrict__ partial, int64_t pstride,
                       int64_t first_row, int64_t rows, int groups_of_rows, int64_t per_group, int dim, float scale,
                       int lanes, T* __restrict__ out) {
-  constexpr int V = Chunk<T>::kN, kCols = 2, kAlone = Few ? -1 : 8;
+  constexpr int V = Chunk<T>::kN, kCols = 2, kAlone = Few ? -1 : 16;
   __shared__ float acc_lds[256 * V * kCols];
   __shared__ uint32_t range[2][32];
   __shared__ int long_rows[32], long_count;
@@ -745,7 +745,14 @@ int embedding_bwd_launch(const EmbeddingArgs& a) {
     if (const int rc = static_cast<int>(hipGetLastError())) return rc;
   }
   const int narrow = row_lanes<T>(a.dim, 64), each = std::max(256 / narrow, 16);
-  const bool few = a.rows < 2048;
+  // One row a workgroup where rows are too few for the chip in sixteens, or have many
+  // tokens each.  One MI355X, us with one row and with sixteen:
+  //   tokens, even       16384                       100000
+  //   rows            1000        4000    16000      2000        4000       16000
+  //   64 bf16         25, 132     36, 33  88, 20     52, 172     61, 159    114, 87
+  //   1024 bf16       31, 84      34, 42  61, 34     72, 136     76, 121    104, 94
+  //   128 f32         20, 47      23, 25  42, 22     48, 85      51, 82      70, 67
+  const bool few = a.rows < 2048 || a.n >= 16 * a.rows;
   auto* sum = few ? embedding_rows_kernel<T, true> : embedding_rows_kernel<T, false>;
   // as many rows a launch as its workgroups may be
   for (int64_t first = 0, slice = kMostBlocks * each; first < a.rows; first += slice) {
