@@ -791,7 +791,7 @@ int block_norm_bwd(int dtype, int kind, int gate_mode, int gate_act, const void*
  * (backward != 0) needs: the hidden rows, float32 parts of long sums that
  * several workgroups share and, where an operand's width, stride or address
  * does not suit 16-byte accesses (float32: always, as three bf16 planes), a
- * copy of it (none in a forward pass of at most 64 rows).  Sized for the case
+ * copy of it (none in a forward pass of at most 16 rows).  Sized for the case
  * that every one is copied. */
 int gated_ffn_workspace(int dtype, int64_t n, int64_t d_in, int64_t hidden, int64_t d_out, int backward,
                         size_t* bytes);

@@ -738,10 +738,11 @@ int embedding_bwd_launch(const EmbeddingArgs& a) {
   }
   const int lanes = row_lanes<T>(a.dim);
   const int64_t range_blocks = p.groups > 1 ? 0 : (a.rows + 1 + 255) / 256;
-  if (range_blocks + p.chunks > 0) {
-    hipLaunchKernelGGL((embedding_chunk_kernel<T>), dim3(static_cast<unsigned>(range_blocks) + static_cast<unsigned>(std::min(p.chunks, kMostBlocks))),
-                       dim3(256), 0, st, static_cast<const T*>(a.grad), a.grad_stride, key[last], pos[last], p.keys,
-                       a.dim, a.n, range_blocks, p.chunks, lanes, rowptr, partial, round_up(a.dim, 8));
+  const int64_t chunk_blocks = range_blocks + std::min(p.chunks, kMostBlocks);
+  if (chunk_blocks > 0) {
+    hipLaunchKernelGGL((embedding_chunk_kernel<T>), dim3(static_cast<unsigned>(chunk_blocks)), dim3(256), 0, st,
+                       static_cast<const T*>(a.grad), a.grad_stride, key[last], pos[last], p.keys, a.dim, a.n,
+                       range_blocks, p.chunks, lanes, rowptr, partial, round_up(a.dim, 8));
     if (const int rc = static_cast<int>(hipGetLastError())) return rc;
   }
   const int narrow = row_lanes<T>(a.dim, 64), each = std::max(256 / narrow, 16);

@@ -2,7 +2,7 @@
 // (gemm_tile.hpp), for one element type per translation unit:
 //   forward   h = act(x Wg^T) * (x Wu^T)     one paired product, the
 //                                            activation and gating its epilogue
-//             out = h Wd^T                   (at most 64 rows: gemm_rows.hpp)
+//             out = h Wd^T                   (few rows: gemm_rows.hpp)
 //   backward  dh = g Wd
 //             h, dg, du from x, Wg, Wu, dh   the paired product again
 //             dx = dg Wg + du Wu             one product of two phases
@@ -119,8 +119,10 @@ int gemm_launch_tile(GemmArgs& g, hipStream_t st) {
 // workgroups of the 64 x 64 tile; a product that fills less than half of them
 // and has a long sum gives each tile several, of at least sixteen steps, whose
 // float32 sums a second kernel adds.  One MI355X, 63 rows of 1352 x 5603 x 272
-// float32, backward: 158 us, 385 us without; shares of eight steps cost 1357
-// rows of 322 x 853 x 257 f16, whose sums have 22 to 28, 6 us of 44.
+// float32, backward: 158 us, 385 us without.  With at least 8, 16 and 32 steps a
+// share, us of backward passes in bf16 | f32: 1357 x 322 x 853 x 257 46, 43, 42 | 95, 96,
+// 96; 500 x 256 x 512 x 256 20, 19, 19 | 43, 46, 53; 64 x 1024 x 4096 x 1024 46, 45, 49 |
+// 105, 111, 129; 300 x 128 x 8000 x 128 43, 40, 42 | 87, 80, 81.
 struct Split {
   int splits = 1;
   int64_t elements = 0;  // of one share
@@ -128,7 +130,7 @@ struct Split {
 template <typename Dt>
 Split plan_split(const GemmArgs& g) {
   constexpr int64_t kStep = Dt::kPlanes == 1 ? 64 : 32;
-    Split p;
+  Split p;
   int64_t tiles = 0;
   for (int z = 0; z < g.batch; ++z) {
     tiles += round_up(g.m[z], 64) / 64 * (round_up(g.n[z], 64) / 64);
@@ -364,7 +366,7 @@ template <typename Dt>
 int ffn_fwd(const GatedFfnArgs& a, size_t* bytes) {
   const bool worst = bytes != nullptr;
   const hipStream_t st = static_cast<hipStream_t>(a.stream);
-  if (a.n <= kFewRows) {
+  if (takes_few_rows<Dt>(a.n, a.d_in, a.hidden)) {
     Arena arena{static_cast<char*>(a.workspace)};
     const int64_t ldh = round_up(a.hidden, 8);
     void* h = arena.take<typename Dt::T>(a.n * ldh);
@@ -431,10 +433,15 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
   dw.batch = 2;
   dw.m[1] = dw.m[0], dw.n[1] = dw.n[0], dw.lda[1] = dw.lda[0], dw.ldb[1] = dw.ldb[0], dw.ldc[1] = dw.ldc[0];
   dw.c[1] = a.gw_up;
-  // Products that do not fill the card share a launch (1357 rows of 322 x 853 x 257: 10 + 9 us apart);
-  // large ones are chosen tiles for each (8192 x 2048 x 5632: 329 + 192 us apart, 578 us together).
+  // The three products share a launch unless they fill many rounds of the card, where each is better chosen
+  // a tile of its own.  One MI355X, us together and apart, by 64 x 64 tiles, bf16 | f32:
+  //   238 (1357 x 322 x 853 x 257)        48,  58   |   101,  122
+  //   1296 (4096 x 768 x 2304 x 768)     196, 207   |   768,  778
+  //   2112 (8192 x 1024 x 2816 x 1024)   504, 525   |  2306, 2360
+  //   8448 (4096 x 2048 x 5632 x 2048)   792, 806   |  4794, 4643
+  // and of 8192 rows of the last 578 and 521 for these products alone.
   const int64_t tiles = round_up(a.hidden, 64) / 64 * (round_up(a.d_in, 64) / 64 * 2 + round_up(a.d_out, 64) / 64);
-  const bool apart = tiles > 1024;
+  const bool apart = tiles > 4096;
   if (!apart) {
     add_phase<Dt>(dw, at, go, h);
     dw.batch = 3;
@@ -453,9 +460,14 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
   int rc = plan.run_pack(st);
   if (!rc) rc = gemm_launch_split<Dt, false, true, kEpiStoreF32>(first, sums, st);
   if (!rc) rc = gemm_launch<Dt, false, false, kEpiGatedBwd>(pair, st);
-  // Nor do dx and the weights' gradients wait for each other: one round of the card together (the
-  // case above 16 us, 12 + 11 us in two launches).
-  if (!rc && a.gx && a.gw_gate && tiles + round_up(a.n, 64) / 64 * (round_up(a.d_in, 64) / 64) <= 768)
+  // Nor do dx and the weights' gradients wait for each other: up to two rounds of the card they share a launch too,
+  // in 64 x 64 tiles.  One MI355X, us in one launch and in two, by tiles, bf16 | f32:
+  //   370 (the first above)               42,  48   |    97,  100
+  //   1024 (2000 x 512 x 2048 x 512)      75,  80   |   236,  238
+  //   1240 (4096 x 640 x 1280 x 640)     115, 123   |   385,  393
+  //   2064 (the second above)            198, 186   |   758,  774
+  //   4160 (the third)                   681, 492   |  2566, 2309
+  if (!rc && a.gx && a.gw_gate && tiles + round_up(a.n, 64) / 64 * (round_up(a.d_in, 64) / 64) <= 2 * 768)
     return gemm_launch_two_split<Dt>(dx, dw, sums, st);
   if (!rc && a.gx) rc = gemm_launch_split<Dt, false, true, kEpiStore>(dx, sums, st);
   if (!rc && a.gw_gate) {

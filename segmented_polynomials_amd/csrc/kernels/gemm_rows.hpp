@@ -1,17 +1,16 @@
 // Products of a few rows with a weight matrix, out[m, o] = sum over k of
-// x[m, k] w[o, k] for at most 64 rows: bound by reading the weights once.  A workgroup
+// x[m, k] w[o, k] for at most 32 rows: bound by reading the weights once.  A workgroup
 // takes 16 weight rows (paired: of both matrices) and its waves share out the
 // sum over k, 64 k at a time; weights and rows go from memory straight into
 // the matrix instructions' registers, with no staging and no barrier before
-// the waves' sums are added, in order, through LDS.  So many loads are in
-// flight that one pass over them is hardly longer than a single load: with 16
-// waves of 4 KB each 64 workgroups already ask for the whole of 8 MB.  Loads
-// are of 16 bytes at any alignment, float32 is split into its planes in
-// registers: no operand is copied first.
+// the waves' sums are added, in order, through LDS.  Loads are of 16 bytes at any
+// alignment, float32 is split into its planes in registers: no operand is
+// copied first.  With an output of 1024 columns the second product has 64
+// workgroups, a quarter of the card, and takes longer (7 us, 8 MB) than the paired
+// one with 256 (6 us, 16 MB; 3 rows of 1024 x 4096 x 1024 bf16): its own loads and
+// sums bound it, not the memory.
 // float16 hidden rows go from the paired product to the second in scaled blocks
 // (gemm_tile.hpp), here of sixteen columns of one row.
-// One MI355X, 3 rows, 1024 x 4096 bf16: gate, up and down take 6 + 8 us, as tiles of
-// 64 x 64 (gemm_tile.hpp) 8 + 18 us.
 #pragma once
 #include <algorithm>
 
@@ -20,8 +19,17 @@
 namespace segpoly {
 namespace kern {
 
-// Rows at most this many take this form.
-constexpr int64_t kFewRows = 64;
+// Which calls take this form: up to 16 rows all, up to 32 those of float32 and those
+// whose three weights stay small.  One MI355X, us here and in tiles (gemm_tile.hpp):
+//                          bf16 1 row      16           32           48 rows    f32 32     48
+//   128 x 512 x 128          5.6,  8.2    6.0,  8.4    7.8,  8.6   10.5,  8.7   16,  19   23,  19
+//   512 x 2048 x 4096        9.0, 14.3   10.9, 14.6   14.5, 15.1   19.2, 15.5   35,  47   50,  47
+//   1024 x 4096 x 1024      11.8, 16.6   15.7, 17.1   21.8, 17.4   30.3, 18.1   59,  55   88,  56
+//   2048 x 5632 x 2048      20.8, 23.2   27.6, 23.8   39.1, 24.1   54.9, 24.3  112, 129  167, 131
+template <typename Dt>
+bool takes_few_rows(int64_t n, int64_t d_in, int64_t hidden) {
+  return n <= 16 || (n <= 32 && (Dt::kPlanes > 1 || hidden * d_in <= int64_t{1} << 21));
+}
 
 struct RowsArgs {
   const void *x, *w, *w2;  // [m][k] with row stride ldx, [n][k] dense; w2 of a paired product
@@ -245,8 +253,7 @@ int gemm_rows_launch(const RowsArgs& g, hipStream_t st) {
 template <typename Dt, bool Pair>
 int gemm_rows(const RowsArgs& g, hipStream_t st) {
   if (g.m <= 16) return gemm_rows_launch<Dt, 1, Pair>(g, st);
-  if (g.m <= 32) return gemm_rows_launch<Dt, 2, Pair>(g, st);
-  return gemm_rows_launch<Dt, 4, Pair>(g, st);
+  return gemm_rows_launch<Dt, 2, Pair>(g, st);
 }
 
 }  // namespace kern
