@@ -292,10 +292,12 @@ struct FfnPlan {
 
   explicit FfnPlan(void* ws) : arena{static_cast<char*>(ws)} {}
 
-  // worst: as if the matrix had to be packed (the size query)
-  Operand use(const void* src, int64_t rows, int64_t width, int64_t ld, bool worst) {
+  // worst: as if the matrix had to be packed (the size query).  summed: over its
+  // rows, in some product, whose loads of the last step would read rows past the
+  // last where rows overlap (each starts within the one before).
+  Operand use(const void* src, int64_t rows, int64_t width, int64_t ld, bool worst, bool summed = false) {
     Operand o{};
-    if (!worst && P == 1 && width % 8 == 0 && ld % 8 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0) {
+    if (!worst && P == 1 && !(summed && ld < width) && width % 8 == 0 && ld % 8 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0) {
       o.plane[0] = static_cast<const uint16_t*>(src);
       o.ld = ld;
       return o;
@@ -413,11 +415,11 @@ int ffn_bwd(const GatedFfnArgs& a, size_t* bytes) {
   const bool worst = bytes != nullptr;
   const hipStream_t st = static_cast<hipStream_t>(a.stream);
   FfnPlan<Dt> plan(a.workspace);
-  const Operand x = plan.use(a.x, a.n, a.d_in, a.x_stride, worst);
+  const Operand x = plan.use(a.x, a.n, a.d_in, a.x_stride, worst, true);
   const Operand wg = plan.use(a.w_gate, a.hidden, a.d_in, a.d_in, worst);
   const Operand wu = plan.use(a.w_up, a.hidden, a.d_in, a.d_in, worst);
   const Operand wd = plan.use(a.w_down, a.d_out, a.hidden, a.hidden, worst);
-  const Operand go = plan.use(a.gout, a.n, a.d_out, a.gout_stride, worst);
+  const Operand go = plan.use(a.gout, a.n, a.d_out, a.gout_stride, worst, true);
   const Operand h = plan.hidden(a.n, a.hidden), dg = plan.hidden(a.n, a.hidden), du = plan.hidden(a.n, a.hidden);
   float* dh = plan.arena.template take<float>(a.n * h.ld);
   GemmArgs first = product<Dt>(a.n, a.hidden, a.d_out, go, wd, dh, h.ld);

@@ -385,3 +385,24 @@ def test_gated_ffn_16_bit_roundings(shape, dtype):
         share = acc.unequal(a, r, t)
         print(f"[parity] {name}: {share:.4f} of the elements rounded another way", flush=True)
         assert share <= acc.UNEQUAL, name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n", [65, 90, 500])
+def test_gated_ffn_bwd_infinity_in_rows_that_overlap(n, dtype):
+    """One gradient row read by all, and rows eight elements apart: the sum over
+    the rows ends with the last, also where a row past it would be memory of others."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"gated ffn backward, overlapping gradient rows with an infinity, n={n} {dtype}")
+    x, wg, wu, wd, gy = ffn_case(n, 64, 72, 40, dtype, 5)
+    x, wu = x.abs() + 0.1, wu.abs() + 0.1  # hidden values are positive: infinity times them is infinity
+    flat = gy.flatten()[:(n - 1) * 8 + 40].clone()
+    flat[-1] = float("inf")
+    one = gy[:1].clone()
+    one[0, 5] = float("inf")
+    for rows in (one.expand(n, 40), flat.as_strided((n, 40), (8, 1))):
+        a = sp.gated_ffn_bwd(x, wg, wu, wd, rows, act="sigmoid")
+        b = sp.gated_ffn_bwd(x, wg, wu, wd, rows.clone(memory_format=torch.contiguous_format), act="sigmoid")
+        assert torch.isinf(b[3]).any() and torch.isfinite(b[3]).any()
+        assert all(torch.equal(p.nan_to_num(7.0, 9.0, 11.0), q.nan_to_num(7.0, 9.0, 11.0)) for p, q in zip(a, b))
