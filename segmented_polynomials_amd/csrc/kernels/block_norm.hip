@@ -7,6 +7,7 @@
 
 #include "../channel_ops.hpp"
 #include "../launch.hpp"
+#include "column_sums.hpp"
 
 namespace segpoly {
 
@@ -35,33 +36,20 @@ int64_t block_norm_parts(int64_t n, int64_t dim) {
 
 namespace kern {
 
-// column sums of the partial rows: 32 columns by 32 interleaved row sets per
-// workgroup, the sets added in order
+// column sums of the partial rows
 __global__ void __launch_bounds__(1024)
 block_norm_fold_kernel(const float* __restrict__ partial, int64_t parts, int64_t dim, const float* __restrict__ w_post,
                        const float* __restrict__ res_scale, float* __restrict__ gpost, float* __restrict__ gscale,
                        float* __restrict__ gpre) {
-  __shared__ float lds[32 * 33];
   if (blockIdx.y == 1 && !gpre) return;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32;
-  const int set = threadIdx.x / 32;
-  float s = 0.f;
-  if (c < dim) {
-#pragma unroll 8
-    for (int64_t p = set; p < parts; p += 32) s += partial[(p * 2 + blockIdx.y) * dim + c];
-  }
-  lds[set * 33 + threadIdx.x % 32] = s;
-  __syncthreads();
-  if (threadIdx.x < 32 && c < dim) {
-    float t = 0.f;
-#pragma unroll
-    for (int q = 0; q < 32; ++q) t += lds[q * 33 + threadIdx.x];
-    if (blockIdx.y == 1) {
-      gpre[c] = t;
-    } else {
-      gpost[c] = res_scale ? t * res_scale[c] : t;
-      if (gscale) gscale[c] = t * w_post[c];
-    }
+  const float t = column_sum(partial + blockIdx.y * dim, parts, 2 * dim, dim, c);
+  if (threadIdx.x >= 32 || c >= dim) return;
+  if (blockIdx.y == 1) {
+    gpre[c] = t;
+  } else {
+    gpost[c] = res_scale ? t * res_scale[c] : t;
+    if (gscale) gscale[c] = t * w_post[c];
   }
 }
 

@@ -20,6 +20,7 @@
 #include "../channel_ops.hpp"
 #include "../launch.hpp"
 #include "channel_types.hpp"
+#include "column_sums.hpp"
 
 namespace segpoly {
 
@@ -154,28 +155,14 @@ embedding_direct_kernel(const T* __restrict__ g, int64_t g_stride, const Index* 
   }
 }
 
-// sums of the segments: 32 values by 32 interleaved sets of segments per
-// workgroup, the sets added in order
+// sums of the segments
 template <typename T>
 __global__ void __launch_bounds__(1024)
 embedding_direct_fold_kernel(const float* __restrict__ partial, int64_t segments, int64_t values, float scale,
                              T* __restrict__ out) {
-  __shared__ float lds[32 * 33];
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32;
-  const int set = threadIdx.x / 32;
-  float s = 0.f;
-  if (c < values) {
-#pragma unroll 8
-    for (int64_t p = set; p < segments; p += 32) s += partial[p * values + c];
-  }
-  lds[set * 33 + threadIdx.x % 32] = s;
-  __syncthreads();
-  if (threadIdx.x < 32 && c < values) {
-    float t = 0.f;
-#pragma unroll
-    for (int q = 0; q < 32; ++q) t += lds[q * 33 + threadIdx.x];
-    out[c] = static_cast<T>(t * scale);
-  }
+  const float t = column_sum(partial, segments, values, values, c);
+  if (threadIdx.x < 32 && c < values) out[c] = static_cast<T>(t * scale);
 }
 
 // ------------------------------------------------------------ sorting
