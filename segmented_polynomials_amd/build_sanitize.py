@@ -64,7 +64,8 @@ def run_tests():
                UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1")
     _run([sys.executable, "-m", "pytest", "-x", "-q", "-p", "no:cacheprovider",
           os.path.join(ROOT, "tests", "test_capi_host.py"),
-          os.path.join(ROOT, "tests", "test_capi_channel_host.py")], env=env)
+          os.path.join(ROOT, "tests", "test_capi_channel_host.py"),
+          os.path.join(ROOT, "tests", "test_capi_channel_edges.py")], env=env)
 
 
 if __name__ == "__main__":
