@@ -14,9 +14,13 @@
 // registers).  G lanes hold one row, E = 8 elements per lane while the row
 // fits in a workgroup; up to 64 lanes the reductions need no barrier, so
 // narrow rows share a wave.  One MI355X, bf16 with a gate per element: forward of
-// 16384 x 2048 67 us, 5.0 TB/s; backward of 8192 x 4096 115 us, 4.7 TB/s (a copy of
+// 16384 x 2048 65 us, 5.2 TB/s; backward of 8192 x 4096 111 us, 4.8 TB/s (a copy of
 // 1 GiB: 5.1).  Before the next row was loaded ahead and the parameters came by
-// 16-byte loads, 98 and 373 us.
+// 16-byte loads, 98 and 373 us.  Above 4096 columns the backward has no registers
+// for the next row: 4096 x 8192 115 us, 4.7 TB/s; above 8192 not for its own
+// sixteen elements a lane: 2048 x 16384 436 us, 1.2 TB/s (forward 64 us).  Backward of
+// 20000 x 128 float32: 17 us for 12 at the copy's rate, workgroups of two steps each,
+// whose first loads and last sums nothing covers.
 #pragma once
 #include <hip/hip_runtime.h>
 

@@ -104,7 +104,8 @@ embedding_fwd_kernel(const T* __restrict__ table, const Index* __restrict__ toke
 // Workgroup (s, t) sums segment s of the positions over the columns of tile t.
 // A lane owns one 16-byte chunk of columns of its group's copy of the table,
 // acc[group][row][tile columns]: no two lanes share an address.  50000 positions
-// into 10 rows of 128 f32 on one MI355X: 11 us and 4 us for the segments' sums;
+// into 10 rows of 128 f32 on one MI355X: 11 us and 3 us for the segments' sums (a
+// group's twelve rows in three rounds of loads, one after another);
 // sorted as a large table 27 us.
 template <typename T, typename Index>
 __global__ void __launch_bounds__(1024 / Chunk<T>::kN)
@@ -564,8 +565,8 @@ __device__ __forceinline__ void sum_range(const T* __restrict__ g, int64_t g_str
 // sums are added in order: the few frequent tokens would otherwise be the
 // kernel's last groups.  (kAlone 8, 16, 32: 100000 tokens spread evenly over 16000
 // rows of 64 bf16 87, 47, 45 us, a text's 65, 59, 59; 16384 of a text over 50000
-// 28, 28, 31.)  Few: one row per workgroup.  32768 x 1024 bf16, 16384 tokens: 24 us, 4.2 TB/s (one row per
-// 64 lanes, empty or not: 41 us).
+// 28, 28, 31.)  Few: one row per workgroup.  32768 x 1024 bf16, 16384 tokens: 20 us,
+// 3.9 TB/s (one row per 64 lanes, empty or not: 41 us).
 template <typename T, bool Few>
 __global__ void __launch_bounds__(256)
 embedding_rows_kernel(const T* __restrict__ g, int64_t g_stride, const uint32_t* __restrict__ pos,
