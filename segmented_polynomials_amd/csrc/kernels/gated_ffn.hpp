@@ -368,7 +368,7 @@ template <typename Dt>
 int ffn_fwd(const GatedFfnArgs& a, size_t* bytes) {
   const bool worst = bytes != nullptr;
   const hipStream_t st = static_cast<hipStream_t>(a.stream);
-  if (takes_few_rows<Dt>(a.n, a.d_in, a.hidden)) {
+  if (takes_few_rows<Dt>(a.n, a.hidden, a.d_out)) {
     Arena arena{static_cast<char*>(a.workspace)};
     const int64_t ldh = round_up(a.hidden, 8);
     void* h = arena.take<typename Dt::T>(a.n * ldh);

@@ -19,16 +19,23 @@
 namespace segpoly {
 namespace kern {
 
-// Which calls take this form: up to 16 rows all, up to 32 those of float32 and those
-// whose three weights stay small.  One MI355X, us here and in tiles (gemm_tile.hpp):
-//                          bf16 1 row      16           32           48 rows    f32 32     48
-//   128 x 512 x 128          5.6,  8.2    6.0,  8.4    7.8,  8.6   10.5,  8.7   16,  19   23,  19
-//   512 x 2048 x 4096        9.0, 14.3   10.9, 14.6   14.5, 15.1   19.2, 15.5   35,  47   50,  47
-//   1024 x 4096 x 1024      11.8, 16.6   15.7, 17.1   21.8, 17.4   30.3, 18.1   59,  55   88,  56
-//   2048 x 5632 x 2048      20.8, 23.2   27.6, 23.8   39.1, 24.1   54.9, 24.3  112, 129  167, 131
+// Which calls take this form: up to 16 rows all, up to 32 those whose second
+// product's long sums over few outputs do not keep too few workgroups busy.  One
+// MI355X, us here and in tiles (gemm_tile.hpp):
+//                          bf16 8-16 rows   17           32          f32 17       32
+//   128 x 512 x 128          6.0,  8.4    7.4,  8.6    7.8,  8.6   15,  18    16,  19
+//   4096 x 1024 x 512       17.7, 25.7   20.7, 25.9   23.4, 26.0   63,  86    66,  89
+//   512 x 2048 x 4096       10.9, 14.6   13.0, 14.7   14.5, 15.1   33,  45    35,  47
+//   1024 x 2048 x 1024      11.5, 16.3   13.9, 16.5   15.6, 16.6   38,  45    40,  46
+//   512 x 4096 x 512        13.7, 15.0   16.0, 15.1   18.7, 15.4   48,  38    52,  40
+//   1024 x 4096 x 1024      15.7, 17.1   18.5, 17.0   21.8, 17.4   57,  53    59,  55
+//   2048 x 5632 x 2048      27.6, 23.8   33.3, 23.7   39.1, 24.1  110, 129   112, 129
+//   128 x 4096 x 8192       21.5, 20.8   25.0, 20.9   29.2, 21.3   64, 122    68, 124
+// One row of the last but one 20.8 and 23.2.  48 rows: 128 x 512 x 128 bf16 10.5, 8.7,
+// 1024 x 4096 x 1024 f32 88, 56.
 template <typename Dt>
-bool takes_few_rows(int64_t n, int64_t d_in, int64_t hidden) {
-  return n <= 16 || (n <= 32 && (Dt::kPlanes > 1 || hidden * d_in <= int64_t{1} << 21));
+bool takes_few_rows(int64_t n, int64_t hidden, int64_t d_out) {
+  return n <= 16 || (n <= 32 && (hidden <= 2048 || (Dt::kPlanes > 1 && hidden <= 3 * d_out)));
 }
 
 struct RowsArgs {
