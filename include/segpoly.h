@@ -824,6 +824,95 @@ int gated_ffn_bwd(int dtype, int act, const void* x, int64_t x_stride, const voi
                   int64_t hidden, int64_t d_out, void* grad_x, void* grad_w_gate, void* grad_w_up, void* grad_w_down,
                   void* workspace, size_t workspace_bytes, void* stream);
 
+#define SEGPOLY_DROPOUT_ELEMENT 0 /* one draw per element */
+#define SEGPOLY_DROPOUT_ROW 1     /* one draw per row */
+
+/*
+ * dropout_fwd: out = residual + keep x / (1 - p).  Whether an element is kept
+ * depends on the seed, the offset, its row and its column alone:
+ *   keep[row, col] = word col % 4 of Philox4x32-10 (Salmon et al. 2011) with the
+ *   key (seed's low, high half) and the counter (col / 4, row, offset's low,
+ *   high half), not below the integer nearest to p 2^32;
+ * with DROPOUT_ROW an element has its row's first column's (whole rows are
+ * dropped: a residual branch of some nodes).  What is dropped counts as zero
+ * whatever it is, NaN included; p = 0 keeps all, p = 1 none.  Different layers and
+ * steps take different offsets.
+ *   x, residual (or NULL), out [n, dim] T; out may be x or residual itself.
+ *   state: NULL, or two int64 on the device that are added to seed and offset (a
+ *   captured graph takes them as they are at each replay).
+ */
+int dropout_fwd(int dtype, int mode, const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                double p, uint64_t seed, uint64_t offset, const void* state, int64_t n, int64_t dim, void* out,
+                int64_t out_stride, void* stream);
+
+/*
+ * dropout_bwd: grad_x = keep grad_out / (1 - p), with the mask made again from
+ * the forward's mode, p, seed, offset and state (the residual's gradient is
+ * grad_out itself).  grad_x may be grad_out itself.
+ */
+int dropout_bwd(int dtype, int mode, const void* grad_out, int64_t grad_out_stride, double p, uint64_t seed,
+                uint64_t offset, const void* state, int64_t n, int64_t dim, void* grad_x, int64_t grad_x_stride,
+                void* stream);
+
+/* expert_sort_workspace: bytes expert_sort needs (counts of each workgroup; none
+ * for lists that one workgroup orders). */
+int expert_sort_workspace(int64_t entries, int64_t num_experts, size_t* bytes);
+
+/*
+ * expert_sort: the entries e (choice j of row i: e = i k + j) in the order of
+ * their expert, equal ones as they come; those without an expert, outside
+ * [0, num_experts), behind all others.
+ *   experts [entries] int32/int64.  All outputs int32, fully overwritten:
+ *   order [entries]: the entry at each slot.  place [entries]: the slot of each
+ *   entry.  offsets [num_experts + 1]: expert q has the slots from offsets[q] to
+ *   offsets[q + 1]; slots from offsets[num_experts] on have none.  ids [entries]:
+ *   the expert of each slot, -1 without one (the sorted class indices of
+ *   linear_fwd, whose rows out of range are zero).
+ * num_experts at most 2048 (E_UNSUPPORTED above).  With no entries experts, order,
+ * place and ids may be NULL.
+ */
+int expert_sort(const void* experts, int idx_dtype, int64_t entries, int64_t num_experts, void* order, void* place,
+                void* offsets, void* ids, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * expert_dispatch_fwd: rows in the experts' order, xs[place[i, j]] = x[i], zero
+ * rows from slot offsets[num_experts] on.
+ *   x [n, dim] T.  place [n, k], offsets as expert_sort left them (k >= 1).
+ *   xs [n k, dim] T, fully overwritten.
+ * A place outside [0, n k) is passed over, here and below.
+ */
+int expert_dispatch_fwd(int dtype, const void* x, int64_t x_stride, const void* place, const void* offsets,
+                        int64_t num_experts, int64_t n, int64_t k, int64_t dim, void* xs, void* stream);
+
+/* expert_dispatch_bwd: grad_x[i] = sum over j of grad_xs[place[i, j]], without
+ * slots from offsets[num_experts] on; in the order of j, in float32.
+ *   grad_xs [n k, dim], grad_x [n, dim] T. */
+int expert_dispatch_bwd(int dtype, const void* grad_xs, int64_t grad_xs_stride, const void* place, const void* offsets,
+                        int64_t num_experts, int64_t n, int64_t k, int64_t dim, void* grad_x, int64_t grad_x_stride,
+                        void* stream);
+
+/*
+ * expert_combine_fwd: rows back in their own order with weights,
+ *   out[i] = residual[i] + sum over j of weights[i, j] ys[place[i, j]],
+ * without slots from offsets[num_experts] on, whatever they hold.
+ *   ys [n k, dim] T.  weights [n, k] float32.  residual [n, dim] T or NULL.
+ *   out [n, dim] T; it may be residual itself.
+ */
+int expert_combine_fwd(int dtype, const void* ys, int64_t ys_stride, const void* place, const void* offsets,
+                       int64_t num_experts, const void* weights, const void* residual, int64_t residual_stride, int64_t n,
+                       int64_t k, int64_t dim, void* out, int64_t out_stride, void* stream);
+
+/*
+ * expert_combine_bwd: vector-Jacobian product of expert_combine_fwd,
+ *   grad_ys[place[i, j]] = weights[i, j] grad_out[i] (zero rows without an expert)
+ *   [n k, dim] T, grad_weights[i, j] = <grad_out[i], ys[place[i, j]]> (zero without
+ *   an expert) [n, k] float32; both fully overwritten.  The residual's gradient is
+ *   grad_out itself.
+ */
+int expert_combine_bwd(int dtype, const void* grad_out, int64_t grad_out_stride, const void* ys, int64_t ys_stride,
+                       const void* place, const void* offsets, int64_t num_experts, const void* weights, int64_t n,
+                       int64_t k, int64_t dim, void* grad_ys, void* grad_weights, void* stream);
+
 /* ------------------------------------------------------- spherical harmonics */
 
 /*

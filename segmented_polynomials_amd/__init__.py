@@ -5,7 +5,9 @@ The functions keep the names of the C ABI in ``include/segpoly.h``:
 ``symcon_bwd`` / ``linear_create`` / ``linear_fwd`` / ``linear_bwd`` / ``fctp_create`` /
 ``fctp_fwd`` / ``fctp_bwd`` / ``sh_fwd`` / ``sh_bwd`` / ``embedding_fwd`` /
 ``embedding_bwd`` / ``block_norm_fwd`` / ``block_norm_bwd`` / ``gated_ffn_fwd`` /
-``gated_ffn_bwd``.  Every
+``gated_ffn_bwd`` / ``dropout_fwd`` / ``dropout_bwd`` / ``expert_sort`` /
+``expert_dispatch_fwd`` / ``expert_dispatch_bwd`` / ``expert_combine_fwd`` /
+``expert_combine_bwd``.  Every
 step of the computation runs in the library's HIP kernels; PyTorch only
 supplies device memory and the current stream.  There is no CPU fallback:
 importing this package fails loudly if the library has not been built.
@@ -41,7 +43,8 @@ EXPORTS = ("tp_create", "tp_query", "tp_irreps_out", "tp_path_info", "tp_path_cg
            "linear_bwd_workspace", "linear_bwd", "linear_destroy", "fctp_create", "fctp_query", "fctp_path_info",
            "fctp_fwd", "fctp_bwd_workspace", "fctp_bwd", "fctp_fwd_per_sample", "fctp_bwd_per_sample", "fctp_conv_fwd", "fctp_conv_bwd_workspace", "fctp_conv_bwd", "fctp_destroy", "edge_scalars_fwd", "edge_scalars_bwd",
            "embedding_fwd", "embedding_bwd_workspace", "embedding_bwd", "block_norm_fwd", "block_norm_bwd_workspace",
-           "block_norm_bwd", "gated_ffn_workspace", "gated_ffn_fwd", "gated_ffn_bwd", "sh_fwd", "sh_bwd", "segpoly_real_cg",
+           "block_norm_bwd", "gated_ffn_workspace", "gated_ffn_fwd", "gated_ffn_bwd", "dropout_fwd", "dropout_bwd", "expert_sort_workspace", "expert_sort", "expert_dispatch_fwd",
+           "expert_dispatch_bwd", "expert_combine_fwd", "expert_combine_bwd", "sh_fwd", "sh_bwd", "segpoly_real_cg",
            "segpoly_last_error", "segpoly_version")
 
 
@@ -74,6 +77,7 @@ def _load():
     _hip_runtime_of_torch()
     lib = ctypes.CDLL(LIB_PATH)
     vp, i64, c_int, c_uint = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint
+    u64 = ctypes.c_uint64
     p64 = ctypes.POINTER(ctypes.c_int64)
     pd = ctypes.POINTER(ctypes.c_double)
     sig = {
@@ -135,6 +139,14 @@ def _load():
         "gated_ffn_fwd": [c_int, c_int, vp, i64, vp, vp, vp, i64, i64, i64, i64, vp, i64, vp, ctypes.c_size_t, vp],
         "gated_ffn_bwd": [c_int, c_int, vp, i64, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp,
                           ctypes.c_size_t, vp],
+        "dropout_fwd": [c_int, c_int, vp, i64, vp, i64, ctypes.c_double, u64, u64, vp, i64, i64, vp, i64, vp],
+        "dropout_bwd": [c_int, c_int, vp, i64, ctypes.c_double, u64, u64, vp, i64, i64, vp, i64, vp],
+        "expert_sort_workspace": [i64, i64, ctypes.POINTER(ctypes.c_size_t)],
+        "expert_sort": [vp, c_int, i64, i64, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
+        "expert_dispatch_fwd": [c_int, vp, i64, vp, vp, i64, i64, i64, i64, vp, vp],
+        "expert_dispatch_bwd": [c_int, vp, i64, vp, vp, i64, i64, i64, i64, vp, i64, vp],
+        "expert_combine_fwd": [c_int, vp, i64, vp, vp, i64, vp, vp, i64, i64, i64, i64, vp, i64, vp],
+        "expert_combine_bwd": [c_int, vp, i64, vp, i64, vp, vp, i64, vp, i64, i64, i64, vp, vp, vp],
         "sh_fwd": [c_int, c_int, c_int, vp, i64, vp, vp],
         "sh_bwd": [c_int, c_int, c_int, vp, vp, i64, vp, vp],
         "segpoly_real_cg": [c_int, c_int, c_int, pd],
@@ -1246,3 +1258,167 @@ def gated_ffn_bwd(x, w_gate, w_up, w_down, grad_out, act="silu", need_dx=True, n
                              d_in, hidden, d_out, _adr(gx), _adr(gwg), _adr(gwu), _adr(gwd), _adr(workspace), nbytes,
                              _raw_stream(x.get_device())))
     return gx, gwg, gwu, gwd
+
+
+# The library launches on the current device: that of the tensors is made
+# current for the call where it is another.
+def _call(index, fn, *args):
+    import torch
+    if torch._C._cuda_getDevice() == index:
+        _check(fn(*args, _raw_stream(index)))
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, _raw_stream(index)))
+
+
+_DROPOUT_MODES = {"element": 0, "row": 1}
+
+
+def _dropout(name, fn, x, p, seed, offset, residual, mode, out):
+    import torch
+    dt = _channel_dtype(x)
+    if mode not in _DROPOUT_MODES:
+        raise ValueError("mode is 'element' or 'row'")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [n, dim]")
+    n, d = x.shape
+    xs = _rows(name, x, x, n, d)
+    rs = 0 if residual is None else _rows("residual", residual, x, n, d)
+    state = None
+    if isinstance(seed, torch.Tensor):
+        state, seed = seed, 0
+        if state.dtype != torch.int64 or state.shape != (2,) or state.get_device() != x.get_device() \
+                or not state.is_contiguous():
+            raise ValueError(f"seed must be an integer, or a contiguous int64 tensor of two on {x.device}")
+    if out is None:
+        out = x.new_empty((n, d))
+        os_ = d
+    else:
+        os_ = _rows("out", out, x, n, d, output=True)
+    seed, offset = seed & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF
+    if fn is lib.dropout_fwd:
+        _call(x.get_device(), fn, dt, _DROPOUT_MODES[mode], _adr(x), xs, _adr(residual), rs, p, seed, offset, _adr(state),
+              n, d, _adr(out), os_)
+    else:
+        _call(x.get_device(), fn, dt, _DROPOUT_MODES[mode], _adr(x), xs, p, seed, offset, _adr(state), n, d, _adr(out), os_)
+    return out
+
+
+def dropout_fwd(x, p, seed, offset=0, residual=None, mode="element", out=None):
+    """out = residual + keep * x / (1 - p) with a mask that is never stored.
+    ``x`` [n, dim] with contiguous rows; ``seed`` and ``offset`` integers, or
+    ``seed`` an int64 tensor (seed, offset) on the device, to which ``offset``
+    is added (a captured graph takes its values at each replay); ``mode``
+    'element', or 'row' to keep or drop whole rows.  Every layer and step needs
+    an offset of its own.  ``out`` may be ``x`` or ``residual``."""
+    return _dropout("x", lib.dropout_fwd, x, p, seed, offset, residual, mode, out)
+
+
+def dropout_bwd(grad_out, p, seed, offset=0, mode="element", grad_x=None):
+    """Gradient of ``dropout_fwd`` to x, with the mask of the same ``p``,
+    ``seed``, ``offset`` and ``mode`` (the residual's is ``grad_out``)."""
+    return _dropout("grad_out", lib.dropout_bwd, grad_out, p, seed, offset, None, mode, grad_x)
+
+
+@functools.lru_cache(256)
+def expert_sort_workspace(entries, num_experts):
+    """Bytes of workspace of ``expert_sort``."""
+    v = ctypes.c_size_t()
+    _check(lib.expert_sort_workspace(entries, num_experts, ctypes.byref(v)))
+    return v.value
+
+
+def expert_sort(experts, num_experts, workspace=None):
+    """The entries of ``experts`` [n, k] int32/int64, by expert: (order, place,
+    offsets, ids), all int32.  ``order`` [n * k]: the entry (i * k + j) of each
+    slot; ``place`` [n, k]: the slot of each entry; ``offsets``
+    [num_experts + 1]: the slots of expert q are offsets[q] to offsets[q + 1];
+    ``ids`` [n * k]: the expert of each slot, the class indices of
+    ``linear_fwd``.  Equal ones keep their order; entries outside
+    [0, num_experts) come last and have the id -1."""
+    import torch
+    idx = _index_dtype(experts)
+    if experts.dim() != 2 or not experts.is_contiguous() or experts.get_device() < 0:
+        raise ValueError("experts must be a contiguous [n, k] tensor on a GPU")
+    entries = experts.numel()
+    nbytes = expert_sort_workspace(entries, num_experts)
+    dev, i32 = experts.device, torch.int32
+    order = torch.empty(entries, dtype=i32, device=dev)
+    place = torch.empty(experts.shape, dtype=i32, device=dev)
+    offsets = torch.empty(num_experts + 1, dtype=i32, device=dev)
+    ids = torch.empty(entries, dtype=i32, device=dev)
+    workspace, nbytes = _channel_workspace(workspace, nbytes, dev)
+    _call(experts.get_device(), lib.expert_sort, _adr(experts), idx, entries, num_experts, _adr(order), _adr(place),
+          _adr(offsets), _adr(ids), _adr(workspace), nbytes)
+    return order, place, offsets, ids
+
+
+def _expert_rows(like, place, offsets):
+    import torch
+    for name, a, dims in (("place", place, 2), ("offsets", offsets, 1)):
+        if a.dtype != torch.int32 or a.dim() != dims or a.get_device() != like.get_device() or not a.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimensions on {like.device}")
+    if like.dim() != 2:
+        raise ValueError("rows must be [n, dim]")
+    return _channel_dtype(like), place.shape[0], place.shape[1], like.shape[1], offsets.shape[0] - 1
+
+
+def _weights(weights, like, n, k):
+    if weights.dtype != _f32() or weights.get_device() != like.get_device() or weights.shape != (n, k) \
+            or not weights.is_contiguous():
+        raise ValueError(f"weights must be a contiguous float32 tensor [{n}, {k}] on {like.device}")
+
+
+def _out_rows(name, out, like, n, d):
+    """An output of rows, made or checked, and its row stride."""
+    if out is None:
+        return like.new_empty((n, d)), d
+    return out, _rows(name, out, like, n, d, output=True)
+
+
+def expert_dispatch_fwd(x, place, offsets):
+    """Rows in the experts' order: xs[place[i, j]] = x[i], zero rows for
+    entries without an expert; ``x`` [n, dim], ``place`` and ``offsets`` of
+    ``expert_sort``, xs [n * k, dim]."""
+    dt, n, k, d, num = _expert_rows(x, place, offsets)
+    xs = _rows("x", x, x, n, d)
+    out = x.new_empty((n * k, d))
+    _call(x.get_device(), lib.expert_dispatch_fwd, dt, _adr(x), xs, _adr(place), _adr(offsets), num, n, k, d, _adr(out))
+    return out
+
+
+def expert_dispatch_bwd(grad_xs, place, offsets, grad_x=None):
+    """Gradient of ``expert_dispatch_fwd``: the sum of a row's copies'."""
+    dt, n, k, d, num = _expert_rows(grad_xs, place, offsets)
+    gs = _rows("grad_xs", grad_xs, grad_xs, n * k, d)
+    grad_x, stride = _out_rows("grad_x", grad_x, grad_xs, n, d)
+    _call(grad_xs.get_device(), lib.expert_dispatch_bwd, dt, _adr(grad_xs), gs, _adr(place), _adr(offsets), num, n, k, d,
+          _adr(grad_x), stride)
+    return grad_x
+
+
+def expert_combine_fwd(ys, place, offsets, weights, residual=None, out=None):
+    """Rows back in their own order: out[i] = residual[i] + sum over j of
+    weights[i, j] * ys[place[i, j]], without entries that have no expert;
+    ``ys`` [n * k, dim], ``weights`` [n, k] float32, ``residual`` [n, dim].
+    ``out`` may be ``residual``."""
+    dt, n, k, d, num = _expert_rows(ys, place, offsets)
+    ss = _rows("ys", ys, ys, n * k, d)
+    _weights(weights, ys, n, k)
+    rs = 0 if residual is None else _rows("residual", residual, ys, n, d)
+    out, stride = _out_rows("out", out, ys, n, d)
+    _call(ys.get_device(), lib.expert_combine_fwd, dt, _adr(ys), ss, _adr(place), _adr(offsets), num, _adr(weights),
+          _adr(residual), rs, n, k, d, _adr(out), stride)
+    return out
+
+
+def expert_combine_bwd(grad_out, ys, place, offsets, weights):
+    """Gradients (grad_ys, grad_weights) of ``expert_combine_fwd`` (the
+    residual's is ``grad_out``)."""
+    dt, n, k, d, num = _expert_rows(ys, place, offsets)
+    ss, gs = _rows("ys", ys, ys, n * k, d), _rows("grad_out", grad_out, ys, n, d)
+    _weights(weights, ys, n, k)
+    grad_ys, grad_weights = ys.new_empty((n * k, d)), weights.new_empty((n, k))
+    _call(ys.get_device(), lib.expert_combine_bwd, dt, _adr(grad_out), gs, _adr(ys), ss, _adr(place), _adr(offsets), num,
+          _adr(weights), n, k, d, _adr(grad_ys), _adr(grad_weights))
+    return grad_ys, grad_weights

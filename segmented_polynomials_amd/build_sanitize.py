@@ -29,7 +29,7 @@ LIB = os.path.join(OUT, "libsegpoly_san.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
 HOST_SOURCES = ["irreps.cpp", "cg.cpp", "tp_descriptor.cpp", "symcon_descriptor.cpp", "capi.cpp", "capi_linear.cpp",
-                "capi_sh.cpp", "capi_fctp.cpp", "capi_edge.cpp", "capi_channel.cpp"]
+                "capi_sh.cpp", "capi_fctp.cpp", "capi_edge.cpp", "capi_channel.cpp", "capi_rows.cpp"]
 SAN = ["-fsanitize=address,undefined", "-fno-omit-frame-pointer", "-fno-sanitize-recover=undefined"]
 
 

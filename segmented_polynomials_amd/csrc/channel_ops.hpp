@@ -1,5 +1,5 @@
 // Arguments of the invariant-channel kernels (embedding, block norm, gated
-// feed-forward): host and device.
+// feed-forward, dropout, routing to experts): host and device.
 #pragma once
 #include <cstddef>
 #include <cstdint>
@@ -97,5 +97,56 @@ struct GatedFfnArgs {
 size_t gated_ffn_workspace_bytes(int dtype, int64_t n, int64_t d_in, int64_t hidden, int64_t d_out, bool backward);
 int launch_gated_ffn_fwd(const GatedFfnArgs& a);
 int launch_gated_ffn_bwd(const GatedFfnArgs& a);
+
+struct DropoutArgs {
+  const void *x, *residual;      // [n, dim]; residual may be null
+  void* out;
+  int64_t n, dim, x_stride, residual_stride, out_stride;
+  uint64_t seed, offset;
+  const int64_t* state;          // device, two numbers added to seed and offset, or null
+  uint32_t below;                // words below it drop
+  int drop_all;
+  float scale;
+  int dtype, rows;               // rows: one draw a row
+  void* stream;
+};
+int launch_dropout(const DropoutArgs& a);
+
+// Entries that one workgroup of the expert sort ranks: 16 waves of up to 16
+// times 64.
+constexpr int kSortWaves = 16;
+constexpr int kMaxExperts = 2048;
+
+struct ExpertSortArgs {
+  const void* experts;           // [entries]
+  int64_t entries;
+  int num, idx;
+  int *order, *place, *offsets, *ids;
+  int* counts;                   // workspace: [blocks + 1][num + 1]
+  void* stream;
+};
+// workgroups of the sort, and of 64 entries each of their waves takes how many
+struct ExpertSortPlan {
+  int64_t blocks;
+  int chunks, waves;
+  size_t bytes;
+};
+ExpertSortPlan expert_sort_plan(int64_t entries, int64_t num);
+int launch_expert_sort(const ExpertSortArgs& a);
+
+struct ExpertRowsArgs {
+  const void *x, *ys, *residual;      // rows by entry's row; rows by slot; [n, dim] or null
+  const float* weights;               // [n, k]
+  const int* place;                   // [n, k]
+  const int* total;                   // one number: slots from it on have no expert
+  void* out;                          // by row or by slot
+  float* grad_weights;
+  int64_t n, k, dim, x_stride, ys_stride, residual_stride, out_stride;
+  int dtype;
+  void* stream;
+};
+int launch_expert_dispatch(const ExpertRowsArgs& a);      // out[place] = x
+int launch_expert_combine(const ExpertRowsArgs& a);       // out = residual + sum of weights (1 if null) ys[place]
+int launch_expert_combine_bwd(const ExpertRowsArgs& a);   // out[place] = weights x, grad_weights = <x, ys[place]>
 
 }  // namespace segpoly

@@ -88,12 +88,9 @@ __device__ __forceinline__ void load_chunk(const T* row, int c, int width, float
 
 // the part of a chunk within the row: 16 bytes, or the halves its count names
 template <typename T>
-__device__ __forceinline__ void store_chunk(T* row, int c, int width, const float* v) {
+__device__ __forceinline__ void store_elements(T* row, int c, int width, T (&t)[Chunk<T>::kN]) {
   constexpr int N = Chunk<T>::kN;
   if (c >= width) return;
-  T t[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) t[i] = static_cast<T>(v[i]);
   T* p = row + c;
   if (c + N <= width) {
     __builtin_memcpy(p, t, 16);
@@ -114,6 +111,20 @@ __device__ __forceinline__ void store_chunk(T* row, int c, int width, const floa
     t[0] = t[2];
   }
   if (n & 1) p[0] = t[0];
+}
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* row, int c, int width, const float* v) {
+  T t[Chunk<T>::kN];
+#pragma unroll
+  for (int i = 0; i < Chunk<T>::kN; ++i) t[i] = static_cast<T>(v[i]);
+  store_elements<T>(row, c, width, t);
+}
+// a settled chunk, bit for bit
+template <typename T>
+__device__ __forceinline__ void store_raw(T* row, int c, int width, u32x4 r) {
+  T t[Chunk<T>::kN];
+  __builtin_memcpy(t, &r, 16);
+  store_elements<T>(row, c, width, t);
 }
 
 // ------------------------------------------------------------ sums over lanes
