@@ -824,6 +824,40 @@ int gated_ffn_bwd(int dtype, int act, const void* x, int64_t x_stride, const voi
                   int64_t hidden, int64_t d_out, void* grad_x, void* grad_w_gate, void* grad_w_up, void* grad_w_down,
                   void* workspace, size_t workspace_bytes, void* stream);
 
+#define SEGPOLY_ACT_NONE 4 /* dense only */
+
+/* dense_workspace: bytes dense_fwd (backward == 0) or dense_bwd (backward != 0)
+ * needs: float32 parts of long sums, copies of operands that do not suit 16-byte
+ * accesses (float32: three bf16 planes of each), the backward's gradient before
+ * the activation and its column sums.  Sized for any strides and alignments. */
+int dense_workspace(int dtype, int act, int64_t n, int64_t d_in, int64_t d_out, int backward, size_t* bytes);
+
+/*
+ * dense_fwd: out = act(x w^T + bias) + residual.
+ *   x [n, d_in], w [d_out, d_in], bias [d_out] or NULL, residual [n, d_out] or
+ *   NULL, out [n, d_out] (may be residual itself), all T.  act: SEGPOLY_ACT_*.
+ * Widths and, of more than one row, x's row stride are at most 2^21
+ * (E_UNSUPPORTED, E_INVALID above); out, x and w have fewer than 2^24 tiles of
+ * 64 x 64 (E_UNSUPPORTED above).  Products on the matrix cores with float32 sums, float32
+ * operands with 24 bits.
+ */
+int dense_fwd(int dtype, int act, const void* x, int64_t x_stride, const void* w, const void* bias, const void* residual,
+              int64_t residual_stride, int64_t n, int64_t d_in, int64_t d_out, void* out, int64_t out_stride,
+              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dense_bwd: vector-Jacobian product of dense_fwd for grad_out [n, d_out]; the
+ * product is computed again where the activation's slope needs it (not with
+ * ACT_NONE, which reads no bias), and the gradient before the activation is held
+ * in T's precision.  grad_x [n, d_in], grad_w [d_out, d_in], grad_bias [d_out],
+ * T, any of them NULL but not all; fully overwritten.  The residual's gradient is
+ * grad_out itself.  With n == 0 the weight's and the bias's gradients are zero,
+ * and no input or workspace is read (all may be NULL).
+ */
+int dense_bwd(int dtype, int act, const void* x, int64_t x_stride, const void* w, const void* bias, const void* grad_out,
+              int64_t grad_out_stride, int64_t n, int64_t d_in, int64_t d_out, void* grad_x, void* grad_w,
+              void* grad_bias, void* workspace, size_t workspace_bytes, void* stream);
+
 #define SEGPOLY_DROPOUT_ELEMENT 0 /* one draw per element */
 #define SEGPOLY_DROPOUT_ROW 1     /* one draw per row */
 

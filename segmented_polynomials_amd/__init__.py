@@ -5,7 +5,7 @@ The functions keep the names of the C ABI in ``include/segpoly.h``:
 ``symcon_bwd`` / ``linear_create`` / ``linear_fwd`` / ``linear_bwd`` / ``fctp_create`` /
 ``fctp_fwd`` / ``fctp_bwd`` / ``sh_fwd`` / ``sh_bwd`` / ``embedding_fwd`` /
 ``embedding_bwd`` / ``block_norm_fwd`` / ``block_norm_bwd`` / ``gated_ffn_fwd`` /
-``gated_ffn_bwd`` / ``dropout_fwd`` / ``dropout_bwd`` / ``expert_sort`` /
+``gated_ffn_bwd`` / ``dense_fwd`` / ``dense_bwd`` / ``dropout_fwd`` / ``dropout_bwd`` / ``expert_sort`` /
 ``expert_dispatch_fwd`` / ``expert_dispatch_bwd`` / ``expert_combine_fwd`` /
 ``expert_combine_bwd``.  Every
 step of the computation runs in the library's HIP kernels; PyTorch only
@@ -43,7 +43,7 @@ EXPORTS = ("tp_create", "tp_query", "tp_irreps_out", "tp_path_info", "tp_path_cg
            "linear_bwd_workspace", "linear_bwd", "linear_destroy", "fctp_create", "fctp_query", "fctp_path_info",
            "fctp_fwd", "fctp_bwd_workspace", "fctp_bwd", "fctp_fwd_per_sample", "fctp_bwd_per_sample", "fctp_conv_fwd", "fctp_conv_bwd_workspace", "fctp_conv_bwd", "fctp_destroy", "edge_scalars_fwd", "edge_scalars_bwd",
            "embedding_fwd", "embedding_bwd_workspace", "embedding_bwd", "block_norm_fwd", "block_norm_bwd_workspace",
-           "block_norm_bwd", "gated_ffn_workspace", "gated_ffn_fwd", "gated_ffn_bwd", "dropout_fwd", "dropout_bwd", "expert_sort_workspace", "expert_sort", "expert_dispatch_fwd",
+           "block_norm_bwd", "gated_ffn_workspace", "gated_ffn_fwd", "gated_ffn_bwd", "dense_workspace", "dense_fwd", "dense_bwd", "dropout_fwd", "dropout_bwd", "expert_sort_workspace", "expert_sort", "expert_dispatch_fwd",
            "expert_dispatch_bwd", "expert_combine_fwd", "expert_combine_bwd", "sh_fwd", "sh_bwd", "segpoly_real_cg",
            "segpoly_last_error", "segpoly_version")
 
@@ -139,6 +139,9 @@ def _load():
         "gated_ffn_fwd": [c_int, c_int, vp, i64, vp, vp, vp, i64, i64, i64, i64, vp, i64, vp, ctypes.c_size_t, vp],
         "gated_ffn_bwd": [c_int, c_int, vp, i64, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp,
                           ctypes.c_size_t, vp],
+        "dense_workspace": [c_int, c_int, i64, i64, i64, c_int, ctypes.POINTER(ctypes.c_size_t)],
+        "dense_fwd": [c_int, c_int, vp, i64, vp, vp, vp, i64, i64, i64, i64, vp, i64, vp, ctypes.c_size_t, vp],
+        "dense_bwd": [c_int, c_int, vp, i64, vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, ctypes.c_size_t, vp],
         "dropout_fwd": [c_int, c_int, vp, i64, vp, i64, ctypes.c_double, u64, u64, vp, i64, i64, vp, i64, vp],
         "dropout_bwd": [c_int, c_int, vp, i64, ctypes.c_double, u64, u64, vp, i64, i64, vp, i64, vp],
         "expert_sort_workspace": [i64, i64, ctypes.POINTER(ctypes.c_size_t)],
@@ -1269,6 +1272,64 @@ def _call(index, fn, *args):
     else:
         with torch.cuda.device(index):
             _check(fn(*args, _raw_stream(index)))
+
+
+_DENSE_ACTS = {**_ACTS, "none": 4}
+
+
+def _dense_common(x, w, bias, act):
+    dt = _channel_dtype(x)
+    if act not in _DENSE_ACTS:
+        raise ValueError("act is 'none', 'silu', 'gelu', 'relu' or 'sigmoid'")
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must be matrices")
+    n, d_in = x.shape
+    d_out = w.shape[0]
+    stride = _rows("x", x, x, n, d_in)
+    _contiguous("w", w, x, (d_out, d_in))
+    if bias is not None:
+        _contiguous("bias", bias, x, (d_out,))
+    return dt, _DENSE_ACTS[act], n, d_in, d_out, stride
+
+
+@functools.lru_cache(256)
+def dense_workspace(dtype, act, n, d_in, d_out, backward=False):
+    """Bytes of workspace of ``dense_fwd`` / ``dense_bwd``; ``dtype`` one of
+    F32, BF16, F16, ``act`` as there."""
+    v = ctypes.c_size_t()
+    _check(lib.dense_workspace(dtype, _DENSE_ACTS.get(act, act), n, d_in, d_out, int(backward), ctypes.byref(v)))
+    return v.value
+
+
+def dense_fwd(x, w, bias=None, act="none", residual=None, out=None, workspace=None):
+    """out = act(x w^T + bias) + residual; ``x`` [n, d_in] and ``residual``
+    [n, d_out] with contiguous rows, ``w`` [d_out, d_in], ``bias`` [d_out], all of
+    one dtype; ``act`` 'none', 'silu', 'gelu', 'relu' or 'sigmoid'.  ``out`` may
+    be ``residual``."""
+    dt, a, n, d_in, d_out, stride = _dense_common(x, w, bias, act)
+    rs = 0 if residual is None else _rows("residual", residual, x, n, d_out)
+    out, os_ = _out_rows("out", out, x, n, d_out)
+    workspace, nbytes = _channel_workspace(workspace, dense_workspace(dt, a, n, d_in, d_out), x.device)
+    _call(x.get_device(), lib.dense_fwd, dt, a, _adr(x), stride, _adr(w), _adr(bias), _adr(residual), rs, n, d_in, d_out,
+          _adr(out), os_, _adr(workspace), nbytes)
+    return out
+
+
+def dense_bwd(x, w, grad_out, bias=None, act="none", need_dx=True, need_dw=True, workspace=None):
+    """Gradients (grad_x, grad_w, grad_bias) of ``dense_fwd``, None where not
+    needed (``need_dw`` is for the weight and the bias); the residual's is
+    ``grad_out``."""
+    dt, a, n, d_in, d_out, stride = _dense_common(x, w, bias, act)
+    gs = _rows("grad_out", grad_out, x, n, d_out)
+    if not (need_dx or need_dw):
+        return None, None, None
+    gx = x.new_empty((n, d_in)) if need_dx else None
+    gw = w.new_empty((d_out, d_in)) if need_dw else None
+    gb = bias.new_empty(d_out) if need_dw and bias is not None else None
+    workspace, nbytes = _channel_workspace(workspace, dense_workspace(dt, a, n, d_in, d_out, True), x.device)
+    _call(x.get_device(), lib.dense_bwd, dt, a, _adr(x), stride, _adr(w), _adr(bias), _adr(grad_out), gs, n, d_in, d_out,
+          _adr(gx), _adr(gw), _adr(gb), _adr(workspace), nbytes)
+    return gx, gw, gb
 
 
 _DROPOUT_MODES = {"element": 0, "row": 1}

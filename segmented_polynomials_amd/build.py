@@ -65,7 +65,7 @@ def build(verbose=False, jobs=None):
     # 2. compile
     jobs_list = []
     for s in HOST_SOURCES + ["capi.cpp", "capi_linear.cpp", "capi_sh.cpp", "capi_fctp.cpp", "capi_edge.cpp",
-                             "capi_channel.cpp", "capi_rows.cpp"]:
+                             "capi_channel.cpp", "capi_rows.cpp", "capi_dense.cpp"]:
         jobs_list.append(["g++", *HOST_FLAGS, *inc, "-c", os.path.join(CSRC, s),
                           "-o", os.path.join(obj, s + ".o")])
     jobs_list.append(["g++", *HOST_FLAGS, *inc, "-c", os.path.join(gen, "registry.cpp"),
@@ -74,7 +74,8 @@ def build(verbose=False, jobs=None):
                                                                 "embedding.hip", "block_norm.hip", "block_norm_bf16.hip",
                                                                 "block_norm_f16.hip", "block_norm_f32.hip", "gated_ffn.hip", "gated_ffn_bf16.hip",
                                                                 "gated_ffn_f16.hip", "gated_ffn_f32.hip", "dropout.hip",
-                                                                "experts.hip")]
+                                                                "experts.hip", "dense.hip", "dense_bf16.hip",
+                                                                "dense_f16.hip", "dense_f32.hip")]
     kernels.append(os.path.join(CSRC, "noalloc.hip"))
     for h in kernels + gen_hip:
         jobs_list.append([hipcc, *HIP_FLAGS, *inc, "-c", h,

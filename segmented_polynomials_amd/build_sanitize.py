@@ -29,7 +29,7 @@ LIB = os.path.join(OUT, "libsegpoly_san.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
 HOST_SOURCES = ["irreps.cpp", "cg.cpp", "tp_descriptor.cpp", "symcon_descriptor.cpp", "capi.cpp", "capi_linear.cpp",
-                "capi_sh.cpp", "capi_fctp.cpp", "capi_edge.cpp", "capi_channel.cpp", "capi_rows.cpp"]
+                "capi_sh.cpp", "capi_fctp.cpp", "capi_edge.cpp", "capi_channel.cpp", "capi_rows.cpp", "capi_dense.cpp"]
 SAN = ["-fsanitize=address,undefined", "-fno-omit-frame-pointer", "-fno-sanitize-recover=undefined"]
 
 
@@ -65,7 +65,9 @@ def run_tests():
     _run([sys.executable, "-m", "pytest", "-x", "-q", "-p", "no:cacheprovider",
           os.path.join(ROOT, "tests", "test_capi_host.py"),
           os.path.join(ROOT, "tests", "test_capi_channel_host.py"),
-          os.path.join(ROOT, "tests", "test_capi_channel_edges.py")], env=env)
+          os.path.join(ROOT, "tests", "test_capi_channel_edges.py"),
+          os.path.join(ROOT, "tests", "test_capi_rows_host.py"),
+          os.path.join(ROOT, "tests", "test_capi_dense_host.py")], env=env)
 
 
 if __name__ == "__main__":

@@ -1,5 +1,5 @@
 // Arguments of the invariant-channel kernels (embedding, block norm, gated
-// feed-forward, dropout, routing to experts): host and device.
+// feed-forward, dense layer, dropout, routing to experts): host and device.
 #pragma once
 #include <cstddef>
 #include <cstdint>
@@ -80,7 +80,7 @@ int64_t block_norm_parts(int64_t n, int64_t dim);
 int launch_block_norm_fwd(const BlockNormArgs& a);
 int launch_block_norm_bwd(const BlockNormArgs& a);
 
-enum : int { kActSilu = 0, kActGelu = 1, kActRelu = 2, kActSigmoid = 3 };
+enum : int { kActSilu = 0, kActGelu = 1, kActRelu = 2, kActSigmoid = 3, kActNone = 4 };  // none: dense only
 
 struct GatedFfnArgs {
   const void *x, *w_gate, *w_up, *w_down;  // [n, d_in], [hidden, d_in] twice, [d_out, hidden]
@@ -97,6 +97,22 @@ struct GatedFfnArgs {
 size_t gated_ffn_workspace_bytes(int dtype, int64_t n, int64_t d_in, int64_t hidden, int64_t d_out, bool backward);
 int launch_gated_ffn_fwd(const GatedFfnArgs& a);
 int launch_gated_ffn_bwd(const GatedFfnArgs& a);
+
+struct DenseArgs {
+  const void *x, *w, *bias, *residual;  // [n, d_in], [d_out, d_in], [d_out], [n, d_out]; the last two may be null
+  const void* gout;                     // backward: [n, d_out]
+  void* out;                            // forward: [n, d_out]
+  void *gx, *gw, *gbias;                // backward, contiguous, any null
+  int64_t n, d_in, d_out;
+  int64_t x_stride, residual_stride, gout_stride, out_stride;
+  int dtype, act;
+  void* workspace;
+  void* stream;
+};
+// workspace bytes for any strides and alignments of these sizes; none for no rows
+size_t dense_workspace_bytes(int dtype, int act, int64_t n, int64_t d_in, int64_t d_out, bool backward);
+int launch_dense_fwd(const DenseArgs& a);
+int launch_dense_bwd(const DenseArgs& a);
 
 struct DropoutArgs {
   const void *x, *residual;      // [n, dim]; residual may be null

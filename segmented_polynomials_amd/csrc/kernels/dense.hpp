@@ -1,0 +1,199 @@
+// The dense layer, out = act(x W^T + bias) + residual, and its gradient as tile
+// products (gemm_tile.hpp), for one element type per translation unit:
+//   forward   one product, bias, activation and residual its epilogue
+//             (few rows: gemm_rows.hpp)
+//   backward  d = g act'(x W^T + bias)      the product again, the slope and the
+//                                           gradient its epilogue; without an
+//                                           activation d is g itself
+//             dx = d W, dW = d^T x, dbias = sums of d's columns
+// Between the products d is held in the operands' type, as it is an operand of
+// matrix instructions: one rounding of a term of a long sum, the size of the
+// inputs' own (float16 in scaled blocks, float32 in three planes, gemm_tile.hpp).
+// The column sums are of d before that rounding: each wave of the product leaves
+// its rows' in float32, a second launch adds them in order.
+#pragma once
+#include <algorithm>
+
+#include "column_sums.hpp"
+#include "gemm_plan.hpp"
+#include "gemm_rows.hpp"
+
+namespace segpoly {
+namespace kern {
+
+// The shares of a long sum, in order, then the epilogue: four columns a lane.
+struct DenseSumArgs {
+  const float* from;
+  int64_t split_stride, m, n, ld;
+  int splits, act;
+  const void *bias, *res;
+  int64_t ld_res;
+  void* to;
+  int64_t ldc;
+};
+template <typename T>
+__global__ void __launch_bounds__(256)
+dense_sum_kernel(DenseSumArgs g) {
+  const int64_t quads = g.ld / 4, total = g.m * quads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = i / quads, c = i % quads * 4;
+    const float* from = g.from + r * g.ld + c;
+    v4f s = {0.f, 0.f, 0.f, 0.f}, res = s;
+    if (g.bias) s = load_four(static_cast<const T*>(g.bias), c, g.n);
+    if (g.res) res = load_four(static_cast<const T*>(g.res) + r * g.ld_res, c, g.n);
+    v4f p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int k = 0; k < g.splits; ++k) p += *reinterpret_cast<const v4f*>(from + k * g.split_stride);
+    T v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = static_cast<T>(dense_act(p[q] + s[q], g.act) + res[q]);
+    T* to = static_cast<T*>(g.to) + r * g.ldc + c;
+    if (c + 4 <= g.n) {
+      __builtin_memcpy(to, v, sizeof(v));
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c + q < g.n) to[q] = v[q];
+    }
+  }
+}
+
+// Column sums of a segment of the rows: 32 chunks of 16 bytes by 8 rows at a
+// time, whose sums are added in order.
+constexpr int64_t kSegmentRows = 256;
+template <typename T>
+__global__ void __launch_bounds__(256)
+dense_columns_kernel(const void* __restrict__ src, int64_t n, int64_t stride, int64_t width, int64_t rows, float* sums) {
+  constexpr int V = Chunk<T>::kN;
+  __shared__ float lds[8][32 * V];
+  const int c = static_cast<int>((blockIdx.x * 32 + threadIdx.x % 32) * V), set = threadIdx.x / 32;
+  const int64_t from = blockIdx.y * rows, to = from + rows < n ? from + rows : n;
+  float s[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s[i] = 0.f;
+#pragma unroll 8
+  for (int64_t r = from + set; r < to; r += 8) {
+    float v[V];
+    load_chunk(static_cast<const T*>(src) + r * stride, c, static_cast<int>(width), v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] += v[i];
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) lds[set][threadIdx.x % 32 * V + i] = s[i];
+  __syncthreads();
+  for (int k = threadIdx.x; k < 32 * V; k += 256) {
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * (32 * V) + k;
+    if (col >= width) continue;
+    float t = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) t += lds[q][k];
+    sums[blockIdx.y * width + col] = t;
+  }
+}
+template <typename T>
+__global__ void __launch_bounds__(1024)
+dense_fold_kernel(const float* __restrict__ sums, int64_t rows, int64_t width, T* to) {
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32;
+  const float t = column_sum(sums, rows, width, width, c);
+  if (threadIdx.x < 32 && c < width) to[c] = static_cast<T>(t);
+}
+
+// rows of a segment: as many segments as fill the card a few times, within the launch's limit
+inline int64_t segment_rows(int64_t n) { return std::max(kSegmentRows, round_up((n + 32767) / 32768, 8)); }
+inline int64_t segments(int64_t n) { return (n + segment_rows(n) - 1) / segment_rows(n); }
+
+template <typename Dt>
+int dense_fwd(const DenseArgs& a, size_t* bytes) {
+  using T = typename Dt::T;
+  const bool worst = bytes != nullptr;
+  const hipStream_t st = static_cast<hipStream_t>(a.stream);
+  if (a.n <= 16) {
+    if (worst) {
+      *bytes = 0;
+      return 0;
+    }
+    RowsArgs r{a.x, a.w, nullptr, a.out, nullptr, nullptr, a.n, a.d_out, a.d_in, a.x_stride, a.out_stride, a.act};
+    r.bias = a.bias, r.res = a.residual, r.ld_res = a.residual_stride;
+    return gemm_rows<Dt, kRowsDense>(r, st);
+  }
+  MatrixPlan<Dt> plan(a.workspace);
+  const Operand x = plan.use(a.x, a.n, a.d_in, a.x_stride, worst);
+  const Operand w = plan.use(a.w, a.d_out, a.d_in, a.d_in, worst);
+  GemmArgs g = product<Dt>(a.n, a.d_out, a.d_in, x, w, a.out, a.out_stride);
+  g.act = a.act, g.bias = a.bias, g.res = a.residual, g.ld_res = a.residual_stride;
+  SplitSpace<Dt> space;
+  space.add(space.of(g));
+  float* sums = plan.arena.template take<float>(space.most);
+  if (worst) {
+    *bytes = plan.arena.at;
+    return 0;
+  }
+  int rc = plan.run_pack(st);
+  if (rc) return rc;
+  const Split p = plan_split<Dt>(g);
+  if (p.splits == 1) return gemm_launch<Dt, false, false, kEpiDense>(g, st);
+  SplitSumArgs q{};
+  split_into(g, p, sums, q);
+  rc = gemm_launch_tile<Dt, 64, 64, 2, 2, kSmallK<Dt>, kSmallS<Dt>, false, false, kEpiStoreF32>(g, st);
+  if (rc) return rc;
+  const DenseSumArgs s{sums, q.split_stride[0], a.n, a.d_out, q.ld[0], p.splits, a.act,
+                       a.bias, a.residual, a.residual_stride, a.out, a.out_stride};
+  const int64_t blocks = std::min<int64_t>((a.n * (q.ld[0] / 4) + 255) / 256, 2048);
+  hipLaunchKernelGGL(dense_sum_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, s);
+  return static_cast<int>(hipGetLastError());
+}
+
+template <typename Dt>
+int dense_bwd(const DenseArgs& a, size_t* bytes) {
+  using T = typename Dt::T;
+  const bool worst = bytes != nullptr, product_again = a.act != kActNone;
+  const hipStream_t st = static_cast<hipStream_t>(a.stream);
+  MatrixPlan<Dt> plan(a.workspace);
+  const Operand x = plan.use(a.x, a.n, a.d_in, a.x_stride, worst, true);
+  const Operand w = plan.use(a.w, a.d_out, a.d_in, a.d_in, worst);
+  const Operand d = product_again ? plan.hidden(a.n, a.d_out) : plan.use(a.gout, a.n, a.d_out, a.gout_stride, worst, true);
+  GemmArgs again = product<Dt>(a.n, a.d_out, a.d_in, x, w, nullptr, 0);
+  again.act = a.act, again.bias = a.bias, again.res = a.gout, again.ld_res = a.gout_stride;
+  again.dg = const_cast<uint16_t*>(d.plane[0]), again.ldh = d.ld, again.plane_stride = a.n * d.ld;
+  again.e_dg = d.exponents, again.e_ld = d.exponents_ld;
+  GemmArgs dx = product<Dt>(a.n, a.d_in, a.d_out, d, w, a.gx, a.d_in);
+  GemmArgs dw = product<Dt>(a.d_out, a.d_in, a.n, d, x, a.gw, a.d_in);
+  SplitSpace<Dt> space;  // sized for every gradient, asked for or not
+  space.add(space.of(dx) + space.of(dw));
+  float* sums = plan.arena.template take<float>(space.most);
+  // the product's tiles have at least 64 rows for two waves
+  float* columns = plan.arena.template take<float>((product_again ? (a.n + 63) / 64 * 2 : segments(a.n)) * a.d_out);
+  if (worst) {
+    *bytes = plan.arena.at;
+    return 0;
+  }
+  int rc = plan.run_pack(st);
+  int64_t column_rows = 0;
+  if (!rc && product_again) {
+    again.column_sums = a.gbias ? columns : nullptr;
+    rc = gemm_launch<Dt, false, false, kEpiDenseBwd>(again, st);
+    column_rows = again.tiles_m[0] * 2;
+  } else if (!rc && a.gbias) {
+    column_rows = segments(a.n);
+    constexpr int kWide = 32 * Chunk<T>::kN;
+    hipLaunchKernelGGL(dense_columns_kernel<T>,
+                       dim3(static_cast<unsigned>((a.d_out + kWide - 1) / kWide), static_cast<unsigned>(column_rows)),
+                       dim3(256), 0, st, a.gout, a.n, a.gout_stride, a.d_out, segment_rows(a.n), columns);
+    rc = static_cast<int>(hipGetLastError());
+  }
+  if (!rc && a.gbias) {
+    hipLaunchKernelGGL(dense_fold_kernel<T>, dim3(static_cast<unsigned>((a.d_out + 31) / 32)), dim3(1024), 0, st, columns,
+                       column_rows, a.d_out, static_cast<T*>(a.gbias));
+    rc = static_cast<int>(hipGetLastError());
+  }
+  if (rc) return rc;
+  const int64_t tiles = round_up(a.d_in, 64) / 64 * (round_up(a.d_out, 64) / 64 + round_up(a.n, 64) / 64);
+  if (a.gx && a.gw && tiles <= 2 * 768) return gemm_launch_two_split<Dt>(dx, dw, sums, st);
+  if (a.gx) rc = gemm_launch_split<Dt, false, true, kEpiStore>(dx, sums, st);
+  if (!rc && a.gw) rc = gemm_launch_split<Dt, true, true, kEpiStore>(dw, sums, st);
+  return rc;
+}
+
+}  // namespace kern
+}  // namespace segpoly

@@ -2,10 +2,10 @@
 // rows.
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
 #include <cstdint>
 
 #include "../channel_ops.hpp"
+#include "zero_fill.hpp"
 
 namespace segpoly {
 namespace kern {
@@ -24,29 +24,13 @@ int ffn_any(const GatedFfnArgs& a, bool backward, size_t* bytes) {
   return backward ? ffn_bwd_f32(a, bytes) : ffn_fwd_f32(a, bytes);
 }
 
-struct ZeroArgs {
-  void* to[3];
-  int64_t count[3];
-};
-template <typename U>
-__global__ void __launch_bounds__(256)
-zero_kernel(ZeroArgs g) {
-  U* to = static_cast<U*>(g.to[blockIdx.y]);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < g.count[blockIdx.y];
-       i += static_cast<int64_t>(gridDim.x) * 256)
-    to[i] = 0;
-}
-
 // The weight gradients of no rows: zeros, without a look at the weights, which
 // the caller need not have.
 int ffn_bwd_no_rows(const GatedFfnArgs& a) {
   if (!a.gw_gate) return 0;
   const int64_t in = a.hidden * a.d_in, out = a.d_out * a.hidden;
-  const ZeroArgs g{{a.gw_gate, a.gw_up, a.gw_down}, {in, in, out}};
-  const int64_t blocks = std::min<int64_t>((std::max(in, out) + 255) / 256, 2048);
-  auto* zero = channel_dtype_bytes(a.dtype) == 4 ? zero_kernel<uint32_t> : zero_kernel<uint16_t>;
-  hipLaunchKernelGGL(zero, dim3(static_cast<unsigned>(blocks), 3), dim3(256), 0, static_cast<hipStream_t>(a.stream), g);
-  return static_cast<int>(hipGetLastError());
+  return zero_fill({{a.gw_gate, a.gw_up, a.gw_down}, {in, in, out}}, channel_dtype_bytes(a.dtype),
+                   static_cast<hipStream_t>(a.stream));
 }
 
 }  // namespace kern

@@ -45,7 +45,11 @@ struct RowsArgs {
   uint32_t* odd;           // and whether any row's is not zero, [hidden / 16], a byte a wave
   int64_t m, n, k, ldx, ldo;
   int act;
+  const void *bias, *res;  // of a dense product: [n], [m][ld_res], either null
+  int64_t ld_res;
 };
+
+enum { kRowsPlain = 0, kRowsPaired = 1, kRowsDense = 2 };
 
 // eight k of a row from column c on, as the planes of a matrix operand
 template <typename Dt>
@@ -82,10 +86,11 @@ constexpr int rows_waves(int m16) {
 }
 
 // M16: blocks of 16 rows of x
-template <typename Dt, int M16, bool Pair>
+template <typename Dt, int M16, int Form>
 __global__ void __launch_bounds__(rows_waves<Dt>(M16) * 64)
 gemm_rows_kernel(RowsArgs g) {
   using T = typename Dt::T;
+  constexpr bool Pair = Form == kRowsPaired;
   constexpr int P = Dt::kPlanes, W = Pair ? 2 : 1;
   __shared__ v4f sums[rows_waves<Dt>(M16)][W][64];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, waves = blockDim.x / 64;
@@ -237,6 +242,11 @@ gemm_rows_kernel(RowsArgs g) {
         if (m < g.m && l / 16 + q == 0) g.exponents[m * ((g.n + 15) / 16) + blockIdx.x] = static_cast<int8_t>(e);
       }
       if (m < g.m && n < g.n) {
+        if constexpr (Form == kRowsDense) {
+          const float bias = g.bias ? static_cast<float>(static_cast<const T*>(g.bias)[n]) : 0.f;
+          v[0] = dense_act(v[0] + bias, g.act);
+          if (g.res) v[0] += static_cast<float>(static_cast<const T*>(g.res)[m * g.ld_res + n]);
+        }
         static_cast<T*>(g.out)[m * g.ldo + n] = static_cast<T>(v[0]);
       }
     }
@@ -249,18 +259,18 @@ gemm_rows_kernel(RowsArgs g) {
   }
 }
 
-template <typename Dt, int M16, bool Pair>
+template <typename Dt, int M16, int Form>
 int gemm_rows_launch(const RowsArgs& g, hipStream_t st) {
   const int64_t waves = std::min<int64_t>(rows_waves<Dt>(M16), std::max<int64_t>(4, (g.k + 63) / 64));
-  hipLaunchKernelGGL((gemm_rows_kernel<Dt, M16, Pair>), dim3(static_cast<unsigned>((g.n + 15) / 16)),
+  hipLaunchKernelGGL((gemm_rows_kernel<Dt, M16, Form>), dim3(static_cast<unsigned>((g.n + 15) / 16)),
                      dim3(static_cast<unsigned>(waves * 64)), 0, st, g);
   return static_cast<int>(hipGetLastError());
 }
 
-template <typename Dt, bool Pair>
+template <typename Dt, int Form>
 int gemm_rows(const RowsArgs& g, hipStream_t st) {
-  if (g.m <= 16) return gemm_rows_launch<Dt, 1, Pair>(g, st);
-  return gemm_rows_launch<Dt, 2, Pair>(g, st);
+  if (g.m <= 16) return gemm_rows_launch<Dt, 1, Form>(g, st);
+  return gemm_rows_launch<Dt, 2, Form>(g, st);
 }
 
 }  // namespace kern

@@ -1,4 +1,4 @@
-// Matrix-core tile kernel of the gated feed-forward operator:
+// Matrix-core tile kernel of the gated feed-forward and the dense operators:
 //   C[m, n] = sum over phases p and k of A_p[m, k] B_p[n, k]
 // for 16-bit operands, float32 accumulation, and an epilogue on the
 // accumulators.  Either operand is stored along k ([rows][k]) or across it
@@ -60,13 +60,22 @@ struct GemmArgs {
   int *e_h, *e_dg, *e_du;
   const int *ea[kMaxBatch], *eb[kMaxBatch];
   int64_t e_ld;
+  // epilogue of the dense operator, all of the io type: [n], [m][ld_res], either
+  // null.  Forward: c = act(product + bias) + res.  Backward: res is the gradient
+  // of the output; dg and e_dg as above, and the sums of dg's columns over each
+  // wave's rows, [tiles_m * WM][n], or null.
+  const void *bias, *res;
+  int64_t ld_res;
+  float* column_sums;
 };
 
-enum { kEpiStore = 0, kEpiStoreF32 = 1, kEpiGated = 2, kEpiGatedBwd = 3 };
+enum { kEpiStore = 0, kEpiStoreF32 = 1, kEpiGated = 2, kEpiGatedBwd = 3, kEpiDense = 4, kEpiDenseBwd = 5 };
 
 // io type T, matrix type E, planes per operand, products held in scaled blocks
 struct DtBF16 { using T = bf16; using E = bf16; static constexpr int kPlanes = 1; static constexpr bool kScaled = false; };
 struct DtF16 { using T = f16; using E = f16; static constexpr int kPlanes = 1; static constexpr bool kScaled = true; };
+// without scaled blocks: of products whose operands are the caller's
+struct DtF16Plain { using T = f16; using E = f16; static constexpr int kPlanes = 1; static constexpr bool kScaled = false; };
 struct DtF32 { using T = float; using E = bf16; static constexpr int kPlanes = 3; static constexpr bool kScaled = false; };
 
 // float16 reaches from 2^-24 to 2^16.  A value that is held in it between two
@@ -180,6 +189,23 @@ __device__ __forceinline__ void act_both(float g, int act, float& a, float& da) 
     a = sigmoid(g);
     da = a * (1.f - a);
   }
+}
+
+// with the dense operator's choice of none, whose gradient needs no product
+__device__ __forceinline__ float dense_act(float g, int act) { return act == kActNone ? g : act_value(g, act); }
+
+// four columns of a row from n on, zeros past its width
+template <typename T>
+__device__ __forceinline__ v4f load_four(const T* row, int64_t n, int64_t width) {
+  T t[4] = {T(0.f), T(0.f), T(0.f), T(0.f)};
+  if (n + 4 <= width) {
+    __builtin_memcpy(t, row + n, sizeof(t));
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q < width) t[q] = row[n + q];
+  }
+  return v4f{static_cast<float>(t[0]), static_cast<float>(t[1]), static_cast<float>(t[2]), static_cast<float>(t[3])};
 }
 
 // a fragment times 2^d, d <= 0: in two steps, for one that takes all of float16's
@@ -657,23 +683,128 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
       }
     }
     using T = std::conditional_t<Epi == kEpiStoreF32, float, typename Dt::T>;
+    const int64_t row0 = m0 + wm * (BM / WM) + lane % 16, col0 = n0 + wn * (BN / WN) + lane / 16 * 4;
+    constexpr bool kDense = Epi == kEpiDense || Epi == kEpiDenseBwd;
+    if constexpr (kDense) {
+      v4f bias[FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int64_t m = m0 + wm * (BM / WM) + i * 16 + lane % 16;
-      if (m >= gm) continue;
-      T* row = static_cast<T*>(g.c[z]) + (Epi == kEpiStoreF32 ? g.split_stride * share : 0) + m * g.ldc[z];
+      for (int j = 0; j < FN; ++j)
+        bias[j] = g.bias ? load_four(static_cast<const T*>(g.bias), col0 + j * 16, gn) : v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int64_t n = n0 + wn * (BN / WN) + j * 16 + lane / 16 * 4;
-        T v[4];
+      for (int i = 0; i < FM; ++i) {
+        const int64_t m = row0 + i * 16;
+        const T* row = static_cast<const T*>(g.res) + (m < gm ? m : 0) * g.ld_res;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = static_cast<T>(acc[i][j][q]);
-        if (n + 4 <= gn) {
-          __builtin_memcpy(row + n, v, sizeof(v));
-        } else {
+        for (int j = 0; j < FN; ++j) {
+          // past the last row and column the gradients are zero, the products too
+          v4f r = {0.f, 0.f, 0.f, 0.f};
+          if (g.res && m < gm) r = load_four(row, col0 + j * 16, gn);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (n + q < gn) row[n + q] = v[q];
+          for (int q = 0; q < 4; ++q) {
+            const float v = acc[i][j][q] + bias[j][q];
+            if constexpr (Epi == kEpiDense) {
+              acc[i][j][q] = dense_act(v, g.act) + r[q];
+            } else {
+              float value, slope;
+              act_both(v, g.act, value, slope);
+              acc[i][j][q] = r[q] * slope;
+            }
+          }
+        }
+      }
+    }
+    if constexpr (Epi != kEpiDenseBwd) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int64_t m = row0 + i * 16;
+        if (m >= gm) continue;
+        T* row = static_cast<T*>(g.c[z]) + (Epi == kEpiStoreF32 ? g.split_stride * share : 0) + m * g.ldc[z];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const int64_t n = col0 + j * 16;
+          T v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = static_cast<T>(acc[i][j][q]);
+          if (n + 4 <= gn) {
+            __builtin_memcpy(row + n, v, sizeof(v));
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (n + q < gn) row[n + q] = v[q];
+          }
+        }
+      }
+    } else {
+      if (g.column_sums) {
+        float* sums = g.column_sums + (m0 / BM * WM + wm) * gn;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < FM; ++i) s += acc[i][j][q];
+            s = lane_sum<16>(s);
+            const int64_t n = col0 + j * 16 + q;
+            if (lane % 16 == 0 && n < gn) sums[n] = s;
+          }
+      }
+      if constexpr (Dt::kScaled) {
+        constexpr int kRows = BM / WM > 64 ? BM / WM / 64 : 1, kCols = BN / WN / 32, kPer = FM / kRows;
+        static_assert(BM == 64 ? WM == 2 && BN / WN == 32 : BM / WM % 64 == 0 && BN / WN % 32 == 0,
+                      "a wave holds whole blocks, or half of one");
+        if constexpr (BM == 64) wait_and_meet<0>();  // every wave has read its last fragments
+#pragma unroll
+        for (int b = 0; b < kRows; ++b)
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            float top = 0.f;
+#pragma unroll
+            for (int i = b * kPer; i < (b + 1) * kPer; ++i)
+#pragma unroll
+              for (int j = c * 2; j < c * 2 + 2; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) top = __builtin_fmaxf(top, finite_abs(acc[i][j][q]));
+            top = lane_max<64>(top);
+            if constexpr (BM == 64) {
+              float* shared = reinterpret_cast<float*>(b0);
+              if (lane == 0) shared[wave] = top;
+              wait_and_meet<63>();
+              top = __builtin_fmaxf(shared[wn], shared[WN + wn]);
+            }
+            const int e = block_exponent(top);
+            const float scale = block_scale(e);
+#pragma unroll
+            for (int i = b * kPer; i < (b + 1) * kPer; ++i)
+#pragma unroll
+              for (int j = c * 2; j < c * 2 + 2; ++j) acc[i][j] *= scale;
+            const int64_t m = m0 + wm * (BM / WM) + b * 64, n = n0 + wn * (BN / WN) + c * 32;
+            if (lane == 0 && (BM > 64 || wm == 0) && m < gm && n < gn) g.e_dg[m / 64 * g.e_ld + n / 32] = e;
+          }
+      }
+      const int64_t width = (gn + 7) / 8 * 8;  // rows of the products' operands are read in 16-byte chunks
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int64_t m = row0 + i * 16;
+        if (m >= gm) continue;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const int64_t n = col0 + j * 16;
+          if (n >= width) continue;
+          E e[P][4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if constexpr (P == 1) {
+              e[0][q] = static_cast<E>(acc[i][j][q]);
+            } else {
+              bf16 s[3];
+              split3(acc[i][j][q], s);
+#pragma unroll
+              for (int p = 0; p < P; ++p) e[p][q] = s[p];
+            }
+          }
+#pragma unroll
+          for (int p = 0; p < P; ++p) __builtin_memcpy(g.dg + p * g.plane_stride + m * g.ldh + n, e[p], 8);
         }
       }
     }
