@@ -15,6 +15,7 @@
 #include <algorithm>
 
 #include "column_sums.hpp"
+#include "dense_stream.hpp"
 #include "gemm_plan.hpp"
 #include "gemm_rows.hpp"
 
@@ -46,8 +47,10 @@ dense_sum_kernel(DenseSumArgs g) {
 #pragma unroll 8
     for (int k = 0; k < g.splits; ++k) p += *reinterpret_cast<const v4f*>(from + k * g.split_stride);
     T v[4];
+    with_act(g.act, [&](auto act) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = static_cast<T>(dense_act(p[q] + s[q], g.act) + res[q]);
+      for (int q = 0; q < 4; ++q) v[q] = static_cast<T>(dense_act(act, p[q] + s[q]) + res[q]);
+    });
     T* to = static_cast<T*>(g.to) + r * g.ldc + c;
     if (c + 4 <= g.n) {
       __builtin_memcpy(to, v, sizeof(v));
@@ -117,6 +120,14 @@ int dense_fwd(const DenseArgs& a, size_t* bytes) {
     r.bias = a.bias, r.res = a.residual, r.ld_res = a.residual_stride;
     return gemm_rows<Dt, kRowsDense>(r, st);
   }
+  if (stream_chunks<Dt>(a.d_in)) {
+    if (worst) {
+      *bytes = 0;
+      return 0;
+    }
+    return dense_stream<Dt>({a.x, a.w, a.bias, a.residual, a.out, a.n, a.x_stride, a.residual_stride, a.out_stride,
+                             static_cast<int>(a.d_in), static_cast<int>(a.d_out), a.act, 0}, st);
+  }
   MatrixPlan<Dt> plan(a.workspace);
   const Operand x = plan.use(a.x, a.n, a.d_in, a.x_stride, worst);
   const Operand w = plan.use(a.w, a.d_out, a.d_in, a.d_in, worst);
@@ -162,8 +173,7 @@ int dense_bwd(const DenseArgs& a, size_t* bytes) {
   SplitSpace<Dt> space;  // sized for every gradient, asked for or not
   space.add(space.of(dx) + space.of(dw));
   float* sums = plan.arena.template take<float>(space.most);
-  // the product's tiles have at least 64 rows for two waves
-  float* columns = plan.arena.template take<float>((product_again ? (a.n + 63) / 64 * 2 : segments(a.n)) * a.d_out);
+  float* columns = plan.arena.template take<float>((product_again ? (a.n + 63) / 64 * 2 + 2 : segments(a.n)) * a.d_out);
   if (worst) {
     *bytes = plan.arena.at;
     return 0;
@@ -173,7 +183,7 @@ int dense_bwd(const DenseArgs& a, size_t* bytes) {
   if (!rc && product_again) {
     again.column_sums = a.gbias ? columns : nullptr;
     rc = gemm_launch<Dt, false, false, kEpiDenseBwd>(again, st);
-    column_rows = again.tiles_m[0] * 2;
+    column_rows = again.column_rows;
   } else if (!rc && a.gbias) {
     column_rows = segments(a.n);
     constexpr int kWide = 32 * Chunk<T>::kN;

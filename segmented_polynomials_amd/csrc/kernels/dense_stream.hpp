@@ -1,0 +1,275 @@
+// The dense layer of many rows and a small weight, out = act(x W^T + bias) +
+// residual: bound by reading x and writing out once.  The weight's planes stay in
+// LDS as matrix operands for the kernel's whole time; a wave takes 16 R rows at a
+// time, its x from memory straight into the registers of the matrix instructions
+// (the next rows' loads in flight meanwhile, float32 split into its planes in
+// registers), and goes over the columns 32 at a time.  No barrier after the
+// weight has been filled in, no copy of x: the tiles of gemm_tile.hpp write
+// float32 rows as planes and read them again, three times the bytes of x.  Columns
+// that do not fit in LDS, and those of few rows, are shared out over workgroups.
+// One MI355X, us here and in tiles, silu (floor: the bytes at 5.0 TB/s):
+//                              bf16               f32
+//   600000 x 64 x 64       29,  50 (31)      69, 166 (61)
+//   100000 x 128 x 128     16,  22 (10)      37,  59 (21)
+//   20162 x 64 x 896       15,  26  (8)      31,  40 (16)
+//   50000 x 256 x 256      22,  24 (10)      75,  79 (28)
+//   5000 x 256 x 512       9.5, 8.7 (2)      26,  26  (6)
+//   1000 x 64 x 64        4.2, 4.8          5.9, 8.2
+//   20000 x 256 x 1024     27,  33 (10)     110,  91 (45)
+// float32 above 128 columns of x has no registers for the rows, and takes the tiles.
+// A pair of column fragments holds the columns in an order that leaves a lane
+// eight neighbouring ones of its row, 16 or 32 bytes to store together.
+#pragma once
+#include <algorithm>
+
+#include "gemm_rows.hpp"
+
+namespace segpoly {
+namespace kern {
+
+struct StreamArgs {
+  const void *x, *w, *bias, *res;
+  void* out;
+  int64_t n, ldx, ld_res, ldo;
+  int k, cols, act;
+  int pairs;  // of column fragments, of a workgroup: (x, y) takes the y-th part of the columns
+};
+
+// Eight float32 as planes.  Values that would round up to infinity, infinities and
+// NaN take split3; a wave without any, nearly all, goes without its comparisons.
+__device__ __forceinline__ void split_eight(const float (&v)[8], u16x8 (&p)[3]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu;
+    top = b > top ? b : top;
+  }
+  if (__ballot(top >= 0x7f7f8000u)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      bf16 s[3];
+      split3(v[i], s);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) p[q][i] = __builtin_bit_cast(uint16_t, s[q]);
+    }
+    return;
+  }
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = v[i];
+#pragma unroll
+  for (int q = 0; q < 3; ++q)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bf16 s = static_cast<bf16>(r[i]);
+      p[q][i] = __builtin_bit_cast(uint16_t, s);
+      if (q < 2) r[i] -= static_cast<float>(s);
+    }
+}
+// Eight elements of a row from column `at` on, and as matrix operands.  Whole: of
+// rows whose width is a multiple of eight, no chunk crosses the end.
+template <typename Dt, bool Whole>
+__device__ __forceinline__ void load_eight(RowChunk<Dt>& c, const typename Dt::T* row, int at, int width) {
+  if constexpr (Whole) {
+#pragma unroll
+    for (int i = 0; i < RowChunk<Dt>::kLoads; ++i) c.raw[i] = u32x4{0, 0, 0, 0};
+    if (at < width) __builtin_memcpy(c.raw, row + at, sizeof(c.raw));
+  } else {
+    c.load(row, at, width);
+  }
+}
+template <typename Dt, bool Whole>
+__device__ __forceinline__ void chunk_planes(const RowChunk<Dt>& c, int at, int width, u16x8 (&p)[Dt::kPlanes]) {
+  if constexpr (Dt::kPlanes == 1) {
+    if constexpr (Whole)
+      p[0] = __builtin_bit_cast(u16x8, c.raw[0]);
+    else
+      c.planes(at, width, p);
+  } else {
+    float v[8];
+    if constexpr (Whole) {
+      __builtin_memcpy(v, c.raw, sizeof(v));
+    } else {
+      unpack_chunk<float>(c.raw[0], at, width, v);
+      unpack_chunk<float>(c.raw[1], at + 4, width, v + 4);
+    }
+    split_eight(v, p);
+  }
+}
+
+// columns of a row of fragments: fragment pair * 2 + j, row i of the instruction
+__device__ __forceinline__ int stream_column(int fragment, int i) {
+  return fragment / 2 * 32 + i / 4 * 8 + fragment % 2 * 4 + i % 4;
+}
+
+// KC: 32 k each of a row.  Loads return in order: the residual's would wait for the
+// next rows' if those were on their way already, so with it they are fetched later.
+// Whole: both widths are multiples of eight.
+template <typename Dt, int KC, int R, bool Res, bool Whole>
+__global__ void __launch_bounds__(512)
+dense_stream_kernel(StreamArgs g) {
+  using T = typename Dt::T;
+  constexpr int P = Dt::kPlanes;
+  extern __shared__ __attribute__((aligned(16))) u16x8 weight[];  // [fragment][KC][P][64]
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
+  const int pair0 = blockIdx.y * g.pairs, all = (g.cols + 31) / 32;
+  const int pairs = all - pair0 < g.pairs ? all - pair0 : g.pairs, units = pairs * 2 * KC;
+  v4f* bias = reinterpret_cast<v4f*>(weight + units * P * 64);  // of four columns each
+  constexpr int kFill = 4;  // in flight together
+  for (int u0 = wave * kFill; u0 < units; u0 += waves * kFill) {
+    RowChunk<Dt> c[kFill];
+    int at[kFill];
+#pragma unroll
+    for (int i = 0; i < kFill; ++i) {
+      const int u = u0 + i, n = pair0 * 32 + stream_column(u / KC, lane % 16);
+      at[i] = u < units && n < g.cols ? u % KC * 32 + lane / 16 * 8 : g.k;
+      c[i].load(static_cast<const T*>(g.w) + static_cast<int64_t>(at[i] < g.k ? n : 0) * g.k, at[i], g.k);
+    }
+#pragma unroll
+    for (int i = 0; i < kFill; ++i) {
+      if (u0 + i >= units) continue;
+      u16x8 p[P];
+      chunk_planes<Dt, false>(c[i], at[i], g.k, p);
+#pragma unroll
+      for (int q = 0; q < P; ++q) weight[((u0 + i) * P + q) * 64 + lane] = p[q];
+    }
+  }
+  for (int i = threadIdx.x; i < pairs * 8; i += blockDim.x)
+    bias[i] = g.bias ? load_four(static_cast<const T*>(g.bias), pair0 * 32 + i * 4, g.cols) : v4f{0.f, 0.f, 0.f, 0.f};
+  __syncthreads();
+  const int64_t tiles = (g.n + 16 * R - 1) / (16 * R), step = static_cast<int64_t>(gridDim.x) * waves;
+  RowChunk<Dt> raw[R][KC];
+  auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      int64_t m = t * (16 * R) + r * 16 + lane % 16;
+      m = m < g.n ? m : g.n - 1;
+#pragma unroll
+      for (int c = 0; c < KC; ++c)
+        load_eight<Dt, Whole>(raw[r][c], static_cast<const T*>(g.x) + m * g.ldx, c * 32 + lane / 16 * 8, g.k);
+    }
+  };
+  int64_t t = static_cast<int64_t>(wave) * gridDim.x + blockIdx.x;
+  if (t < tiles) fetch(t);
+  for (; t < tiles; t += step) {
+    u16x8 x[R][KC][P];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int c = 0; c < KC; ++c) chunk_planes<Dt, Whole>(raw[r][c], c * 32 + lane / 16 * 8, g.k, x[r][c]);
+    if (!Res && t + step < tiles) fetch(t + step);
+    for (int pair = 0; pair < pairs; ++pair) {
+      const int n = (pair0 + pair) * 32 + lane / 16 * 8;
+      v4f res[R][2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          res[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
+          if constexpr (Res) {
+            int64_t m = t * (16 * R) + r * 16 + lane % 16;
+            m = m < g.n ? m : g.n - 1;
+            res[r][j] = load_four(static_cast<const T*>(g.res) + m * g.ld_res, n + j * 4, g.cols);
+          }
+        }
+      v4f acc[R][2], small[R][2];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[r][j] = small[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        u16x8 w[2][P];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < P; ++q) w[j][q] = weight[(((pair * 2 + j) * KC + c) * P + q) * 64 + lane];
+        constexpr int kProducts = P == 1 ? 1 : 6;
+#pragma unroll
+        for (int s = 0; s < kProducts; ++s)
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if constexpr (P == 1) {
+                acc[r][j] = mma16(typename Dt::E{}, w[j][0], x[r][c][0], acc[r][j]);
+              } else {
+                v4f& a = s < kProducts - 1 ? small[r][j] : acc[r][j];
+                a = mma16(typename Dt::E{}, w[j][kPairs3[s][1]], x[r][c][kPairs3[s][0]], a);
+              }
+            }
+      }
+      with_act(g.act, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          T v[8];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const v4f b = bias[pair * 8 + lane / 16 * 2 + j];
+            if constexpr (P > 1) acc[r][j] = add_small(acc[r][j], small[r][j]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              v[j * 4 + q] = static_cast<T>(dense_act(act, acc[r][j][q] + b[q]) + res[r][j][q]);
+          }
+          const int64_t m = t * (16 * R) + r * 16 + lane % 16;
+          if (m >= g.n || n >= g.cols) continue;
+          T* to = static_cast<T*>(g.out) + m * g.ldo + n;
+          if (Whole || n + 8 <= g.cols) {
+            __builtin_memcpy(to, v, sizeof(v));
+          } else {
+#pragma unroll
+            for (int q = 0; q < 7; ++q)
+              if (n + q < g.cols) to[q] = v[q];
+          }
+        }
+      });
+    }
+    if (Res && t + step < tiles) fetch(t + step);
+  }
+}
+
+// 32 k each of a row that stay in registers, or 0 for rows that do not.
+template <typename Dt>
+int stream_chunks(int64_t d_in) {
+  constexpr int kMost = Dt::kPlanes == 1 ? 8 : 4;
+  for (int chunks = 1; chunks <= kMost; chunks *= 2)
+    if (d_in <= chunks * 32) return chunks;
+  return 0;
+}
+
+// Bytes of LDS of 32 columns of the weight and their bias.
+template <typename Dt>
+int64_t stream_pair_bytes(int chunks) { return 32 * (chunks * Dt::kPlanes * 64 + 4); }
+
+template <typename Dt, int KC, int R>
+int stream_launch(StreamArgs g, hipStream_t st) {
+  const int64_t tiles = (g.n + 16 * R - 1) / (16 * R), all = (g.cols + 31) / 32;
+  // two workgroups share a unit's LDS; fewer columns each until eight waves a unit have
+  // work (20162 x 64 x 896 bf16: 15 us, 19 with four)
+  int64_t pairs = std::min(all, std::max<int64_t>(1, 80 * 1024 / stream_pair_bytes<Dt>(KC)));
+  while (pairs > 1 && tiles * ((all + pairs - 1) / pairs) < 2048) pairs = (pairs + 1) / 2;
+  const int64_t groups = (all + pairs - 1) / pairs;
+  g.pairs = static_cast<int>((all + groups - 1) / groups);
+  const int64_t blocks = std::min<int64_t>(tiles, std::max<int64_t>(1, 512 / groups));
+  const bool whole = g.k % 8 == 0 && g.cols % 8 == 0;
+  auto* kernel = whole ? (g.res ? dense_stream_kernel<Dt, KC, R, true, true> : dense_stream_kernel<Dt, KC, R, false, true>)
+                       : (g.res ? dense_stream_kernel<Dt, KC, R, true, false> : dense_stream_kernel<Dt, KC, R, false, false>);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(groups)), dim3(512),
+                     g.pairs * stream_pair_bytes<Dt>(KC), st, g);
+  return static_cast<int>(hipGetLastError());
+}
+
+template <typename Dt>
+int dense_stream(const StreamArgs& g, hipStream_t st) {
+  constexpr int kFour = Dt::kPlanes == 1 ? 2 : 1;
+  const int chunks = stream_chunks<Dt>(g.k);
+  if (chunks == 1) return stream_launch<Dt, 1, 2>(g, st);
+  if (chunks == 2) return stream_launch<Dt, 2, 2>(g, st);
+  if constexpr (Dt::kPlanes == 1) {
+    if (chunks == 8) return stream_launch<Dt, 8, 1>(g, st);
+  }
+  return stream_launch<Dt, 4, kFour>(g, st);
+}
+
+}  // namespace kern
+}  // namespace segpoly

@@ -90,6 +90,7 @@ int gemm_launch_tile(GemmArgs& g, hipStream_t st) {
   }
   if (tiles == 0) return 0;  // no rows
   if (g.splits < 1) g.splits = 1;
+  g.column_rows = g.tiles_m[0] * WM;
   hipLaunchKernelGGL((gemm_tile_kernel<Dt, BM, BN, WM, WN, KS, S, AAcross, BAcross, Epi>),
                      dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(g.splits)), dim3(WM * WN * 64), 0, st, g);
   return static_cast<int>(hipGetLastError());
@@ -228,7 +229,7 @@ int gemm_launch(GemmArgs& g, hipStream_t st) {
     return (each > 1 && rounds > 1 ? 0.5 * (rounds + whole) : whole) * static_cast<double>(bm * bn * each) / rate;
   };
   if constexpr (Dt::kPlanes == 1) {
-    constexpr bool kTwoAcross = AAcross && BAcross, kBwd = Epi == kEpiGatedBwd;
+    constexpr bool kTwoAcross = AAcross && BAcross, kBwd = Epi == kEpiGatedBwd || Epi == kEpiDenseBwd || Epi == kEpiDense;
     const double large = kTwoAcross || kBwd ? cost(256, 128, kBwd ? 1 : 2, 1.0) : cost(256, 256, 1, 1.0);
     const double c128 = cost(128, 128, 2, 0.8), c64 = cost(64, 64, 3, 0.45);
     if (large <= c128 && large <= c64) {

@@ -244,7 +244,7 @@ gemm_rows_kernel(RowsArgs g) {
       if (m < g.m && n < g.n) {
         if constexpr (Form == kRowsDense) {
           const float bias = g.bias ? static_cast<float>(static_cast<const T*>(g.bias)[n]) : 0.f;
-          v[0] = dense_act(v[0] + bias, g.act);
+          with_act(g.act, [&](auto act) { v[0] = dense_act(act, v[0] + bias); });
           if (g.res) v[0] += static_cast<float>(static_cast<const T*>(g.res)[m * g.ld_res + n]);
         }
         static_cast<T*>(g.out)[m * g.ldo + n] = static_cast<T>(v[0]);

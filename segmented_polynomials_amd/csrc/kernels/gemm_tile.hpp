@@ -63,9 +63,9 @@ struct GemmArgs {
   // epilogue of the dense operator, all of the io type: [n], [m][ld_res], either
   // null.  Forward: c = act(product + bias) + res.  Backward: res is the gradient
   // of the output; dg and e_dg as above, and the sums of dg's columns over each
-  // wave's rows, [tiles_m * WM][n], or null.
+  // wave's rows, [column_rows][n], or null.
   const void *bias, *res;
-  int64_t ld_res;
+  int64_t ld_res, column_rows;  // tiles_m times the tile's waves along m, at most 2 ceil(m / 64) + 2
   float* column_sums;
 };
 
@@ -191,8 +191,30 @@ __device__ __forceinline__ void act_both(float g, int act, float& a, float& da) 
   }
 }
 
-// with the dense operator's choice of none, whose gradient needs no product
-__device__ __forceinline__ float dense_act(float g, int act) { return act == kActNone ? g : act_value(g, act); }
+// `body` with the activation as a compile-time constant: a branch per value costs
+// more than the value (200000 x 64 x 200 bf16 forward 129 us with it, 72 without)
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& body) {
+  if (act == kActNone) return body(std::integral_constant<int, kActNone>{});
+  if (act == kActSilu) return body(std::integral_constant<int, kActSilu>{});
+  if (act == kActGelu) return body(std::integral_constant<int, kActGelu>{});
+  if (act == kActRelu) return body(std::integral_constant<int, kActRelu>{});
+  return body(std::integral_constant<int, kActSigmoid>{});
+}
+template <typename Act>
+__device__ __forceinline__ float dense_act(Act, float z) {
+  if constexpr (Act::value == kActNone)
+    return z;
+  else
+    return act_value(z, Act::value);
+}
+// the slope alone
+template <typename Act>
+__device__ __forceinline__ float dense_slope(Act, float z) {
+  float value, slope = 1.f;
+  if constexpr (Act::value != kActNone) act_both(z, Act::value, value, slope);
+  return slope;
+}
 
 // four columns of a row from n on, zeros past its width
 template <typename T>
@@ -319,13 +341,63 @@ struct TileLds {
   __shared__ __attribute__((aligned(16))) uint16_t a3[L::kA3];     \
   __shared__ __attribute__((aligned(16))) uint16_t b3[L::kB3]
 
+// The results of a BM x BN tile, 16 bits each, to rows m < gm, columns n < width of
+// `to`.  A fragment's lanes hold four columns of sixteen rows, 32 bytes of a line:
+// they go through LDS, 64 rows to a buffer, and leave in whole lines.  16-byte slot
+// s of row r holds chunk s ^ r, so that sixteen rows of a column fall into different
+// banks.  value(i, j, q): element q of the wave's fragment (i, j).
+template <int BM, int BN, int WM, int WN, typename V, typename F>
+__device__ __forceinline__ void store_lines(uint16_t* q0, uint16_t* q1, uint16_t* q2, uint16_t* q3, V* to, int64_t ld,
+                                            int64_t m0, int64_t n0, int64_t gm, int64_t width, F&& value) {
+  constexpr int FM = BM / WM / 16, FN = BN / WN / 16, kThreads = WM * WN * 64, kChunks = BN / 8;
+  static_assert(sizeof(V) == 2 && BM <= 256 && kThreads / kChunks <= 64, "a pass of the threads is within a buffer");
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int wm = wave / WN, wn = wave % WN;
+  auto buffer = [](int piece, uint16_t* p0, uint16_t* p1, uint16_t* p2, uint16_t* p3) __attribute__((always_inline)) {
+    uint16_t* p = p0;
+    if (BM > 64 && piece == 1) p = p1;
+    if (BM > 128 && piece == 2) p = p2;
+    if (BM > 128 && piece == 3) p = p3;
+    return p;
+  };
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int first = wm * (BM / WM) + i * 16, r = first % 64 + lane % 16;
+    uint16_t* at = buffer(first / 64, q0, q1, q2, q3) + r * BN;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int c = wn * (BN / WN) + j * 16 + lane / 16 * 4;
+      const V v[4] = {value(i, j, 0), value(i, j, 1), value(i, j, 2), value(i, j, 3)};
+      __builtin_memcpy(at + ((c / 8 ^ r % kChunks) * 8) + c % 8, v, 8);
+    }
+  }
+  wait_and_meet<63>();
+#pragma unroll
+  for (int t = 0; t < BM * kChunks / kThreads; ++t) {
+    const int u = t * kThreads + static_cast<int>(threadIdx.x), r = u / kChunks, c = u % kChunks;
+    const uint16_t* from = buffer(t * kThreads / kChunks / 64, q0, q1, q2, q3) + r % 64 * BN + (c ^ r % kChunks) * 8;
+    const int64_t m = m0 + r, n = n0 + c * 8;
+    if (m >= gm || n >= width) continue;
+    const u16x8 v = *reinterpret_cast<const u16x8*>(from);
+    V* row = to + m * ld + n;
+    if (n + 8 <= width) {
+      __builtin_memcpy(row, &v, 16);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 7; ++q)
+        if (n + q < width) row[q] = __builtin_bit_cast(V, static_cast<uint16_t>(v[q]));
+    }
+  }
+}
+
 // Tile `id` of the batches' tiles, share `share` of its steps.
 template <typename Dt, int BM, int BN, int WM, int WN, int KS, int S, bool AAcross, bool BAcross, int Epi>
 __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int share, uint16_t* a0, uint16_t* b0,
                                           uint16_t* a1, uint16_t* b1, uint16_t* a2, uint16_t* b2, uint16_t* a3,
                                           uint16_t* b3) {
   using E = typename Dt::E;
-  constexpr bool kPair = Epi == kEpiGated || Epi == kEpiGatedBwd;
+  constexpr bool kPair = Epi == kEpiGated || Epi == kEpiGatedBwd, kDense = Epi == kEpiDense || Epi == kEpiDenseBwd;
+  constexpr bool kUnits = Dt::kScaled && !kPair && !kDense;  // operands may come in scaled blocks
   constexpr int kWaves = WM * WN, P = Dt::kPlanes;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // fragments per wave
   constexpr int kStageA = P * BM * KS, kStageB = P * BN * KS;
@@ -643,7 +715,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
       }
     }
   };
-  if constexpr (Dt::kScaled && !kPair) {
+  if constexpr (kUnits) {
     if (g.ea[z * g.phases]) load_seen(along_a, seen_a);
     if constexpr (kScaledB)
       if (g.eb[z * g.phases]) load_seen(along_b, seen_b);
@@ -651,7 +723,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
   issue(a0, b0);
   if constexpr (S > 2) issue(a1, b1);
   if constexpr (S > 3) issue(a2, b2);
-  if constexpr (Dt::kScaled && !kPair) {
+  if constexpr (kUnits) {
     if (g.ea[z * g.phases]) look(along_a, seen_a, unit_a, least_a);
     if constexpr (kScaledB)
       if (g.eb[z * g.phases]) look(along_b, seen_b, unit_b, least_b);
@@ -673,7 +745,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
 
   // ---------------------------------------------------------- epilogue
   if constexpr (!kPair) {
-    if constexpr (Dt::kScaled) {
+    if constexpr (kUnits) {
       if (in_units) {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
@@ -684,36 +756,41 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
     }
     using T = std::conditional_t<Epi == kEpiStoreF32, float, typename Dt::T>;
     const int64_t row0 = m0 + wm * (BM / WM) + lane % 16, col0 = n0 + wn * (BN / WN) + lane / 16 * 4;
-    constexpr bool kDense = Epi == kEpiDense || Epi == kEpiDenseBwd;
     if constexpr (kDense) {
       v4f bias[FN];
 #pragma unroll
       for (int j = 0; j < FN; ++j)
         bias[j] = g.bias ? load_four(static_cast<const T*>(g.bias), col0 + j * 16, gn) : v4f{0.f, 0.f, 0.f, 0.f};
+      with_act(g.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int64_t m = row0 + i * 16;
-        const T* row = static_cast<const T*>(g.res) + (m < gm ? m : 0) * g.ld_res;
+        for (int i = 0; i < FM; ++i) {
+          // all rows' loads and slopes at once do not fit in the registers
+          if (FM * FN >= 32) {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          const int64_t m = row0 + i * 16;
+          const T* row = static_cast<const T*>(g.res) + (m < gm ? m : 0) * g.ld_res;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          // past the last row and column the gradients are zero, the products too
-          v4f r = {0.f, 0.f, 0.f, 0.f};
-          if (g.res && m < gm) r = load_four(row, col0 + j * 16, gn);
+          for (int j = 0; j < FN; ++j) {
+            // past the last row and column the gradients are zero, the products too
+            v4f r = {0.f, 0.f, 0.f, 0.f};
+            if (g.res && m < gm) r = load_four(row, col0 + j * 16, gn);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float v = acc[i][j][q] + bias[j][q];
-            if constexpr (Epi == kEpiDense) {
-              acc[i][j][q] = dense_act(v, g.act) + r[q];
-            } else {
-              float value, slope;
-              act_both(v, g.act, value, slope);
-              acc[i][j][q] = r[q] * slope;
+            for (int q = 0; q < 4; ++q) {
+              const float z = acc[i][j][q] + bias[j][q];
+              acc[i][j][q] = Epi == kEpiDense ? dense_act(act, z) + r[q] : r[q] * dense_slope(act, z);
             }
           }
         }
-      }
+      });
     }
-    if constexpr (Epi != kEpiDenseBwd) {
+    static_assert(!kDense || (64 * BN <= kStageA && 64 * BN <= kStageB && (P == 1 || BM <= 128)), "64 rows fit in a buffer");
+    if constexpr (Epi == kEpiDense && sizeof(T) == 2) {
+      wait_and_meet<0>();  // every wave has read its last fragments
+      store_lines<BM, BN, WM, WN>(a0, b0, a1, b1, static_cast<T*>(g.c[z]), g.ldc[z], m0, n0, gm, gn,
+                                  [&](int i, int j, int q) { return static_cast<T>(acc[i][j][q]); });
+    } else if constexpr (Epi != kEpiDenseBwd) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int64_t m = row0 + i * 16;
@@ -735,6 +812,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
         }
       }
     } else {
+      wait_and_meet<0>();  // every wave has read its last fragments
       if (g.column_sums) {
         float* sums = g.column_sums + (m0 / BM * WM + wm) * gn;
 #pragma unroll
@@ -753,7 +831,6 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
         constexpr int kRows = BM / WM > 64 ? BM / WM / 64 : 1, kCols = BN / WN / 32, kPer = FM / kRows;
         static_assert(BM == 64 ? WM == 2 && BN / WN == 32 : BM / WM % 64 == 0 && BN / WN % 32 == 0,
                       "a wave holds whole blocks, or half of one");
-        if constexpr (BM == 64) wait_and_meet<0>();  // every wave has read its last fragments
 #pragma unroll
         for (int b = 0; b < kRows; ++b)
 #pragma unroll
@@ -782,30 +859,23 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
             if (lane == 0 && (BM > 64 || wm == 0) && m < gm && n < gn) g.e_dg[m / 64 * g.e_ld + n / 32] = e;
           }
       }
-      const int64_t width = (gn + 7) / 8 * 8;  // rows of the products' operands are read in 16-byte chunks
+      // rows of the products' operands are read in 16-byte chunks
+      const int64_t width = (gn + 7) / 8 * 8;
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int64_t m = row0 + i * 16;
-        if (m >= gm) continue;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          const int64_t n = col0 + j * 16;
-          if (n >= width) continue;
-          E e[P][4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if constexpr (P == 1) {
-              e[0][q] = static_cast<E>(acc[i][j][q]);
-            } else {
-              bf16 s[3];
-              split3(acc[i][j][q], s);
-#pragma unroll
-              for (int p = 0; p < P; ++p) e[p][q] = s[p];
-            }
-          }
-#pragma unroll
-          for (int p = 0; p < P; ++p) __builtin_memcpy(g.dg + p * g.plane_stride + m * g.ldh + n, e[p], 8);
-        }
+      for (int p = 0; p < P; ++p) {
+        // a plane's buffers are free again when the next has left
+        constexpr bool kTurns = P > 1;
+        store_lines<BM, BN, WM, WN>(kTurns && p % 2 ? a1 : a0, kTurns && p % 2 ? b1 : b0, kTurns ? a0 : a1,
+                                    kTurns ? b0 : b1, reinterpret_cast<E*>(g.dg) + p * g.plane_stride, g.ldh, m0, n0, gm,
+                                    width, [&](int i, int j, int q) {
+                                      if constexpr (P == 1) {
+                                        return static_cast<E>(acc[i][j][q]);
+                                      } else {
+                                        bf16 s[3];
+                                        split3(acc[i][j][q], s);
+                                        return s[p];
+                                      }
+                                    });
       }
     }
   } else {

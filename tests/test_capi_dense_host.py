@@ -32,9 +32,9 @@ COMMON = [(dict(dtype=sp.F64), sp.E_UNSUPPORTED), (dict(dtype=9), sp.E_INVALID),
     (dict(os=7), sp.E_INVALID), (dict(rs=-1), sp.E_INVALID),
     (dict(n=0, x=None, w=None, out=None, ws=None), sp.OK)])
 def test_dense_fwd(change, code):
-    a = dict(dtype=sp.BF16, act=0, x=P, xs=8, w=P, bias=P, res=P, rs=8, n=40, d_in=8, d_out=8, out=P, os=8, ws=P, short=0)
+    a = dict(dtype=sp.BF16, act=0, x=P, xs=512, w=P, bias=P, res=P, rs=8, n=40, d_in=512, d_out=8, out=P, os=8, ws=P, short=0)
     a.update(change)
-    rc, size = need(sp.BF16, 0, 40, 8, 8, 0)
+    rc, size = need(sp.BF16, 0, 40, 512, 8, 0)
     assert rc == sp.OK and size > 0
     assert sp.lib.dense_fwd(a["dtype"], a["act"], a["x"], a["xs"], a["w"], a["bias"], a["res"], a["rs"], a["n"],
                             a["d_in"], a["d_out"], a["out"], a["os"], a["ws"], size - a["short"], None) == code
