@@ -8,7 +8,8 @@
 //             dx = d W, dW = d^T x, dbias = sums of d's columns
 // Between the products d is held in the operands' type, as it is an operand of
 // matrix instructions: one rounding of a term of a long sum, the size of the
-// inputs' own (float16 in scaled blocks, float32 in three planes, gemm_tile.hpp).
+// inputs' own (float16 in scaled blocks, gemm_tile.hpp; float32 as it is,
+// gemm_staged.hpp).
 // The column sums are of d before that rounding: each wave of the product leaves
 // its rows' in float32, a second launch adds them in order.
 #pragma once
@@ -172,6 +173,8 @@ int dense_bwd(const DenseArgs& a, size_t* bytes) {
   GemmArgs dw = product<Dt>(a.d_out, a.d_in, a.n, d, x, a.gw, a.d_in);
   SplitSpace<Dt> space;  // sized for every gradient, asked for or not
   space.add(space.of(dx) + space.of(dw));
+  space.add(space.of(plan_split_wide<Dt>(dx)));
+  space.add(space.of(plan_split_wide<Dt>(dw)));
   float* sums = plan.arena.template take<float>(space.most);
   float* columns = plan.arena.template take<float>((product_again ? (a.n + 63) / 64 * 2 + 2 : segments(a.n)) * a.d_out);
   if (worst) {
@@ -200,8 +203,8 @@ int dense_bwd(const DenseArgs& a, size_t* bytes) {
   if (rc) return rc;
   const int64_t tiles = round_up(a.d_in, 64) / 64 * (round_up(a.d_out, 64) / 64 + round_up(a.n, 64) / 64);
   if (a.gx && a.gw && tiles <= 2 * 768) return gemm_launch_two_split<Dt>(dx, dw, sums, st);
-  if (a.gx) rc = gemm_launch_split<Dt, false, true, kEpiStore>(dx, sums, st);
-  if (!rc && a.gw) rc = gemm_launch_split<Dt, true, true, kEpiStore>(dw, sums, st);
+  if (a.gx) rc = gemm_launch_split<Dt, false, true, kEpiStore, true>(dx, sums, st);
+  if (!rc && a.gw) rc = gemm_launch_split<Dt, true, true, kEpiStore, true>(dw, sums, st);
   return rc;
 }
 

@@ -4,8 +4,8 @@
 namespace segpoly {
 namespace kern {
 
-int dense_fwd_f32(const DenseArgs& a, size_t* bytes) { return dense_fwd<DtF32>(a, bytes); }
-int dense_bwd_f32(const DenseArgs& a, size_t* bytes) { return dense_bwd<DtF32>(a, bytes); }
+int dense_fwd_f32(const DenseArgs& a, size_t* bytes) { return dense_fwd<DtF32Staged>(a, bytes); }
+int dense_bwd_f32(const DenseArgs& a, size_t* bytes) { return dense_bwd<DtF32Staged>(a, bytes); }
 
 }  // namespace kern
 }  // namespace segpoly

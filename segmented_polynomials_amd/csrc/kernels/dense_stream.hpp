@@ -22,7 +22,7 @@
 #pragma once
 #include <algorithm>
 
-#include "gemm_rows.hpp"
+#include "gemm_staged.hpp"
 
 namespace segpoly {
 namespace kern {
@@ -35,68 +35,6 @@ struct StreamArgs {
   int pairs;  // of column fragments, of a workgroup: (x, y) takes the y-th part of the columns
 };
 
-// Eight float32 as planes.  Values that would round up to infinity, infinities and
-// NaN take split3; a wave without any, nearly all, goes without its comparisons.
-__device__ __forceinline__ void split_eight(const float (&v)[8], u16x8 (&p)[3]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu;
-    top = b > top ? b : top;
-  }
-  if (__ballot(top >= 0x7f7f8000u)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      bf16 s[3];
-      split3(v[i], s);
-#pragma unroll
-      for (int q = 0; q < 3; ++q) p[q][i] = __builtin_bit_cast(uint16_t, s[q]);
-    }
-    return;
-  }
-  float r[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = v[i];
-#pragma unroll
-  for (int q = 0; q < 3; ++q)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bf16 s = static_cast<bf16>(r[i]);
-      p[q][i] = __builtin_bit_cast(uint16_t, s);
-      if (q < 2) r[i] -= static_cast<float>(s);
-    }
-}
-// Eight elements of a row from column `at` on, and as matrix operands.  Whole: of
-// rows whose width is a multiple of eight, no chunk crosses the end.
-template <typename Dt, bool Whole>
-__device__ __forceinline__ void load_eight(RowChunk<Dt>& c, const typename Dt::T* row, int at, int width) {
-  if constexpr (Whole) {
-#pragma unroll
-    for (int i = 0; i < RowChunk<Dt>::kLoads; ++i) c.raw[i] = u32x4{0, 0, 0, 0};
-    if (at < width) __builtin_memcpy(c.raw, row + at, sizeof(c.raw));
-  } else {
-    c.load(row, at, width);
-  }
-}
-template <typename Dt, bool Whole>
-__device__ __forceinline__ void chunk_planes(const RowChunk<Dt>& c, int at, int width, u16x8 (&p)[Dt::kPlanes]) {
-  if constexpr (Dt::kPlanes == 1) {
-    if constexpr (Whole)
-      p[0] = __builtin_bit_cast(u16x8, c.raw[0]);
-    else
-      c.planes(at, width, p);
-  } else {
-    float v[8];
-    if constexpr (Whole) {
-      __builtin_memcpy(v, c.raw, sizeof(v));
-    } else {
-      unpack_chunk<float>(c.raw[0], at, width, v);
-      unpack_chunk<float>(c.raw[1], at + 4, width, v + 4);
-    }
-    split_eight(v, p);
-  }
-}
-
 // columns of a row of fragments: fragment pair * 2 + j, row i of the instruction
 __device__ __forceinline__ int stream_column(int fragment, int i) {
   return fragment / 2 * 32 + i / 4 * 8 + fragment % 2 * 4 + i % 4;
@@ -104,7 +42,7 @@ __device__ __forceinline__ int stream_column(int fragment, int i) {
 
 // KC: 32 k each of a row.  Loads return in order: the residual's would wait for the
 // next rows' if those were on their way already, so with it they are fetched later.
-// Whole: both widths are multiples of eight.
+// Whole: x's width is a multiple of 16 bytes, the output's of eight columns.
 template <typename Dt, int KC, int R, bool Res, bool Whole>
 __global__ void __launch_bounds__(512)
 dense_stream_kernel(StreamArgs g) {
@@ -251,7 +189,7 @@ int stream_launch(StreamArgs g, hipStream_t st) {
   const int64_t groups = (all + pairs - 1) / pairs;
   g.pairs = static_cast<int>((all + groups - 1) / groups);
   const int64_t blocks = std::min<int64_t>(tiles, std::max<int64_t>(1, 512 / groups));
-  const bool whole = g.k % 8 == 0 && g.cols % 8 == 0;
+  const bool whole = g.k % Chunk<typename Dt::T>::kN == 0 && g.cols % 8 == 0;
   auto* kernel = whole ? (g.res ? dense_stream_kernel<Dt, KC, R, true, true> : dense_stream_kernel<Dt, KC, R, false, true>)
                        : (g.res ? dense_stream_kernel<Dt, KC, R, true, false> : dense_stream_kernel<Dt, KC, R, false, false>);
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(groups)), dim3(512),

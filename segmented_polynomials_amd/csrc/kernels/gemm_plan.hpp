@@ -6,6 +6,7 @@
 #include <cmath>
 
 #include "../launch.hpp"
+#include "gemm_staged.hpp"
 #include "gemm_tile.hpp"
 
 namespace segpoly {
@@ -79,6 +80,12 @@ void add_phase(GemmArgs& g, int& at, const Operand& a, const Operand& b, const O
   ++at;
 }
 
+// rows of both staged operands in multiples of 16 bytes
+template <bool AAcross, bool BAcross>
+bool staged_whole(const GemmArgs& g) {
+  return (AAcross ? g.m[0] : g.k) % 4 == 0 && (BAcross ? g.n[0] : g.k) % 4 == 0;
+}
+
 template <typename Dt, int BM, int BN, int WM, int WN, int KS, int S, bool AAcross, bool BAcross, int Epi>
 int gemm_launch_tile(GemmArgs& g, hipStream_t st) {
   const int64_t bn = Epi == kEpiGated || Epi == kEpiGatedBwd ? BN / 2 : BN;
@@ -91,8 +98,15 @@ int gemm_launch_tile(GemmArgs& g, hipStream_t st) {
   if (tiles == 0) return 0;  // no rows
   if (g.splits < 1) g.splits = 1;
   g.column_rows = g.tiles_m[0] * WM;
-  hipLaunchKernelGGL((gemm_tile_kernel<Dt, BM, BN, WM, WN, KS, S, AAcross, BAcross, Epi>),
-                     dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(g.splits)), dim3(WM * WN * 64), 0, st, g);
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(g.splits));
+  if constexpr (kStaged<Dt>) {
+    auto* kernel = staged_whole<AAcross, BAcross>(g) ? gemm_staged_kernel<BM, BN, WM, WN, AAcross, BAcross, Epi, true>
+                                                     : gemm_staged_kernel<BM, BN, WM, WN, AAcross, BAcross, Epi, false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(WM * WN * 64), 0, st, g);
+  } else {
+    hipLaunchKernelGGL((gemm_tile_kernel<Dt, BM, BN, WM, WN, KS, S, AAcross, BAcross, Epi>), grid, dim3(WM * WN * 64), 0, st,
+                       g);
+  }
   return static_cast<int>(hipGetLastError());
 }
 
@@ -120,6 +134,22 @@ Split plan_split(const GemmArgs& g) {
   const int64_t steps = (g.k + kStep - 1) / kStep * g.phases;
   if (tiles > 0 && tiles < 384)
     p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(768 / tiles, steps / 16)));
+  return p;
+}
+
+// The same in tiles of 128 x 128, each element read and split or moved by half as
+// many tiles, where their shares fill the card: a compute unit holds one workgroup of
+// staged operands, two of others.  One MI355X, us of the weight's gradient: OLD_WIDE
+template <typename Dt>
+Split plan_split_wide(const GemmArgs& g) {
+  constexpr int64_t kStep = Dt::kPlanes == 1 ? 64 : 32, kHeld = Dt::kPlanes == 1 ? 512 : 256;
+  Split p;
+  if (g.batch != 1 || g.phases != 1 || g.m[0] <= 64 || g.n[0] <= 64) return p;
+  const int64_t tiles = (g.m[0] + 127) / 128 * ((g.n[0] + 127) / 128), steps = (g.k + kStep - 1) / kStep;
+  const int64_t splits = std::min(kHeld / tiles, steps / 16);
+  if (splits < 2 || tiles * splits * 4 < kHeld * 3) return p;
+  p.splits = static_cast<int>(splits);
+  p.elements = g.m[0] * round_up(g.n[0], 4);
   return p;
 }
 
@@ -160,15 +190,26 @@ constexpr int kSmallS = Dt::kPlanes == 1 ? 3 : 2;
 
 // A product with a plain epilogue, split if that pays; `sums` is the space that
 // SplitSpace found for it.
-template <typename Dt, bool AAcross, bool BAcross, int Epi>
+template <typename Dt, bool AAcross, bool BAcross, int Epi, bool Wide = false>
 int gemm_launch_split(GemmArgs& g, float* sums, hipStream_t st) {
   using T = std::conditional_t<Epi == kEpiStoreF32, float, typename Dt::T>;
-  const Split p = plan_split<Dt>(g);
-  if (p.splits == 1) return gemm_launch<Dt, AAcross, BAcross, Epi>(g, st);
   SplitSumArgs q{};
-  split_into(g, p, sums, q);
-  const int rc =
-      gemm_launch_tile<Dt, 64, 64, 2, 2, kSmallK<Dt>, kSmallS<Dt>, AAcross, BAcross, kEpiStoreF32>(g, st);
+  int rc;
+  const Split wide = Wide ? plan_split_wide<Dt>(g) : Split{};
+  if (wide.splits > 1) {
+    if constexpr (Wide) {
+      split_into(g, wide, sums, q);
+      if constexpr (Dt::kPlanes == 1)
+        rc = gemm_launch_tile<Dt, 128, 128, 2, 2, 64, 2, AAcross, BAcross, kEpiStoreF32>(g, st);
+      else
+        rc = gemm_launch_tile<Dt, 128, 128, 2, 4, 32, 2, AAcross, BAcross, kEpiStoreF32>(g, st);
+    }
+  } else {
+    const Split p = plan_split<Dt>(g);
+    if (p.splits == 1) return gemm_launch<Dt, AAcross, BAcross, Epi>(g, st);
+    split_into(g, p, sums, q);
+    rc = gemm_launch_tile<Dt, 64, 64, 2, 2, kSmallK<Dt>, kSmallS<Dt>, AAcross, BAcross, kEpiStoreF32>(g, st);
+  }
   return rc ? rc : split_sum_launch<T>(q, st);
 }
 
@@ -186,8 +227,15 @@ int gemm_launch_two(GemmArgs& x, GemmArgs& w, hipStream_t st) {
   }
   const int64_t blocks = tiles[0] * x.splits + tiles[1] * w.splits;
   if (blocks == 0) return 0;
-  hipLaunchKernelGGL((gemm_two_kernel<Dt, kSmallK<Dt>, kSmallS<Dt>, EpiX, EpiW>), dim3(static_cast<unsigned>(blocks)),
-                     dim3(256), 0, st, x, w, tiles[0], tiles[1]);
+  const dim3 grid(static_cast<unsigned>(blocks));
+  if constexpr (kStaged<Dt>) {
+    auto* kernel = staged_whole<false, true>(x) && staged_whole<true, true>(w) ? gemm_staged_two_kernel<EpiX, EpiW, true>
+                                                                               : gemm_staged_two_kernel<EpiX, EpiW, false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, x, w, tiles[0], tiles[1]);
+  } else {
+    hipLaunchKernelGGL((gemm_two_kernel<Dt, kSmallK<Dt>, kSmallS<Dt>, EpiX, EpiW>), grid, dim3(256), 0, st, x, w, tiles[0],
+                       tiles[1]);
+  }
   return static_cast<int>(hipGetLastError());
 }
 
@@ -278,7 +326,7 @@ struct MatrixPlan {
   // last where rows overlap (each starts within the one before).
   Operand use(const void* src, int64_t rows, int64_t width, int64_t ld, bool worst, bool summed = false) {
     Operand o{};
-    if (!worst && P == 1 && !(summed && ld < width) && width % 8 == 0 && ld % 8 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0) {
+    if (kStaged<Dt> || (!worst && P == 1 && !(summed && ld < width) && width % 8 == 0 && ld % 8 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0)) {
       o.plane[0] = static_cast<const uint16_t*>(src);
       o.ld = ld;
       return o;
@@ -295,6 +343,11 @@ struct MatrixPlan {
   }
   Operand hidden(int64_t n, int64_t hidden) {
     Operand o{};
+    if constexpr (kStaged<Dt>) {  // float32 rows
+      o.ld = round_up(hidden, 4);
+      o.plane[0] = reinterpret_cast<const uint16_t*>(arena.take<float>(n * o.ld));
+      return o;
+    }
     o.ld = round_up(hidden, 64);
     uint16_t* p = arena.take<uint16_t>(P * n * o.ld);
     if (p)
@@ -317,10 +370,8 @@ struct MatrixPlan {
 template <typename Dt>
 struct SplitSpace {
   int64_t most = 0;
-  static int64_t of(const GemmArgs& g) {
-    const Split p = plan_split<Dt>(g);
-    return p.splits > 1 ? p.splits * p.elements : 0;
-  }
+  static int64_t of(const GemmArgs& g) { return of(plan_split<Dt>(g)); }
+  static int64_t of(const Split& p) { return p.splits > 1 ? p.splits * p.elements : 0; }
   void add(int64_t elements) { most = std::max(most, elements); }
 };
 

@@ -62,8 +62,8 @@ struct GemmArgs {
   int64_t e_ld;
   // epilogue of the dense operator, all of the io type: [n], [m][ld_res], either
   // null.  Forward: c = act(product + bias) + res.  Backward: res is the gradient
-  // of the output; dg and e_dg as above, and the sums of dg's columns over each
-  // wave's rows, [column_rows][n], or null.
+  // of the output; dg (of float32 operands [m][ldh] float32) and e_dg as above, and
+  // the sums of dg's columns over each wave's rows, [column_rows][n], or null.
   const void *bias, *res;
   int64_t ld_res, column_rows;  // tiles_m times the tile's waves along m, at most 2 ceil(m / 64) + 2
   float* column_sums;
@@ -71,12 +71,16 @@ struct GemmArgs {
 
 enum { kEpiStore = 0, kEpiStoreF32 = 1, kEpiGated = 2, kEpiGatedBwd = 3, kEpiDense = 4, kEpiDenseBwd = 5 };
 
-// io type T, matrix type E, planes per operand, products held in scaled blocks
+// io type T, matrix type E, planes per operand, products held in scaled blocks;
+// staged: operands are read as they are (gemm_staged.hpp)
 struct DtBF16 { using T = bf16; using E = bf16; static constexpr int kPlanes = 1; static constexpr bool kScaled = false; };
 struct DtF16 { using T = f16; using E = f16; static constexpr int kPlanes = 1; static constexpr bool kScaled = true; };
 // without scaled blocks: of products whose operands are the caller's
 struct DtF16Plain { using T = f16; using E = f16; static constexpr int kPlanes = 1; static constexpr bool kScaled = false; };
 struct DtF32 { using T = float; using E = bf16; static constexpr int kPlanes = 3; static constexpr bool kScaled = false; };
+struct DtF32Staged : DtF32 {};
+template <typename Dt>
+constexpr bool kStaged = std::is_same_v<Dt, DtF32Staged>;
 
 // float16 reaches from 2^-24 to 2^16.  A value that is held in it between two
 // products can pass both ends where the inputs and the result do not, so its
@@ -341,6 +345,18 @@ struct TileLds {
   __shared__ __attribute__((aligned(16))) uint16_t a3[L::kA3];     \
   __shared__ __attribute__((aligned(16))) uint16_t b3[L::kB3]
 
+// Workgroups go round the eight dies, each with its own L2: give each die
+// a run of neighbouring tiles, in bands of eight tile rows.
+template <int BM, int BN>
+__device__ __forceinline__ void tile_corner(int64_t id, int64_t tiles_m, int64_t tiles_n, int64_t& m0, int64_t& n0) {
+  const int64_t die = id % 8, tiles = tiles_m * tiles_n, q = tiles / 8, r = tiles % 8;
+  const int64_t t = die * q + (die < r ? die : r) + id / 8;
+  const int64_t band = t / (8 * tiles_n), in_band = t % (8 * tiles_n);
+  const int64_t band_rows = tiles_m - band * 8 < 8 ? tiles_m - band * 8 : 8;
+  m0 = (band * 8 + in_band % band_rows) * BM;
+  n0 = in_band / band_rows * BN;
+}
+
 // The results of a BM x BN tile, 16 bits each, to rows m < gm, columns n < width of
 // `to`.  A fragment's lanes hold four columns of sixteen rows, 32 bytes of a line:
 // they go through LDS, 64 rows to a buffer, and leave in whole lines.  16-byte slot
@@ -390,6 +406,134 @@ __device__ __forceinline__ void store_lines(uint16_t* q0, uint16_t* q1, uint16_t
   }
 }
 
+// The epilogue of a product with one output: a tile's sums, batch z, corner (m0, n0).
+template <typename Dt, int BM, int BN, int WM, int WN, int KS, int Epi>
+__device__ __forceinline__ void finish_tile(const GemmArgs& g, int z, int64_t m0, int64_t n0, int share,
+                                            v4f (&acc)[BM / WM / 16][BN / WN / 16], uint16_t* a0, uint16_t* b0,
+                                            uint16_t* a1, uint16_t* b1) {
+  using E = typename Dt::E;
+  constexpr bool kDense = Epi == kEpiDense || Epi == kEpiDenseBwd;
+  constexpr int P = Dt::kPlanes, FM = BM / WM / 16, FN = BN / WN / 16;
+  const int lane = threadIdx.x % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int wm = wave / WN, wn = wave % WN;
+  const int64_t gm = g.m[z], gn = g.n[z];
+  using T = std::conditional_t<Epi == kEpiStoreF32, float, typename Dt::T>;
+  const int64_t row0 = m0 + wm * (BM / WM) + lane % 16, col0 = n0 + wn * (BN / WN) + lane / 16 * 4;
+  if constexpr (kDense) {
+    v4f bias[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      bias[j] = g.bias ? load_four(static_cast<const T*>(g.bias), col0 + j * 16, gn) : v4f{0.f, 0.f, 0.f, 0.f};
+    with_act(g.act, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        // all rows' loads and slopes at once do not fit in the registers
+        if (FM * FN >= 32) {
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        const int64_t m = row0 + i * 16;
+        const T* row = static_cast<const T*>(g.res) + (m < gm ? m : 0) * g.ld_res;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          // past the last row and column the gradients are zero, the products too
+          v4f r = {0.f, 0.f, 0.f, 0.f};
+          if (g.res && m < gm) r = load_four(row, col0 + j * 16, gn);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float z = acc[i][j][q] + bias[j][q];
+            acc[i][j][q] = Epi == kEpiDense ? dense_act(act, z) + r[q] : r[q] * dense_slope(act, z);
+          }
+        }
+      }
+    });
+  }
+  // float32 rows: 16 bytes a lane, 64 of a row together
+  auto store_rows = [&](T* to, int64_t ld) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int64_t m = row0 + i * 16;
+      if (m >= gm) continue;
+      T* row = to + m * ld;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int64_t n = col0 + j * 16;
+        T v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = static_cast<T>(acc[i][j][q]);
+        if (n + 4 <= gn) {
+          __builtin_memcpy(row + n, v, sizeof(v));
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (n + q < gn) row[n + q] = v[q];
+        }
+      }
+    }
+  };
+  static_assert(!kDense || P > 1 || (64 * BN <= BM * KS && 64 * BN <= BN * KS), "64 rows fit in a buffer");
+  if constexpr (Epi == kEpiDense && P == 1) {
+    wait_and_meet<0>();  // every wave has read its last fragments
+    store_lines<BM, BN, WM, WN>(a0, b0, a1, b1, static_cast<T*>(g.c[z]), g.ldc[z], m0, n0, gm, gn,
+                                [&](int i, int j, int q) { return static_cast<T>(acc[i][j][q]); });
+  } else if constexpr (Epi != kEpiDenseBwd) {
+    store_rows(static_cast<T*>(g.c[z]) + (Epi == kEpiStoreF32 ? g.split_stride * share : 0), g.ldc[z]);
+  } else {
+    if (g.column_sums) {
+      float* sums = g.column_sums + (m0 / BM * WM + wm) * gn;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float s = 0.f;
+#pragma unroll
+          for (int i = 0; i < FM; ++i) s += acc[i][j][q];
+          s = lane_sum<16>(s);
+          const int64_t n = col0 + j * 16 + q;
+          if (lane % 16 == 0 && n < gn) sums[n] = s;
+        }
+    }
+    if constexpr (P > 1) return store_rows(reinterpret_cast<float*>(g.dg), g.ldh);
+    wait_and_meet<0>();  // every wave has read its last fragments
+    if constexpr (Dt::kScaled) {
+      constexpr int kRows = BM / WM > 64 ? BM / WM / 64 : 1, kCols = BN / WN / 32, kPer = FM / kRows;
+      static_assert(BM == 64 ? WM == 2 && BN / WN == 32 : BM / WM % 64 == 0 && BN / WN % 32 == 0,
+                    "a wave holds whole blocks, or half of one");
+#pragma unroll
+      for (int b = 0; b < kRows; ++b)
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          float top = 0.f;
+#pragma unroll
+          for (int i = b * kPer; i < (b + 1) * kPer; ++i)
+#pragma unroll
+            for (int j = c * 2; j < c * 2 + 2; ++j)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) top = __builtin_fmaxf(top, finite_abs(acc[i][j][q]));
+          top = lane_max<64>(top);
+          if constexpr (BM == 64) {
+            float* shared = reinterpret_cast<float*>(b0);
+            if (lane == 0) shared[wave] = top;
+            wait_and_meet<63>();
+            top = __builtin_fmaxf(shared[wn], shared[WN + wn]);
+          }
+          const int e = block_exponent(top);
+          const float scale = block_scale(e);
+#pragma unroll
+          for (int i = b * kPer; i < (b + 1) * kPer; ++i)
+#pragma unroll
+            for (int j = c * 2; j < c * 2 + 2; ++j) acc[i][j] *= scale;
+          const int64_t m = m0 + wm * (BM / WM) + b * 64, n = n0 + wn * (BN / WN) + c * 32;
+          if (lane == 0 && (BM > 64 || wm == 0) && m < gm && n < gn) g.e_dg[m / 64 * g.e_ld + n / 32] = e;
+        }
+    }
+    if constexpr (P == 1)  // rows of the products' operands are read in 16-byte chunks
+      store_lines<BM, BN, WM, WN>(a0, b0, a1, b1, reinterpret_cast<E*>(g.dg), g.ldh, m0, n0, gm, (gn + 7) / 8 * 8,
+                                  [&](int i, int j, int q) { return static_cast<E>(acc[i][j][q]); });
+  }
+}
+
 // Tile `id` of the batches' tiles, share `share` of its steps.
 template <typename Dt, int BM, int BN, int WM, int WN, int KS, int S, bool AAcross, bool BAcross, int Epi>
 __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int share, uint16_t* a0, uint16_t* b0,
@@ -412,17 +556,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
   }
   const int64_t gm = g.m[z], gn = g.n[z], lda = g.lda[z], ldb = g.ldb[z], tiles_m = g.tiles_m[z], tiles_n = g.tiles_n[z];
 
-  // Workgroups go round the eight dies, each with its own L2: give each die
-  // a run of neighbouring tiles, in bands of eight tile rows.
-  int64_t t;
-  {
-    const int64_t die = id % 8, tiles = tiles_m * tiles_n, q = tiles / 8, r = tiles % 8;
-    t = die * q + (die < r ? die : r) + id / 8;
-  }
-  const int64_t band = t / (8 * tiles_n), in_band = t % (8 * tiles_n);
-  const int64_t band_rows = tiles_m - band * 8 < 8 ? tiles_m - band * 8 : 8;
-  const int64_t m0 = (band * 8 + in_band % band_rows) * BM;
-  const int64_t n0 = in_band / band_rows * (kPair ? BN / 2 : BN);
+  int64_t m0, n0;
+  tile_corner<BM, kPair ? BN / 2 : BN>(id, tiles_m, tiles_n, m0, n0);
 
   TileLoad<BM, KS, kWaves, AAcross> la;
   TileLoad<BN, KS, kWaves, BAcross> lb;
@@ -754,130 +889,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
             acc[i][j] *= power_of_two(unit_a[i / (FM / GA)]) * power_of_two(unit_b[j / (FN / GB)]);
       }
     }
-    using T = std::conditional_t<Epi == kEpiStoreF32, float, typename Dt::T>;
-    const int64_t row0 = m0 + wm * (BM / WM) + lane % 16, col0 = n0 + wn * (BN / WN) + lane / 16 * 4;
-    if constexpr (kDense) {
-      v4f bias[FN];
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-        bias[j] = g.bias ? load_four(static_cast<const T*>(g.bias), col0 + j * 16, gn) : v4f{0.f, 0.f, 0.f, 0.f};
-      with_act(g.act, [&](auto act) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          // all rows' loads and slopes at once do not fit in the registers
-          if (FM * FN >= 32) {
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_sched_barrier(0);
-          }
-          const int64_t m = row0 + i * 16;
-          const T* row = static_cast<const T*>(g.res) + (m < gm ? m : 0) * g.ld_res;
-#pragma unroll
-          for (int j = 0; j < FN; ++j) {
-            // past the last row and column the gradients are zero, the products too
-            v4f r = {0.f, 0.f, 0.f, 0.f};
-            if (g.res && m < gm) r = load_four(row, col0 + j * 16, gn);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float z = acc[i][j][q] + bias[j][q];
-              acc[i][j][q] = Epi == kEpiDense ? dense_act(act, z) + r[q] : r[q] * dense_slope(act, z);
-            }
-          }
-        }
-      });
-    }
-    static_assert(!kDense || (64 * BN <= kStageA && 64 * BN <= kStageB && (P == 1 || BM <= 128)), "64 rows fit in a buffer");
-    if constexpr (Epi == kEpiDense && sizeof(T) == 2) {
-      wait_and_meet<0>();  // every wave has read its last fragments
-      store_lines<BM, BN, WM, WN>(a0, b0, a1, b1, static_cast<T*>(g.c[z]), g.ldc[z], m0, n0, gm, gn,
-                                  [&](int i, int j, int q) { return static_cast<T>(acc[i][j][q]); });
-    } else if constexpr (Epi != kEpiDenseBwd) {
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int64_t m = row0 + i * 16;
-        if (m >= gm) continue;
-        T* row = static_cast<T*>(g.c[z]) + (Epi == kEpiStoreF32 ? g.split_stride * share : 0) + m * g.ldc[z];
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          const int64_t n = col0 + j * 16;
-          T v[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = static_cast<T>(acc[i][j][q]);
-          if (n + 4 <= gn) {
-            __builtin_memcpy(row + n, v, sizeof(v));
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (n + q < gn) row[n + q] = v[q];
-          }
-        }
-      }
-    } else {
-      wait_and_meet<0>();  // every wave has read its last fragments
-      if (g.column_sums) {
-        float* sums = g.column_sums + (m0 / BM * WM + wm) * gn;
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < FM; ++i) s += acc[i][j][q];
-            s = lane_sum<16>(s);
-            const int64_t n = col0 + j * 16 + q;
-            if (lane % 16 == 0 && n < gn) sums[n] = s;
-          }
-      }
-      if constexpr (Dt::kScaled) {
-        constexpr int kRows = BM / WM > 64 ? BM / WM / 64 : 1, kCols = BN / WN / 32, kPer = FM / kRows;
-        static_assert(BM == 64 ? WM == 2 && BN / WN == 32 : BM / WM % 64 == 0 && BN / WN % 32 == 0,
-                      "a wave holds whole blocks, or half of one");
-#pragma unroll
-        for (int b = 0; b < kRows; ++b)
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) {
-            float top = 0.f;
-#pragma unroll
-            for (int i = b * kPer; i < (b + 1) * kPer; ++i)
-#pragma unroll
-              for (int j = c * 2; j < c * 2 + 2; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) top = __builtin_fmaxf(top, finite_abs(acc[i][j][q]));
-            top = lane_max<64>(top);
-            if constexpr (BM == 64) {
-              float* shared = reinterpret_cast<float*>(b0);
-              if (lane == 0) shared[wave] = top;
-              wait_and_meet<63>();
-              top = __builtin_fmaxf(shared[wn], shared[WN + wn]);
-            }
-            const int e = block_exponent(top);
-            const float scale = block_scale(e);
-#pragma unroll
-            for (int i = b * kPer; i < (b + 1) * kPer; ++i)
-#pragma unroll
-              for (int j = c * 2; j < c * 2 + 2; ++j) acc[i][j] *= scale;
-            const int64_t m = m0 + wm * (BM / WM) + b * 64, n = n0 + wn * (BN / WN) + c * 32;
-            if (lane == 0 && (BM > 64 || wm == 0) && m < gm && n < gn) g.e_dg[m / 64 * g.e_ld + n / 32] = e;
-          }
-      }
-      // rows of the products' operands are read in 16-byte chunks
-      const int64_t width = (gn + 7) / 8 * 8;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        // a plane's buffers are free again when the next has left
-        constexpr bool kTurns = P > 1;
-        store_lines<BM, BN, WM, WN>(kTurns && p % 2 ? a1 : a0, kTurns && p % 2 ? b1 : b0, kTurns ? a0 : a1,
-                                    kTurns ? b0 : b1, reinterpret_cast<E*>(g.dg) + p * g.plane_stride, g.ldh, m0, n0, gm,
-                                    width, [&](int i, int j, int q) {
-                                      if constexpr (P == 1) {
-                                        return static_cast<E>(acc[i][j][q]);
-                                      } else {
-                                        bf16 s[3];
-                                        split3(acc[i][j][q], s);
-                                        return s[p];
-                                      }
-                                    });
-      }
-    }
+    finish_tile<Dt, BM, BN, WM, WN, KS, Epi>(g, z, m0, n0, share, acc, a0, b0, a1, b1);
   } else {
     // A fragment's lanes hold four columns of sixteen rows, 32 bytes of a line:
     // the results go through LDS, one 16-bit plane after another in two buffers,
