@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "column_sums.hpp"
+#include "dense_few.hpp"
 #include "dense_stream.hpp"
 #include "gemm_plan.hpp"
 #include "gemm_rows.hpp"
@@ -63,12 +64,27 @@ dense_sum_kernel(DenseSumArgs g) {
   }
 }
 
+template <typename T>
+int dense_sum(const DenseSumArgs& g, hipStream_t st) {
+  const int64_t blocks = std::min<int64_t>((g.m * (g.ld / 4) + 255) / 256, 2048);
+  hipLaunchKernelGGL(dense_sum_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, g);
+  return static_cast<int>(hipGetLastError());
+}
+
+// The shares of x w^T of few rows, [shares][n][ld].
+template <typename Dt>
+int few_sums(RowsArgs r, float* sums, int64_t ld, hipStream_t st) {
+  r.out = sums, r.ldo = ld, r.k_share = few_share(r.k, r.n), r.share_stride = r.m * ld;
+  return gemm_rows<Dt, kRowsSums>(r, st);
+}
+
 // Column sums of a segment of the rows: 32 chunks of 16 bytes by 8 rows at a
 // time, whose sums are added in order.
 constexpr int64_t kSegmentRows = 256;
 template <typename T>
 __global__ void __launch_bounds__(256)
-dense_columns_kernel(const void* __restrict__ src, int64_t n, int64_t stride, int64_t width, int64_t rows, float* sums) {
+dense_columns_kernel(const void* __restrict__ src, int64_t n, int64_t stride, int64_t width, int64_t rows, float* sums,
+                     int64_t ld_sums) {
   constexpr int V = Chunk<T>::kN;
   __shared__ float lds[8][32 * V];
   const int c = static_cast<int>((blockIdx.x * 32 + threadIdx.x % 32) * V), set = threadIdx.x / 32;
@@ -92,34 +108,51 @@ dense_columns_kernel(const void* __restrict__ src, int64_t n, int64_t stride, in
     float t = 0.f;
 #pragma unroll
     for (int q = 0; q < 8; ++q) t += lds[q][k];
-    sums[blockIdx.y * width + col] = t;
+    sums[blockIdx.y * ld_sums + col] = t;
   }
 }
+// to[m][c] = sum over p of sums[p][m][c], `ld` between rows
 template <typename T>
 __global__ void __launch_bounds__(1024)
-dense_fold_kernel(const float* __restrict__ sums, int64_t rows, int64_t width, T* to) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32;
-  const float t = column_sum(sums, rows, width, width, c);
-  if (threadIdx.x < 32 && c < width) to[c] = static_cast<T>(t);
+dense_fold_kernel(const float* __restrict__ sums, int64_t parts, int64_t ld, int64_t width, T* to) {
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32, m = blockIdx.y;
+  const float t = column_sum(sums + m * ld, parts, gridDim.y * ld, width, c);
+  if (threadIdx.x < 32 && c < width) to[m * width + c] = static_cast<T>(t);
+}
+template <typename T>
+int dense_fold(const float* sums, int64_t parts, int64_t rows, int64_t ld, int64_t width, void* to, hipStream_t st) {
+  hipLaunchKernelGGL(dense_fold_kernel<T>, dim3(static_cast<unsigned>((width + 31) / 32), static_cast<unsigned>(rows)),
+                     dim3(1024), 0, st, sums, parts, ld, width, static_cast<T*>(to));
+  return static_cast<int>(hipGetLastError());
 }
 
 // rows of a segment: as many segments as fill the card a few times, within the launch's limit
 inline int64_t segment_rows(int64_t n) { return std::max(kSegmentRows, round_up((n + 32767) / 32768, 8)); }
 inline int64_t segments(int64_t n) { return (n + segment_rows(n) - 1) / segment_rows(n); }
 
+constexpr int64_t kFewRows = 16, kFewRowsBwd = 4;
+
 template <typename Dt>
 int dense_fwd(const DenseArgs& a, size_t* bytes) {
   using T = typename Dt::T;
   const bool worst = bytes != nullptr;
   const hipStream_t st = static_cast<hipStream_t>(a.stream);
-  if (a.n <= 16) {
+  if (a.n <= kFewRows) {
+    const int64_t shares = few_shares(a.d_in, a.d_out);
+    Arena arena{static_cast<char*>(a.workspace)};
+    const int64_t ld = round_up(a.d_out, 4);
+    float* sums = arena.take<float>(shares > 1 ? shares * a.n * ld : 0);
     if (worst) {
-      *bytes = 0;
+      *bytes = arena.at;
       return 0;
     }
     RowsArgs r{a.x, a.w, nullptr, a.out, nullptr, nullptr, a.n, a.d_out, a.d_in, a.x_stride, a.out_stride, a.act};
     r.bias = a.bias, r.res = a.residual, r.ld_res = a.residual_stride;
-    return gemm_rows<Dt, kRowsDense>(r, st);
+    if (shares == 1) return gemm_rows<Dt, kRowsDense>(r, st);
+    const int rc = few_sums<Dt>(r, sums, ld, st);
+    return rc ? rc
+              : dense_sum<T>({sums, a.n * ld, a.n, a.d_out, ld, static_cast<int>(shares), a.act, a.bias, a.residual,
+                              a.residual_stride, a.out, a.out_stride}, st);
   }
   if (stream_chunks<Dt>(a.d_in)) {
     if (worst) {
@@ -149,16 +182,50 @@ int dense_fwd(const DenseArgs& a, size_t* bytes) {
   split_into(g, p, sums, q);
   rc = gemm_launch_tile<Dt, 64, 64, 2, 2, kSmallK<Dt>, kSmallS<Dt>, false, false, kEpiStoreF32>(g, st);
   if (rc) return rc;
-  const DenseSumArgs s{sums, q.split_stride[0], a.n, a.d_out, q.ld[0], p.splits, a.act,
-                       a.bias, a.residual, a.residual_stride, a.out, a.out_stride};
-  const int64_t blocks = std::min<int64_t>((a.n * (q.ld[0] / 4) + 255) / 256, 2048);
-  hipLaunchKernelGGL(dense_sum_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, s);
-  return static_cast<int>(hipGetLastError());
+  return dense_sum<T>({sums, q.split_stride[0], a.n, a.d_out, q.ld[0], p.splits, a.act, a.bias, a.residual,
+                       a.residual_stride, a.out, a.out_stride}, st);
+}
+
+// At most kFewRowsBwd rows: three or four launches, each about as long as the weight
+// takes to cross memory once.
+template <typename Dt>
+int dense_bwd_few(const DenseArgs& a, size_t* bytes) {
+  using T = typename Dt::T;
+  const bool again = a.act != kActNone;
+  const hipStream_t st = static_cast<hipStream_t>(a.stream);
+  Arena arena{static_cast<char*>(a.workspace)};
+  const int64_t ld = round_up(a.d_out, 4), ld_dx = round_up(a.d_in, 4), shares = few_shares(a.d_in, a.d_out);
+  const FewPlan p = few_plan<T>(a.n, a.d_in, a.d_out);
+  float* d = arena.take<float>(a.n * ld);
+  float* sums = arena.take<float>(again ? shares * a.n * ld : 0);
+  float* dx = arena.take<float>(p.parts * a.n * ld_dx);
+  if (bytes) {
+    *bytes = arena.at;
+    return 0;
+  }
+  int rc = 0;
+  if (again) {
+    RowsArgs r{a.x, a.w, nullptr, nullptr, nullptr, nullptr, a.n, a.d_out, a.d_in, a.x_stride, 0, 0};
+    rc = few_sums<Dt>(r, sums, ld, st);
+    if (rc) return rc;
+  }
+  SlopeArgs s{};
+  s.from = again ? sums : nullptr, s.split_stride = a.n * ld, s.m = a.n, s.n = a.d_out, s.ld = ld;
+  s.splits = static_cast<int>(shares), s.act = a.act, s.bias = again ? a.bias : nullptr, s.gout = a.gout;
+  s.ld_gout = a.gout_stride, s.d = d, s.ld_d = ld, s.gbias = a.gbias;
+  rc = dense_slope<Dt, true>(s, st);
+  if (rc || (!a.gx && !a.gw)) return rc;
+  FewArgs f{a.x, a.w, d, a.gx ? dx : nullptr, a.gw, a.d_in, a.d_out, a.x_stride, ld, ld_dx, static_cast<int>(a.n),
+            static_cast<int>(p.rows), p.lanes};
+  rc = dense_few_bwd<T>(f, p, st);
+  if (rc || !a.gx) return rc;
+  return dense_fold<T>(dx, p.parts, a.n, ld_dx, a.d_in, a.gx, st);
 }
 
 template <typename Dt>
 int dense_bwd(const DenseArgs& a, size_t* bytes) {
   using T = typename Dt::T;
+  if (a.n <= kFewRowsBwd) return dense_bwd_few<Dt>(a, bytes);
   const bool worst = bytes != nullptr, product_again = a.act != kActNone;
   const hipStream_t st = static_cast<hipStream_t>(a.stream);
   MatrixPlan<Dt> plan(a.workspace);
@@ -169,37 +236,57 @@ int dense_bwd(const DenseArgs& a, size_t* bytes) {
   again.act = a.act, again.bias = a.bias, again.res = a.gout, again.ld_res = a.gout_stride;
   again.dg = const_cast<uint16_t*>(d.plane[0]), again.ldh = d.ld, again.plane_stride = a.n * d.ld;
   again.e_dg = d.exponents, again.e_ld = d.exponents_ld;
+  Split shared = product_again ? plan_split<Dt>(again) : Split{};
+  const bool few = product_again && a.n <= kFewRows;
+  const int64_t ld_shared = round_up(a.d_out, 4);
+  if (few) shared.splits = static_cast<int>(few_shares(a.d_in, a.d_out)), shared.elements = a.n * ld_shared;
   GemmArgs dx = product<Dt>(a.n, a.d_in, a.d_out, d, w, a.gx, a.d_in);
   GemmArgs dw = product<Dt>(a.d_out, a.d_in, a.n, d, x, a.gw, a.d_in);
   SplitSpace<Dt> space;  // sized for every gradient, asked for or not
+  space.add(product_again ? shared.splits * shared.elements : 0);
   space.add(space.of(dx) + space.of(dw));
   space.add(space.of(plan_split_wide<Dt>(dx)));
   space.add(space.of(plan_split_wide<Dt>(dw)));
   float* sums = plan.arena.template take<float>(space.most);
-  float* columns = plan.arena.template take<float>((product_again ? (a.n + 63) / 64 * 2 + 2 : segments(a.n)) * a.d_out);
+  const int64_t ld_columns = round_up(a.d_out, 4);
+  float* columns =
+      plan.arena.template take<float>((product_again ? (a.n + 63) / 64 * 2 + 2 : segments(a.n)) * ld_columns);
   if (worst) {
     *bytes = plan.arena.at;
     return 0;
   }
   int rc = plan.run_pack(st);
+  if (rc) return rc;
   int64_t column_rows = 0;
-  if (!rc && product_again) {
+  if (few || shared.splits > 1) {
+    if (few) {
+      const RowsArgs r{a.x, a.w, nullptr, nullptr, nullptr, nullptr, a.n, a.d_out, a.d_in, a.x_stride, 0, 0};
+      rc = few_sums<Dt>(r, sums, ld_shared, st);
+    } else {
+      SplitSumArgs q{};
+      split_into(again, shared, sums, q);
+      rc = gemm_launch_tile<Dt, 64, 64, 2, 2, kSmallK<Dt>, kSmallS<Dt>, false, false, kEpiStoreF32>(again, st);
+    }
+    if (rc) return rc;
+    SlopeArgs s{};
+    s.from = sums, s.split_stride = shared.elements, s.m = a.n, s.n = a.d_out, s.ld = ld_shared, s.splits = shared.splits;
+    s.act = a.act, s.bias = a.bias, s.gout = a.gout, s.ld_gout = a.gout_stride, s.d = again.dg, s.ld_d = d.ld;
+    s.exponents = d.exponents, s.e_ld = d.exponents_ld, s.column_sums = a.gbias ? columns : nullptr;
+    rc = dense_slope<Dt, kStaged<Dt>>(s, st);
+    column_rows = (a.n + 63) / 64;
+  } else if (product_again) {
     again.column_sums = a.gbias ? columns : nullptr;
     rc = gemm_launch<Dt, false, false, kEpiDenseBwd>(again, st);
     column_rows = again.column_rows;
-  } else if (!rc && a.gbias) {
+  } else if (a.gbias) {
     column_rows = segments(a.n);
     constexpr int kWide = 32 * Chunk<T>::kN;
     hipLaunchKernelGGL(dense_columns_kernel<T>,
                        dim3(static_cast<unsigned>((a.d_out + kWide - 1) / kWide), static_cast<unsigned>(column_rows)),
-                       dim3(256), 0, st, a.gout, a.n, a.gout_stride, a.d_out, segment_rows(a.n), columns);
+                       dim3(256), 0, st, a.gout, a.n, a.gout_stride, a.d_out, segment_rows(a.n), columns, ld_columns);
     rc = static_cast<int>(hipGetLastError());
   }
-  if (!rc && a.gbias) {
-    hipLaunchKernelGGL(dense_fold_kernel<T>, dim3(static_cast<unsigned>((a.d_out + 31) / 32)), dim3(1024), 0, st, columns,
-                       column_rows, a.d_out, static_cast<T*>(a.gbias));
-    rc = static_cast<int>(hipGetLastError());
-  }
+  if (!rc && a.gbias) rc = dense_fold<T>(columns, column_rows, 1, ld_columns, a.d_out, a.gbias, st);
   if (rc) return rc;
   const int64_t tiles = round_up(a.d_in, 64) / 64 * (round_up(a.d_out, 64) / 64 + round_up(a.n, 64) / 64);
   if (a.gx && a.gw && tiles <= 2 * 768) return gemm_launch_two_split<Dt>(dx, dw, sums, st);

@@ -47,9 +47,11 @@ struct RowsArgs {
   int act;
   const void *bias, *res;  // of a dense product: [n], [m][ld_res], either null
   int64_t ld_res;
+  int64_t k_share;  // of sums: workgroups (x, y) take the y-th k_share of k; out float32, shares share_stride apart
+  int64_t share_stride;
 };
 
-enum { kRowsPlain = 0, kRowsPaired = 1, kRowsDense = 2 };
+enum { kRowsPlain = 0, kRowsPaired = 1, kRowsDense = 2, kRowsSums = 3 };
 
 // eight k of a row from column c on, as the planes of a matrix operand
 template <typename Dt>
@@ -94,7 +96,11 @@ gemm_rows_kernel(RowsArgs g) {
   constexpr int P = Dt::kPlanes, W = Pair ? 2 : 1;
   __shared__ v4f sums[rows_waves<Dt>(M16)][W][64];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, waves = blockDim.x / 64;
-  const int k = static_cast<int>(g.k);
+  int k = static_cast<int>(g.k), k_first = 0;
+  if constexpr (Form == kRowsSums) {
+    k_first = static_cast<int>(blockIdx.y * g.k_share);
+    k = k_first + g.k_share < g.k ? k_first + static_cast<int>(g.k_share) : static_cast<int>(g.k);
+  }
   const int64_t o = static_cast<int64_t>(blockIdx.x) * 16 + lane % 16, last = g.n - 1;
   const T* w[W];  // rows past the last repeat it, and are not stored
   w[0] = static_cast<const T*>(g.w) + (o < last ? o : last) * g.k;
@@ -118,7 +124,7 @@ gemm_rows_kernel(RowsArgs g) {
   // float16: where any exponent is not zero the sum is made a second time, with
   // them.  Row i's is then in units of the present ones (lane % 16 has it), as in
   // gemm_tile, and the two sixteens of a step are added apart.
-  constexpr bool kUnits = Dt::kScaled && !Pair;
+  constexpr bool kUnits = Dt::kScaled && Form == kRowsPlain;
   int unit[M16], top[M16];
   const int groups = (k + 15) / 16;
   u32x4 odd = {0, 0, 0, 0};
@@ -151,7 +157,7 @@ gemm_rows_kernel(RowsArgs g) {
   auto run = [&](auto units) {
     constexpr int kUnroll = units ? 1 : P == 1 && M16 == 1 ? 4 : 2;
 #pragma unroll(kUnroll)
-    for (int k0 = wave * 64; k0 < k; k0 += waves * 64) {
+    for (int k0 = k_first + wave * 64; k0 < k; k0 += waves * 64) {
       RowChunk<Dt> rw[2][W], rx[2][M16];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -247,7 +253,10 @@ gemm_rows_kernel(RowsArgs g) {
           with_act(g.act, [&](auto act) { v[0] = dense_act(act, v[0] + bias); });
           if (g.res) v[0] += static_cast<float>(static_cast<const T*>(g.res)[m * g.ld_res + n]);
         }
-        static_cast<T*>(g.out)[m * g.ldo + n] = static_cast<T>(v[0]);
+        if constexpr (Form == kRowsSums)
+          static_cast<float*>(g.out)[blockIdx.y * g.share_stride + m * g.ldo + n] = v[0];
+        else
+          static_cast<T*>(g.out)[m * g.ldo + n] = static_cast<T>(v[0]);
       }
     }
   }
@@ -261,9 +270,10 @@ gemm_rows_kernel(RowsArgs g) {
 
 template <typename Dt, int M16, int Form>
 int gemm_rows_launch(const RowsArgs& g, hipStream_t st) {
-  const int64_t waves = std::min<int64_t>(rows_waves<Dt>(M16), std::max<int64_t>(4, (g.k + 63) / 64));
-  hipLaunchKernelGGL((gemm_rows_kernel<Dt, M16, Form>), dim3(static_cast<unsigned>((g.n + 15) / 16)),
-                     dim3(static_cast<unsigned>(waves * 64)), 0, st, g);
+  const int64_t k = Form == kRowsSums ? g.k_share : g.k;
+  const int64_t waves = std::min<int64_t>(rows_waves<Dt>(M16), std::max<int64_t>(4, (k + 63) / 64));
+  const dim3 grid(static_cast<unsigned>((g.n + 15) / 16), static_cast<unsigned>((g.k + k - 1) / k));
+  hipLaunchKernelGGL((gemm_rows_kernel<Dt, M16, Form>), grid, dim3(static_cast<unsigned>(waves * 64)), 0, st, g);
   return static_cast<int>(hipGetLastError());
 }
 

@@ -63,7 +63,8 @@ struct GemmArgs {
   // epilogue of the dense operator, all of the io type: [n], [m][ld_res], either
   // null.  Forward: c = act(product + bias) + res.  Backward: res is the gradient
   // of the output; dg (of float32 operands [m][ldh] float32) and e_dg as above, and
-  // the sums of dg's columns over each wave's rows, [column_rows][n], or null.
+  // the sums of dg's columns over each wave's rows, [column_rows][n up to a multiple
+  // of four], or null.
   const void *bias, *res;
   int64_t ld_res, column_rows;  // tiles_m times the tile's waves along m, at most 2 ceil(m / 64) + 2
   float* column_sums;
@@ -481,7 +482,7 @@ __device__ __forceinline__ void finish_tile(const GemmArgs& g, int z, int64_t m0
     store_rows(static_cast<T*>(g.c[z]) + (Epi == kEpiStoreF32 ? g.split_stride * share : 0), g.ldc[z]);
   } else {
     if (g.column_sums) {
-      float* sums = g.column_sums + (m0 / BM * WM + wm) * gn;
+      float* sums = g.column_sums + (m0 / BM * WM + wm) * ((gn + 3) / 4 * 4);
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
