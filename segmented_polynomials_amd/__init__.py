@@ -1263,6 +1263,11 @@ def gated_ffn_bwd(x, w_gate, w_up, w_down, grad_out, act="silu", need_dx=True, n
     return gx, gwg, gwu, gwd
 
 
+def _scratch(workspace, nbytes, device):
+    """As _channel_workspace; nothing is made where none is needed."""
+    return (None, 0) if nbytes == 0 and workspace is None else _channel_workspace(workspace, nbytes, device)
+
+
 # The library launches on the current device: that of the tensors is made
 # current for the call where it is another.
 def _call(index, fn, *args):
@@ -1309,7 +1314,7 @@ def dense_fwd(x, w, bias=None, act="none", residual=None, out=None, workspace=No
     dt, a, n, d_in, d_out, stride = _dense_common(x, w, bias, act)
     rs = 0 if residual is None else _rows("residual", residual, x, n, d_out)
     out, os_ = _out_rows("out", out, x, n, d_out)
-    workspace, nbytes = _channel_workspace(workspace, dense_workspace(dt, a, n, d_in, d_out), x.device)
+    workspace, nbytes = _scratch(workspace, dense_workspace(dt, a, n, d_in, d_out), x.device)
     _call(x.get_device(), lib.dense_fwd, dt, a, _adr(x), stride, _adr(w), _adr(bias), _adr(residual), rs, n, d_in, d_out,
           _adr(out), os_, _adr(workspace), nbytes)
     return out
@@ -1326,7 +1331,7 @@ def dense_bwd(x, w, grad_out, bias=None, act="none", need_dx=True, need_dw=True,
     gx = x.new_empty((n, d_in)) if need_dx else None
     gw = w.new_empty((d_out, d_in)) if need_dw else None
     gb = bias.new_empty(d_out) if need_dw and bias is not None else None
-    workspace, nbytes = _channel_workspace(workspace, dense_workspace(dt, a, n, d_in, d_out, True), x.device)
+    workspace, nbytes = _scratch(workspace, dense_workspace(dt, a, n, d_in, d_out, True), x.device)
     _call(x.get_device(), lib.dense_bwd, dt, a, _adr(x), stride, _adr(w), _adr(bias), _adr(grad_out), gs, n, d_in, d_out,
           _adr(gx), _adr(gw), _adr(gb), _adr(workspace), nbytes)
     return gx, gw, gb
@@ -1403,15 +1408,13 @@ def expert_sort(experts, num_experts, workspace=None):
         raise ValueError("experts must be a contiguous [n, k] tensor on a GPU")
     entries = experts.numel()
     nbytes = expert_sort_workspace(entries, num_experts)
-    dev, i32 = experts.device, torch.int32
-    order = torch.empty(entries, dtype=i32, device=dev)
-    place = torch.empty(experts.shape, dtype=i32, device=dev)
-    offsets = torch.empty(num_experts + 1, dtype=i32, device=dev)
-    ids = torch.empty(entries, dtype=i32, device=dev)
-    workspace, nbytes = _channel_workspace(workspace, nbytes, dev)
+    dev = experts.device
+    order, place, ids = torch.empty((3, *experts.shape), dtype=torch.int32, device=dev).unbind(0)
+    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
+    workspace, nbytes = _scratch(workspace, nbytes, dev)
     _call(experts.get_device(), lib.expert_sort, _adr(experts), idx, entries, num_experts, _adr(order), _adr(place),
           _adr(offsets), _adr(ids), _adr(workspace), nbytes)
-    return order, place, offsets, ids
+    return order.view(-1), place, offsets, ids.view(-1)
 
 
 def _expert_rows(like, place, offsets):

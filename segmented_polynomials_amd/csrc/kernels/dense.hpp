@@ -17,6 +17,7 @@
 
 #include "column_sums.hpp"
 #include "dense_few.hpp"
+#include "dense_fused.hpp"
 #include "dense_stream.hpp"
 #include "gemm_plan.hpp"
 #include "gemm_rows.hpp"
@@ -111,18 +112,34 @@ dense_columns_kernel(const void* __restrict__ src, int64_t n, int64_t stride, in
     sums[blockIdx.y * ld_sums + col] = t;
   }
 }
-// to[m][c] = sum over p of sums[p][m][c], `ld` between rows
+// to[m][c] = sum over p of sums[p][m][c]; `ld` between rows, a multiple of four from the
+// width on.  Row `rows` is the bias's, of partial rows of its own.
+struct FoldArgs {
+  const float *sums, *bias_sums;
+  int64_t parts, rows, width, bias_parts, bias_width;
+  void *to, *to_bias;
+};
 template <typename T>
 __global__ void __launch_bounds__(1024)
-dense_fold_kernel(const float* __restrict__ sums, int64_t parts, int64_t ld, int64_t width, T* to) {
+dense_fold_kernel(FoldArgs g) {
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32, m = blockIdx.y;
-  const float t = column_sum(sums + m * ld, parts, gridDim.y * ld, width, c);
-  if (threadIdx.x < 32 && c < width) to[m * width + c] = static_cast<T>(t);
+  const bool bias = m == g.rows;
+  const int64_t width = bias ? g.bias_width : g.width, ld = (width + 3) / 4 * 4;
+  if (static_cast<int64_t>(blockIdx.x) * 32 >= width) return;
+  const float t = bias ? column_sum(g.bias_sums, g.bias_parts, ld, width, c)
+                       : column_sum(g.sums + m * ld, g.parts, g.rows * ld, width, c);
+  T* to = static_cast<T*>(bias ? g.to_bias : g.to) + (bias ? 0 : m * width);
+  if (threadIdx.x < 32 && c < width) to[c] = static_cast<T>(t);
 }
+// what of the two is asked for, and not null
 template <typename T>
-int dense_fold(const float* sums, int64_t parts, int64_t rows, int64_t ld, int64_t width, void* to, hipStream_t st) {
-  hipLaunchKernelGGL(dense_fold_kernel<T>, dim3(static_cast<unsigned>((width + 31) / 32), static_cast<unsigned>(rows)),
-                     dim3(1024), 0, st, sums, parts, ld, width, static_cast<T*>(to));
+int dense_fold(FoldArgs g, hipStream_t st) {
+  if (!g.to) g.rows = g.width = 0;
+  if (!g.to_bias) g.bias_width = 0;
+  const int64_t wide = std::max(g.width, g.bias_width), rows = g.rows + (g.bias_width ? 1 : 0);
+  if (wide == 0 || rows == 0) return 0;
+  hipLaunchKernelGGL(dense_fold_kernel<T>, dim3(static_cast<unsigned>((wide + 31) / 32), static_cast<unsigned>(rows)),
+                     dim3(1024), 0, st, g);
   return static_cast<int>(hipGetLastError());
 }
 
@@ -219,12 +236,32 @@ int dense_bwd_few(const DenseArgs& a, size_t* bytes) {
             static_cast<int>(p.rows), p.lanes};
   rc = dense_few_bwd<T>(f, p, st);
   if (rc || !a.gx) return rc;
-  return dense_fold<T>(dx, p.parts, a.n, ld_dx, a.d_in, a.gx, st);
+  return dense_fold<T>({dx, nullptr, p.parts, a.n, a.d_in, 0, 0, a.gx, nullptr}, st);
+}
+
+// Up to 64 by 64 columns: one pass over the rows, then its workgroups' sums.
+template <typename Dt>
+int dense_bwd_fused(const DenseArgs& a, size_t* bytes) {
+  using T = typename Dt::T;
+  const hipStream_t st = static_cast<hipStream_t>(a.stream);
+  Arena arena{static_cast<char*>(a.workspace)};
+  const int64_t blocks = fused_blocks<T>(a.n), ld = round_up(a.d_in, 4), ld_bias = round_up(a.d_out, 4);
+  float* dw = arena.take<float>(blocks * a.d_out * ld);
+  float* dbias = arena.take<float>(blocks * ld_bias);
+  if (bytes) {
+    *bytes = arena.at;
+    return 0;
+  }
+  int rc = dense_fused_bwd<Dt>({a.x, a.w, a.act == kActNone ? nullptr : a.bias, a.gout, a.gx, a.gw ? dw : nullptr,
+                                a.gbias ? dbias : nullptr, a.n, a.x_stride, a.gout_stride, static_cast<int>(a.d_in),
+                                static_cast<int>(a.d_out), a.act}, st);
+  return rc ? rc : dense_fold<T>({dw, dbias, blocks, a.d_out, a.d_in, blocks, a.d_out, a.gw, a.gbias}, st);
 }
 
 template <typename Dt>
 int dense_bwd(const DenseArgs& a, size_t* bytes) {
   using T = typename Dt::T;
+  if (takes_fused_bwd<T>(a.n, a.d_in, a.d_out)) return dense_bwd_fused<Dt>(a, bytes);
   if (a.n <= kFewRowsBwd) return dense_bwd_few<Dt>(a, bytes);
   const bool worst = bytes != nullptr, product_again = a.act != kActNone;
   const hipStream_t st = static_cast<hipStream_t>(a.stream);
@@ -286,12 +323,20 @@ int dense_bwd(const DenseArgs& a, size_t* bytes) {
                        dim3(256), 0, st, a.gout, a.n, a.gout_stride, a.d_out, segment_rows(a.n), columns, ld_columns);
     rc = static_cast<int>(hipGetLastError());
   }
-  if (!rc && a.gbias) rc = dense_fold<T>(columns, column_rows, 1, ld_columns, a.d_out, a.gbias, st);
+  // the bias's sums: few partial rows join the last launch that adds shares, which reads them one after another
+  SplitSumArgs last{};
+  if (a.gbias && column_rows <= 16 && (a.gx || a.gw)) {
+    last.batch = 1, last.from[0] = columns, last.to[0] = a.gbias, last.m[0] = 1, last.n[0] = a.d_out;
+    last.ld[0] = ld_columns, last.ldc[0] = a.d_out, last.split_stride[0] = ld_columns;
+    last.splits[0] = static_cast<int>(column_rows);
+  } else if (!rc) {
+    rc = dense_fold<T>({nullptr, columns, 0, 0, 0, column_rows, a.d_out, nullptr, a.gbias}, st);
+  }
   if (rc) return rc;
   const int64_t tiles = round_up(a.d_in, 64) / 64 * (round_up(a.d_out, 64) / 64 + round_up(a.n, 64) / 64);
-  if (a.gx && a.gw && tiles <= 2 * 768) return gemm_launch_two_split<Dt>(dx, dw, sums, st);
-  if (a.gx) rc = gemm_launch_split<Dt, false, true, kEpiStore, true>(dx, sums, st);
-  if (!rc && a.gw) rc = gemm_launch_split<Dt, true, true, kEpiStore, true>(dw, sums, st);
+  if (a.gx && a.gw && tiles <= 2 * 768) return gemm_launch_two_split<Dt>(dx, dw, sums, st, last);
+  if (a.gx) rc = gemm_launch_split<Dt, false, true, kEpiStore, true>(dx, sums, st, a.gw ? SplitSumArgs{} : last);
+  if (!rc && a.gw) rc = gemm_launch_split<Dt, true, true, kEpiStore, true>(dw, sums, st, last);
   return rc;
 }
 

@@ -56,18 +56,19 @@ dense_stream_kernel(StreamArgs g) {
   constexpr int kFill = 4;  // in flight together
   for (int u0 = wave * kFill; u0 < units; u0 += waves * kFill) {
     RowChunk<Dt> c[kFill];
-    int at[kFill];
+    int limit[kFill];
 #pragma unroll
     for (int i = 0; i < kFill; ++i) {
       const int u = u0 + i, n = pair0 * 32 + stream_column(u / KC, lane % 16);
-      at[i] = u < units && n < g.cols ? u % KC * 32 + lane / 16 * 8 : g.k;
-      c[i].load(static_cast<const T*>(g.w) + static_cast<int64_t>(at[i] < g.k ? n : 0) * g.k, at[i], g.k);
+      limit[i] = u < units && n < g.cols ? g.k : 0;
+      load_eight<Dt, false>(c[i], static_cast<const T*>(g.w) + static_cast<int64_t>(limit[i] ? n : 0) * g.k,
+                            u % KC * 32 + lane / 16 * 8, g.k, limit[i]);
     }
 #pragma unroll
     for (int i = 0; i < kFill; ++i) {
       if (u0 + i >= units) continue;
       u16x8 p[P];
-      chunk_planes<Dt, false>(c[i], at[i], g.k, p);
+      chunk_planes<Dt, false>(c[i], (u0 + i) % KC * 32 + lane / 16 * 8, g.k, limit[i], p);
 #pragma unroll
       for (int q = 0; q < P; ++q) weight[((u0 + i) * P + q) * 64 + lane] = p[q];
     }
@@ -84,7 +85,7 @@ dense_stream_kernel(StreamArgs g) {
       m = m < g.n ? m : g.n - 1;
 #pragma unroll
       for (int c = 0; c < KC; ++c)
-        load_eight<Dt, Whole>(raw[r][c], static_cast<const T*>(g.x) + m * g.ldx, c * 32 + lane / 16 * 8, g.k);
+        load_eight<Dt, Whole>(raw[r][c], static_cast<const T*>(g.x) + m * g.ldx, c * 32 + lane / 16 * 8, g.k, g.k);
     }
   };
   int64_t t = static_cast<int64_t>(wave) * gridDim.x + blockIdx.x;
@@ -94,7 +95,7 @@ dense_stream_kernel(StreamArgs g) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int c = 0; c < KC; ++c) chunk_planes<Dt, Whole>(raw[r][c], c * 32 + lane / 16 * 8, g.k, x[r][c]);
+      for (int c = 0; c < KC; ++c) chunk_planes<Dt, Whole>(raw[r][c], c * 32 + lane / 16 * 8, g.k, g.k, x[r][c]);
     if (!Res && t + step < tiles) fetch(t + step);
     for (int pair = 0; pair < pairs; ++pair) {
       const int n = (pair0 + pair) * 32 + lane / 16 * 8;

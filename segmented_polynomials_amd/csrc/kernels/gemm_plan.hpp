@@ -147,7 +147,7 @@ Split plan_split_wide(const GemmArgs& g) {
   if (g.batch != 1 || g.phases != 1 || g.m[0] <= 64 || g.n[0] <= 64) return p;
   const int64_t tiles = (g.m[0] + 127) / 128 * ((g.n[0] + 127) / 128), steps = (g.k + kStep - 1) / kStep;
   const int64_t splits = std::min(kHeld / tiles, steps / 16);
-  if (splits < 2 || tiles * splits * 4 < kHeld * 3) return p;
+  if (splits < 2 || tiles * 4 > kHeld || tiles * splits * 4 < kHeld * 3) return p;
   p.splits = static_cast<int>(splits);
   p.elements = g.m[0] * round_up(g.n[0], 4);
   return p;
@@ -189,11 +189,10 @@ template <typename Dt>
 constexpr int kSmallS = Dt::kPlanes == 1 ? 3 : 2;
 
 // A product with a plain epilogue, split if that pays; `sums` is the space that
-// SplitSpace found for it.
+// SplitSpace found for it.  q: sums of others to be added up with its shares.
 template <typename Dt, bool AAcross, bool BAcross, int Epi, bool Wide = false>
-int gemm_launch_split(GemmArgs& g, float* sums, hipStream_t st) {
+int gemm_launch_split(GemmArgs& g, float* sums, hipStream_t st, SplitSumArgs q = {}) {
   using T = std::conditional_t<Epi == kEpiStoreF32, float, typename Dt::T>;
-  SplitSumArgs q{};
   int rc;
   const Split wide = Wide ? plan_split_wide<Dt>(g) : Split{};
   if (wide.splits > 1) {
@@ -206,9 +205,12 @@ int gemm_launch_split(GemmArgs& g, float* sums, hipStream_t st) {
     }
   } else {
     const Split p = plan_split<Dt>(g);
-    if (p.splits == 1) return gemm_launch<Dt, AAcross, BAcross, Epi>(g, st);
-    split_into(g, p, sums, q);
-    rc = gemm_launch_tile<Dt, 64, 64, 2, 2, kSmallK<Dt>, kSmallS<Dt>, AAcross, BAcross, kEpiStoreF32>(g, st);
+    if (p.splits == 1) {
+      rc = gemm_launch<Dt, AAcross, BAcross, Epi>(g, st);
+    } else {
+      split_into(g, p, sums, q);
+      rc = gemm_launch_tile<Dt, 64, 64, 2, 2, kSmallK<Dt>, kSmallS<Dt>, AAcross, BAcross, kEpiStoreF32>(g, st);
+    }
   }
   return rc ? rc : split_sum_launch<T>(q, st);
 }
@@ -241,9 +243,8 @@ int gemm_launch_two(GemmArgs& x, GemmArgs& w, hipStream_t st) {
 
 // The two together, each split if that pays.
 template <typename Dt>
-int gemm_launch_two_split(GemmArgs& x, GemmArgs& w, float* sums, hipStream_t st) {
+int gemm_launch_two_split(GemmArgs& x, GemmArgs& w, float* sums, hipStream_t st, SplitSumArgs q = {}) {
   const Split px = plan_split<Dt>(x), pw = plan_split<Dt>(w);
-  SplitSumArgs q{};
   int64_t at = 0;
   if (px.splits > 1) at += split_into(x, px, sums, q);
   if (pw.splits > 1) split_into(w, pw, sums + at, q);

@@ -47,37 +47,57 @@ __device__ __forceinline__ void split_eight(const float (&v)[8], u16x8 (&p)[3]) 
   if (__ballot(split_fast(v, p))) split_slow(v, p);
 }
 
-// Eight elements of a row from column `at` on, zeros past its width.  Whole: of
-// rows whose width is a multiple of four, no 16 bytes cross the end.
+// Eight elements of a row from column `at` on, those from `limit` on zeros: the width,
+// or 0 for a row that does not count, whose address is another's.  Whole: of rows whose
+// width is a multiple of 16 bytes, no load crosses the end.  Else one that would is from
+// further left, and a wave with any moves its elements after they have landed
+// (settle_eight): without branches around the loads odd widths cost what even ones do.
 template <typename Dt, bool Whole>
-__device__ __forceinline__ void load_eight(RowChunk<Dt>& c, const typename Dt::T* row, int at, int width) {
+__device__ __forceinline__ void load_eight(RowChunk<Dt>& c, const typename Dt::T* row, int at, int width, int limit) {
   constexpr int N = Chunk<typename Dt::T>::kN;
-  if constexpr (Whole) {
 #pragma unroll
-    for (int i = 0; i < RowChunk<Dt>::kLoads; ++i) {
+  for (int i = 0; i < RowChunk<Dt>::kLoads; ++i) {
+    const int col = at + i * N;
+    if constexpr (Whole) {
       c.raw[i] = u32x4{0, 0, 0, 0};
-      if (at + i * N < width) __builtin_memcpy(&c.raw[i], row + at + i * N, 16);
+      if (col < limit) __builtin_memcpy(&c.raw[i], row + col, 16);
+    } else if (width >= N) {
+      __builtin_memcpy(&c.raw[i], row + (col + N <= width ? col : width - N), 16);
+    } else {
+      c.raw[i] = load_raw(row, limit ? col : width, width);
     }
-  } else {
-    c.load(row, at, width);
   }
+}
+template <typename Dt>
+__device__ __forceinline__ void settle_eight(RowChunk<Dt>& c, int at, int width, int limit) {
+  using T = typename Dt::T;
+  constexpr int N = Chunk<T>::kN;
+  if (width < N || !__ballot(at + 8 > limit)) return;
+#pragma unroll
+  for (int i = 0; i < RowChunk<Dt>::kLoads; ++i) {
+    const int col = at + i * N;
+    c.raw[i] = settle_chunk<T>(c.raw[i], col, width);
+    if (col >= limit) c.raw[i] = u32x4{0, 0, 0, 0};
+  }
+}
+// the eight values
+template <typename Dt, bool Whole>
+__device__ __forceinline__ void eight_values(RowChunk<Dt> c, int at, int width, int limit, float (&v)[8]) {
+  if constexpr (!Whole) settle_eight<Dt>(c, at, width, limit);
+  typename Dt::T t[8];
+  __builtin_memcpy(t, c.raw, sizeof(t));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(t[i]);
 }
 // and as matrix operands
 template <typename Dt, bool Whole>
-__device__ __forceinline__ void chunk_planes(const RowChunk<Dt>& c, int at, int width, u16x8 (&p)[Dt::kPlanes]) {
+__device__ __forceinline__ void chunk_planes(RowChunk<Dt> c, int at, int width, int limit, u16x8 (&p)[Dt::kPlanes]) {
   if constexpr (Dt::kPlanes == 1) {
-    if constexpr (Whole)
-      p[0] = __builtin_bit_cast(u16x8, c.raw[0]);
-    else
-      c.planes(at, width, p);
+    if constexpr (!Whole) settle_eight<Dt>(c, at, width, limit);
+    p[0] = __builtin_bit_cast(u16x8, c.raw[0]);
   } else {
     float v[8];
-    if constexpr (Whole) {
-      __builtin_memcpy(v, c.raw, sizeof(v));
-    } else {
-      unpack_chunk<float>(c.raw[0], at, width, v);
-      unpack_chunk<float>(c.raw[1], at + 4, width, v + 4);
-    }
+    eight_values<Dt, Whole>(c, at, width, limit, v);
     split_eight(v, p);
   }
 }
@@ -129,7 +149,7 @@ struct StagedOperand {
       }
     } else {
       load_eight<DtF32, Whole>(c, Across ? base + (step * kStagedK + (columns(step) ? row : 0)) * ld : base, first(step),
-                               columns(step));
+                               width, columns(step));
     }
   }
   __device__ __forceinline__ void values(const RowChunk<DtF32>& c, int64_t step, float (&v)[8]) const {
@@ -138,11 +158,8 @@ struct StagedOperand {
       __builtin_memcpy(v, c.raw, sizeof(v));
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = (Across ? kk < k : first(step) + i / 4 * 4 < k) ? v[i] : 0.f;
-    } else if constexpr (Whole) {
-      __builtin_memcpy(v, c.raw, sizeof(v));
     } else {
-      unpack_chunk<float>(c.raw[0], first(step), columns(step), v);
-      unpack_chunk<float>(c.raw[1], first(step) + 4, columns(step), v + 4);
+      eight_values<DtF32, Whole>(c, first(step), width, columns(step), v);
     }
   }
   __device__ __forceinline__ void place(const u16x8 (&p)[3], uint16_t* lds) const {

@@ -170,14 +170,14 @@ def test_strides_and_parts(n, di, do, dtype, act):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("n", [5, 40, 700, 40000])
-def test_infinities_and_nan(n, dtype):
+@pytest.mark.parametrize("n,di,do", [(3, 72, 40), (5, 72, 40), (40, 72, 40), (700, 72, 40), (40000, 72, 40),
+                                     (700, 64, 40), (40000, 50, 33), (900, 300, 200)])
+def test_infinities_and_nan(n, di, do, dtype):
     """They come through as the formula has them, and stay in their row,
     column or sum."""
     need_gpu()
     import segmented_polynomials_amd as sp
-    di, do = 72, 40
-    announce(f"dense: infinities and NaN n={n} {dtype}")
+    announce(f"dense: infinities and NaN n={n} {di} {do} {dtype}")
     x, w, b, res, g = case(n, di, do, dtype, 3)
     clean, cgx = sp.dense_fwd(x, w, bias=b), sp.dense_bwd(x, w, g, bias=b)
     for bad in (float("inf"), float("nan")):
@@ -208,7 +208,7 @@ def test_infinities_and_nan(n, dtype):
 
 @pytest.mark.parametrize("scale", [2.0 ** -22, 2.0 ** -14, 2.0 ** 8])
 @pytest.mark.parametrize("act", ["gelu", "sigmoid"])
-@pytest.mark.parametrize("n,di,do", [(40, 72, 136), (3000, 130, 300)])
+@pytest.mark.parametrize("n,di,do", [(40, 72, 136), (3000, 130, 300), (3, 72, 136), (20000, 60, 64), (70, 9000, 64)])
 def test_float16_range(n, di, do, act, scale):
     """Gradients at the ends of float16's range: the gradient before the
     activation, which may be past them, keeps its 11 bits."""
@@ -238,7 +238,8 @@ def test_float32_accuracy():
     6 2^-24 for activation, products and roundings."""
     need_gpu()
     import segmented_polynomials_amd as sp
-    for n, di, do in ((5, 333, 1001), (33, 2048, 96), (300, 512, 512), (60000, 64, 64), (700, 96, 1500)):
+    for n, di, do in ((3, 333, 1001), (5, 333, 1001), (33, 2048, 96), (300, 512, 512), (60000, 64, 64), (700, 96, 1500),
+                      (4000, 300, 300)):
         announce(f"dense: float32 accuracy {n} {di} {do}")
         x, w, b, res, g = case(n, di, do, "f32", 7)
         (out, _), grads = reference(x, w, b, None, g, "silu", "f32")
