@@ -278,11 +278,17 @@ int gemm_launch(GemmArgs& g, hipStream_t st) {
     return (each > 1 && rounds > 1 ? 0.5 * (rounds + whole) : whole) * static_cast<double>(bm * bn * each) / rate;
   };
   if constexpr (Dt::kPlanes == 1) {
-    constexpr bool kTwoAcross = AAcross && BAcross, kBwd = Epi == kEpiGatedBwd || Epi == kEpiDenseBwd || Epi == kEpiDense;
+    constexpr bool kTwoAcross = AAcross && BAcross, kBwd = Epi == kEpiGatedBwd;
+    // the dense epilogues' activations and slopes take a tile as long as a few hundred k: beside a second workgroup's
+    // products (8192 x 2048 x 5632 bf16, gradient with gelu: 586 us, 618 in 256 x 128 tiles; 20000 x 512 x 512 forward
+    // 28, 34)
+    constexpr bool kDense = Epi == kEpiDense || Epi == kEpiDenseBwd;
     const double large = kTwoAcross || kBwd ? cost(256, 128, kBwd ? 1 : 2, 1.0) : cost(256, 256, 1, 1.0);
     const double c128 = cost(128, 128, 2, 0.8), c64 = cost(64, 64, 3, 0.45);
-    if (large <= c128 && large <= c64) {
-      if constexpr (kTwoAcross)
+    if (!kDense && large <= c128 && large <= c64) {
+      if constexpr (kDense)
+        return 0;  // not reached
+      else if constexpr (kTwoAcross)
         return gemm_launch_tile<Dt, 256, 128, 2, 2, 32, 3, AAcross, BAcross, Epi>(g, st);
       else if constexpr (kBwd)
         return gemm_launch_tile<Dt, 256, 128, 4, 2, 64, 3, AAcross, BAcross, Epi>(g, st);

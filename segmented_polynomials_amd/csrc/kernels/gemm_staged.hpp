@@ -281,7 +281,7 @@ __device__ __forceinline__ void gemm_staged(const GemmArgs& g, int64_t id, int s
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = add_small(acc[i][j], small[i][j]);
-  finish_tile<DtF32Staged, BM, BN, WM, WN, KS, Epi>(g, 0, m0, n0, share, acc, a0, b0, a1, b1);
+  finish_tile<DtF32Staged, BM, BN, WM, WN, KS, Epi>(g, 0, m0, n0, share, acc, a0, b0);
 }
 
 #define SEGPOLY_STAGED_LDS(BM, BN)                                        \

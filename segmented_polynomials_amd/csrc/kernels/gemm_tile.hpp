@@ -364,23 +364,16 @@ __device__ __forceinline__ void tile_corner(int64_t id, int64_t tiles_m, int64_t
 // s of row r holds chunk s ^ r, so that sixteen rows of a column fall into different
 // banks.  value(i, j, q): element q of the wave's fragment (i, j).
 template <int BM, int BN, int WM, int WN, typename V, typename F>
-__device__ __forceinline__ void store_lines(uint16_t* q0, uint16_t* q1, uint16_t* q2, uint16_t* q3, V* to, int64_t ld,
-                                            int64_t m0, int64_t n0, int64_t gm, int64_t width, F&& value) {
+__device__ __forceinline__ void store_lines(uint16_t* q0, uint16_t* q1, V* to, int64_t ld, int64_t m0, int64_t n0,
+                                            int64_t gm, int64_t width, F&& value) {
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16, kThreads = WM * WN * 64, kChunks = BN / 8;
-  static_assert(sizeof(V) == 2 && BM <= 256 && kThreads / kChunks <= 64, "a pass of the threads is within a buffer");
+  static_assert(sizeof(V) == 2 && BM <= 128 && kThreads / kChunks <= 64, "a pass of the threads is within a buffer");
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wm = wave / WN, wn = wave % WN;
-  auto buffer = [](int piece, uint16_t* p0, uint16_t* p1, uint16_t* p2, uint16_t* p3) __attribute__((always_inline)) {
-    uint16_t* p = p0;
-    if (BM > 64 && piece == 1) p = p1;
-    if (BM > 128 && piece == 2) p = p2;
-    if (BM > 128 && piece == 3) p = p3;
-    return p;
-  };
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int first = wm * (BM / WM) + i * 16, r = first % 64 + lane % 16;
-    uint16_t* at = buffer(first / 64, q0, q1, q2, q3) + r * BN;
+    uint16_t* at = (first < 64 ? q0 : q1) + r * BN;
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       const int c = wn * (BN / WN) + j * 16 + lane / 16 * 4;
@@ -392,7 +385,7 @@ __device__ __forceinline__ void store_lines(uint16_t* q0, uint16_t* q1, uint16_t
 #pragma unroll
   for (int t = 0; t < BM * kChunks / kThreads; ++t) {
     const int u = t * kThreads + static_cast<int>(threadIdx.x), r = u / kChunks, c = u % kChunks;
-    const uint16_t* from = buffer(t * kThreads / kChunks / 64, q0, q1, q2, q3) + r % 64 * BN + (c ^ r % kChunks) * 8;
+    const uint16_t* from = (t * kThreads / kChunks < 64 ? q0 : q1) + r % 64 * BN + (c ^ r % kChunks) * 8;
     const int64_t m = m0 + r, n = n0 + c * 8;
     if (m >= gm || n >= width) continue;
     const u16x8 v = *reinterpret_cast<const u16x8*>(from);
@@ -410,8 +403,7 @@ __device__ __forceinline__ void store_lines(uint16_t* q0, uint16_t* q1, uint16_t
 // The epilogue of a product with one output: a tile's sums, batch z, corner (m0, n0).
 template <typename Dt, int BM, int BN, int WM, int WN, int KS, int Epi>
 __device__ __forceinline__ void finish_tile(const GemmArgs& g, int z, int64_t m0, int64_t n0, int share,
-                                            v4f (&acc)[BM / WM / 16][BN / WN / 16], uint16_t* a0, uint16_t* b0,
-                                            uint16_t* a1, uint16_t* b1) {
+                                            v4f (&acc)[BM / WM / 16][BN / WN / 16], uint16_t* a0, uint16_t* b0) {
   using E = typename Dt::E;
   constexpr bool kDense = Epi == kEpiDense || Epi == kEpiDenseBwd;
   constexpr int P = Dt::kPlanes, FM = BM / WM / 16, FN = BN / WN / 16;
@@ -429,11 +421,6 @@ __device__ __forceinline__ void finish_tile(const GemmArgs& g, int z, int64_t m0
     with_act(g.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        // all rows' loads and slopes at once do not fit in the registers
-        if (FM * FN >= 32) {
-          asm volatile("" ::: "memory");
-          __builtin_amdgcn_sched_barrier(0);
-        }
         const int64_t m = row0 + i * 16;
         const T* row = static_cast<const T*>(g.res) + (m < gm ? m : 0) * g.ld_res;
 #pragma unroll
@@ -476,7 +463,7 @@ __device__ __forceinline__ void finish_tile(const GemmArgs& g, int z, int64_t m0
   static_assert(!kDense || P > 1 || (64 * BN <= BM * KS && 64 * BN <= BN * KS), "64 rows fit in a buffer");
   if constexpr (Epi == kEpiDense && P == 1) {
     wait_and_meet<0>();  // every wave has read its last fragments
-    store_lines<BM, BN, WM, WN>(a0, b0, a1, b1, static_cast<T*>(g.c[z]), g.ldc[z], m0, n0, gm, gn,
+    store_lines<BM, BN, WM, WN>(a0, b0, static_cast<T*>(g.c[z]), g.ldc[z], m0, n0, gm, gn,
                                 [&](int i, int j, int q) { return static_cast<T>(acc[i][j][q]); });
   } else if constexpr (Epi != kEpiDenseBwd) {
     store_rows(static_cast<T*>(g.c[z]) + (Epi == kEpiStoreF32 ? g.split_stride * share : 0), g.ldc[z]);
@@ -530,7 +517,7 @@ __device__ __forceinline__ void finish_tile(const GemmArgs& g, int z, int64_t m0
         }
     }
     if constexpr (P == 1)  // rows of the products' operands are read in 16-byte chunks
-      store_lines<BM, BN, WM, WN>(a0, b0, a1, b1, reinterpret_cast<E*>(g.dg), g.ldh, m0, n0, gm, (gn + 7) / 8 * 8,
+      store_lines<BM, BN, WM, WN>(a0, b0, reinterpret_cast<E*>(g.dg), g.ldh, m0, n0, gm, (gn + 7) / 8 * 8,
                                   [&](int i, int j, int q) { return static_cast<E>(acc[i][j][q]); });
   }
 }
@@ -890,7 +877,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
             acc[i][j] *= power_of_two(unit_a[i / (FM / GA)]) * power_of_two(unit_b[j / (FN / GB)]);
       }
     }
-    finish_tile<Dt, BM, BN, WM, WN, KS, Epi>(g, z, m0, n0, share, acc, a0, b0, a1, b1);
+    finish_tile<Dt, BM, BN, WM, WN, KS, Epi>(g, z, m0, n0, share, acc, a0, b0);
   } else {
     // A fragment's lanes hold four columns of sixteen rows, 32 bytes of a line:
     // the results go through LDS, one 16-bit plane after another in two buffers,
