@@ -134,6 +134,11 @@ Split plan_split(const GemmArgs& g) {
   const int64_t steps = (g.k + kStep - 1) / kStep * g.phases;
   if (tiles > 0 && tiles < 384)
     p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(768 / tiles, steps / 16)));
+  // A step of staged operands takes a microsecond where a unit has one workgroup: shares of five steps until most
+  // units have one.  One MI355X, us with five and sixteen at least, float32: 40 x 700 x 700 forward 12, 25, gradient
+  // 27, 53; 700 x 1500 x 96 13, 29 and 31, 61; 1357 x 322 x 853 gradient 68, 75.
+  if (kStaged<Dt> && tiles > 0 && tiles * p.splits < 192)
+    p.splits = static_cast<int>(std::max<int64_t>(p.splits, std::min<int64_t>((256 + tiles - 1) / tiles, steps / 5)));
   return p;
 }
 
