@@ -81,7 +81,7 @@ int few_sums(RowsArgs r, float* sums, int64_t ld, hipStream_t st) {
 
 // Column sums of a segment of the rows: 32 chunks of 16 bytes by 8 rows at a
 // time, whose sums are added in order.
-constexpr int64_t kSegmentRows = 256;
+constexpr int64_t kSegmentRows = 64;  // 500 x 256 bf16 gradient without activation 11 us, 14 with 256; 20000 x 128 21, 24
 template <typename T>
 __global__ void __launch_bounds__(256)
 dense_columns_kernel(const void* __restrict__ src, int64_t n, int64_t stride, int64_t width, int64_t rows, float* sums,
@@ -143,18 +143,41 @@ int dense_fold(FoldArgs g, hipStream_t st) {
   return static_cast<int>(hipGetLastError());
 }
 
-// rows of a segment: as many segments as fill the card a few times, within the launch's limit
-inline int64_t segment_rows(int64_t n) { return std::max(kSegmentRows, round_up((n + 32767) / 32768, 8)); }
+// rows of a segment: at most 2048 segments, whose sums are added up again
+inline int64_t segment_rows(int64_t n) { return std::max(kSegmentRows, round_up((n + 2047) / 2048, 8)); }
 inline int64_t segments(int64_t n) { return (n + segment_rows(n) - 1) / segment_rows(n); }
 
 constexpr int64_t kFewRows = 16, kFewRowsBwd = 4;
+
+// The rows' form of the product against tiles (or the streaming form).  One MI355X, us, silu, rows' form first:
+//                 16 x 64 x 64    16 x 1024 x 1024   16 x 4096 x 4096   32 x 256 x 256   32 x 1024 x 4096   32 x 4096 x 4096
+//   forward bf16      3.1, 3.6          6.4, 8.1            11, 12          4.3, 4.4          6.7, 8.1            16, 13
+//           f32       4.6, 5.3          9.1, 13             23, 29          7.2, 12            14, 16             39, 28
+//   gradient's: 16 rows of 64 x 64 bf16 9.2, 8.1, f32 12, 10; of 256 x 256 10.5, 9.7 and 19, 22; of 1024 x 1024
+//   15, 16 and 23, 27; of 4096 x 4096 41, 39 and 83, 87 (its slope takes a launch more)
+inline bool takes_few_fwd(int64_t n, int64_t d_in, int64_t d_out) {
+  return n <= kFewRows || (n <= 2 * kFewRows && d_in > 128 && d_in <= 1024 && d_out <= 4096);
+}
+template <typename Dt>
+bool takes_few_bwd(int64_t n, int64_t d_in) { return n <= kFewRows && d_in >= (kStaged<Dt> ? 128 : 512); }
+
+// Float32: the gradients of x and the weight apart, each in tiles of 128 x 128, where x's fill rounds of a workgroup
+// a unit and the weight's are shared out; else together in tiles of 64 x 64.  One MI355X, us apart, together: 8000 x
+// 512 x 512 110, 123 (252 tiles of x); 4000 x 1024 x 512 121, 134 (256); 20000 x 256 x 256 107, 98 (314); 3000 x 512 x
+// 512 86, 68 (96).  bf16 the same calls 53, 49; 46, 43; 52, 50; 37, 31.
+template <typename Dt>
+bool takes_apart(const DenseArgs& a, const GemmArgs& dw) {
+  if (!kStaged<Dt> || plan_split_wide<Dt>(dw).splits < 2) return false;
+  const int64_t tiles = (a.n + 127) / 128 * ((a.d_in + 127) / 128);
+  return tiles * 4 >= round_up(tiles, 256) * 3;
+}
 
 template <typename Dt>
 int dense_fwd(const DenseArgs& a, size_t* bytes) {
   using T = typename Dt::T;
   const bool worst = bytes != nullptr;
   const hipStream_t st = static_cast<hipStream_t>(a.stream);
-  if (a.n <= kFewRows) {
+  if (takes_few_fwd(a.n, a.d_in, a.d_out)) {
     const int64_t shares = few_shares(a.d_in, a.d_out);
     Arena arena{static_cast<char*>(a.workspace)};
     const int64_t ld = round_up(a.d_out, 4);
@@ -274,7 +297,7 @@ int dense_bwd(const DenseArgs& a, size_t* bytes) {
   again.dg = const_cast<uint16_t*>(d.plane[0]), again.ldh = d.ld, again.plane_stride = a.n * d.ld;
   again.e_dg = d.exponents, again.e_ld = d.exponents_ld;
   Split shared = product_again ? plan_split<Dt>(again) : Split{};
-  const bool few = product_again && a.n <= kFewRows;
+  const bool few = product_again && takes_few_bwd<Dt>(a.n, a.d_in);
   const int64_t ld_shared = round_up(a.d_out, 4);
   if (few) shared.splits = static_cast<int>(few_shares(a.d_in, a.d_out)), shared.elements = a.n * ld_shared;
   GemmArgs dx = product<Dt>(a.n, a.d_in, a.d_out, d, w, a.gx, a.d_in);
@@ -323,7 +346,8 @@ int dense_bwd(const DenseArgs& a, size_t* bytes) {
                        dim3(256), 0, st, a.gout, a.n, a.gout_stride, a.d_out, segment_rows(a.n), columns, ld_columns);
     rc = static_cast<int>(hipGetLastError());
   }
-  // the bias's sums: few partial rows join the last launch that adds shares, which reads them one after another
+  // the bias's sums: few partial rows join the last launch that adds shares, which reads them one after another (500 x
+  // 256 x 256 float32, 14 rows: 27 us, 29 apart; 1357 x 322 x 853 bf16, 42 rows: 30, 28)
   SplitSumArgs last{};
   if (a.gbias && column_rows <= 16 && (a.gx || a.gw)) {
     last.batch = 1, last.from[0] = columns, last.to[0] = a.gbias, last.m[0] = 1, last.n[0] = a.d_out;
@@ -334,7 +358,8 @@ int dense_bwd(const DenseArgs& a, size_t* bytes) {
   }
   if (rc) return rc;
   const int64_t tiles = round_up(a.d_in, 64) / 64 * (round_up(a.d_out, 64) / 64 + round_up(a.n, 64) / 64);
-  if (a.gx && a.gw && tiles <= 2 * 768) return gemm_launch_two_split<Dt>(dx, dw, sums, st, last);
+  if (a.gx && a.gw && tiles <= 2 * 768 && !takes_apart<Dt>(a, dw))
+    return gemm_launch_two_split<Dt>(dx, dw, sums, st, last);
   if (a.gx) rc = gemm_launch_split<Dt, false, true, kEpiStore, true>(dx, sums, st, a.gw ? SplitSumArgs{} : last);
   if (!rc && a.gw) rc = gemm_launch_split<Dt, true, true, kEpiStore, true>(dw, sums, st, last);
   return rc;

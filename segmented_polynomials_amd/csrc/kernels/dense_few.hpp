@@ -1,6 +1,6 @@
 // The dense layer of few rows, and the slope of products whose long sums are shared
 // out.
-//   forward   at most sixteen rows: gemm_rows.hpp; a long sum for few columns is
+//   forward   at most sixteen rows (32 of some widths): gemm_rows.hpp; a long sum for few columns is
 //             shared out over workgroups
 //   backward  the product again in the same form, its slope in a launch of its own that
 //             leaves d and the bias's gradient; then, of at most four rows, one pass over

@@ -11,7 +11,7 @@
 // of the lanes with its expert; counts of a wave stay in LDS.  One workgroup
 // orders short lists in one launch; longer ones take one launch that counts and one
 // that places, between them a third that adds the counts up where many
-// workgroups would each read all of them.
+// workgroups would each read too many of them.
 // The row operators run along the rows i, not the slots: a row of x, g or out
 // crosses memory once, whatever k is, and only the k rows by slot are scattered.
 // All are bound by memory.
@@ -33,6 +33,7 @@ enum { kSortAll = 0, kSortCount = 1, kSortPlace = 2 };
 struct SortLds {
   uint16_t before[kSortWaves][kMaxExperts + 2];  // a wave's count; then the count of the waves before it
   int base[kMaxExperts + 1];
+  int mine[kMaxExperts + 1];  // of the workgroups before
   int wave_sum[kSortWaves];
 };
 
@@ -77,7 +78,25 @@ expert_sort_kernel(ExpertSortArgs a, int blocks, int summed) {
     if (at < a.entries) e = static_cast<const I*>(a.experts)[at];
     expert[c] = e >= 0 && e < a.num ? static_cast<int>(e) : a.num;
   }
+  if constexpr (Mode == kSortPlace) {
+    for (int e = threadIdx.x; e < classes; e += blockDim.x) {
+      l.base[e] = summed ? a.counts[static_cast<int64_t>(blocks) * classes + e] : 0;
+      l.mine[e] = summed ? a.counts[static_cast<int64_t>(blockIdx.x) * classes + e] : 0;
+    }
+  }
   __syncthreads();
+  if constexpr (Mode == kSortPlace) {
+    // few workgroups' counts: all threads share them out (whole numbers: any order)
+    if (!summed) {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < blocks * classes; i += blockDim.x) {
+        const int e = i % classes, c = a.counts[i];
+        if (c == 0) continue;
+        atomicAdd(&l.base[e], c);
+        if (i / classes < static_cast<int>(blockIdx.x)) atomicAdd(&l.mine[e], c);
+      }
+    }
+  }
   const int bits = 32 - __clz(a.num);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -97,7 +116,6 @@ expert_sort_kernel(ExpertSortArgs a, int blocks, int summed) {
     asm volatile("" ::: "memory");
   }
   __syncthreads();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * classes;
   for (int e = threadIdx.x; e < classes; e += blockDim.x) {
     int run = 0;
     for (int w = 0; w < waves; ++w) {
@@ -105,50 +123,21 @@ expert_sort_kernel(ExpertSortArgs a, int blocks, int summed) {
       l.before[w][e] = static_cast<uint16_t>(run);
       run += c;
     }
-    if constexpr (Mode == kSortCount) a.counts[row + e] = run;
+    if constexpr (Mode == kSortCount) a.counts[static_cast<int64_t>(blockIdx.x) * classes + e] = run;
     if constexpr (Mode == kSortAll) l.base[e] = run;
   }
   if constexpr (Mode == kSortCount) return;
-  int mine[(kMaxExperts + kSortWaves * 64) / (kSortWaves * 64)] = {};  // of the workgroups before
-  if constexpr (Mode == kSortPlace) {
-#pragma unroll
-    for (int q = 0; q < static_cast<int>(sizeof(mine) / 4); ++q) {
-      const int e = q * (kSortWaves * 64) + threadIdx.x;  // these launches have all the waves
-      if (e >= classes) continue;
-      int total = 0;
-      if (summed) {
-        mine[q] = a.counts[row + e];
-        total = a.counts[static_cast<int64_t>(blocks) * classes + e];
-      } else {
-#pragma unroll 8
-        for (int b = 0; b < blocks; ++b) {
-          const int c = a.counts[static_cast<int64_t>(b) * classes + e];
-          mine[q] += b < static_cast<int>(blockIdx.x) ? c : 0;
-          total += c;
-        }
-      }
-      l.base[e] = total;
-    }
-  }
   __syncthreads();
   scan_base(l, classes);
   __syncthreads();
   if (blockIdx.x == 0)
     for (int e = threadIdx.x; e < classes; e += blockDim.x) a.offsets[e] = l.base[e];
-  if constexpr (Mode == kSortPlace) {
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < static_cast<int>(sizeof(mine) / 4); ++q) {
-      const int e = q * (kSortWaves * 64) + threadIdx.x;
-      if (e < classes) l.base[e] += mine[q];
-    }
-    __syncthreads();
-  }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int64_t at = first + c * 64;
     if (at >= a.entries) continue;
-    const int slot = l.base[expert[c]] + l.before[wave][expert[c]] + rank[c];
+    int slot = l.base[expert[c]] + l.before[wave][expert[c]] + rank[c];
+    if constexpr (Mode == kSortPlace) slot += l.mine[expert[c]];
     if (slot >= a.entries) continue;  // not reached while the list stays as it was counted
     a.place[at] = slot;
     a.order[slot] = static_cast<int>(at);
@@ -193,7 +182,9 @@ int expert_sort_launch(const ExpertSortArgs& a, const ExpertSortPlan& p) {
   }
   hipLaunchKernelGGL((expert_sort_kernel<I, C, kSortCount>), grid, threads, 0, st, a, blocks, 0);
   if (const hipError_t e = hipGetLastError()) return static_cast<int>(e);
-  const bool sum = blocks > 64;
+  // Unsummed, every workgroup reads all counts.  One MI355X, us so and with the third launch, by counts (blocks x
+  // classes): 3835 10.1, 11.5; 8320 12.3, 13.3 and 19.6, 20.6; 16512 15.8, 14.0 and 24.2, 22.4; 65792 36.8, 17.4
+  const bool sum = blocks * classes > 10240;
   if (sum) {
     hipLaunchKernelGGL(expert_counts_kernel, dim3(static_cast<unsigned>((classes + 31) / 32)), dim3(1024), 0, st, a.counts,
                        blocks, classes);
@@ -421,7 +412,14 @@ template <typename T>
 int combine_bwd_launch(const ExpertRowsArgs& a) {
   const int64_t chunks = (a.dim + Chunk<T>::kN - 1) / Chunk<T>::kN;
   const hipStream_t st = static_cast<hipStream_t>(a.stream);
-  const int per = chunks <= 16 ? 16 : chunks <= 128 ? 4 : 1;
+  // Rows of a workgroup: 16, 4 or 1.  One MI355X, us of 20000 rows of four choices, by width:
+  //               bf16 256     512    1024    2048 (8192 rows)  4096 (8192, k 8)   f32 128 (50000, k 2)  256   512  1024
+  //     16              19      33      81      65              301                    27                 32    80   193
+  //      4              31      35      75      59              254                    52                 36    78   160
+  //      1              90      90     128      68              237                   173                 87   120   148
+  // and few rows take more lanes each: 500 rows of 1024 bf16 15, 7.0, 6.5, f32 23, 9.3, 6.6.
+  int per = chunks <= 64 ? 16 : chunks <= (sizeof(T) == 2 ? 256 : 128) ? 4 : 1;
+  while (per > 1 && (a.n + per - 1) / per < 512 && chunks > 256 / per) per /= 4;
   const int64_t blocks = (a.n + per - 1) / per;
   const dim3 grid(static_cast<unsigned>(std::min(blocks, kMostBlocks)));
   auto* kernel = per == 16 ? expert_combine_bwd_kernel<T, 16>
@@ -435,8 +433,14 @@ int combine_bwd_launch(const ExpertRowsArgs& a) {
 ExpertSortPlan expert_sort_plan(int64_t entries, int64_t num) {
   ExpertSortPlan p{};
   p.waves = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kSortWaves, (entries + 63) / 64)));
-  p.chunks = entries <= 64 * kSortWaves ? 1 : entries <= 64 * kSortWaves * 4 * 128 ? 4 : 16;
-  if (entries > 64 * kSortWaves) p.waves = kSortWaves;
+  // 64 entries each of a wave: one where that gives the units work, more where the counts would grow as long as the
+  // list.  One MI355X, us with 1, 4 and 16 by entries (experts): 1200 (8) 7.3, 5.8, 10.8; 2048 (64) 8.2, 7.4, 13.7;
+  // 8000 (64) 8.7, 13, 18; 131072 (256) 16, 20, 46; 524288 (64) 23, 21, 39; 1048576 (128) 43, 26, 48; 2000000 (16) 58,
+  // 32, 38; 4000000 (2048) 387, 184, 139; 16000000 (64) 477, 254, 220.
+  constexpr int64_t kTurn = 64 * kSortWaves;
+  const bool one = entries <= kTurn, single = entries <= 4 * kTurn;
+  p.chunks = one || (!single && entries <= 256 * kTurn) ? 1 : entries <= 2048 * kTurn ? 4 : 16;
+  if (!one) p.waves = kSortWaves;
   const int64_t each = int64_t{64} * p.waves * p.chunks;
   p.blocks = std::max<int64_t>(1, (entries + each - 1) / each);
   p.bytes = p.blocks == 1 ? 0 : static_cast<size_t>(p.blocks + 1) * (num + 1) * 4;

@@ -144,7 +144,9 @@ Split plan_split(const GemmArgs& g) {
 
 // The same in tiles of 128 x 128, each element read and split or moved by half as
 // many tiles, where their shares fill the card: a compute unit holds one workgroup of
-// staged operands, two of others.  One MI355X, us of the weight's gradient: OLD_WIDE
+// staged operands, two of others.  One MI355X, us of the gradients with these and in tiles of 64 x 64:
+// 20000 x 512 x 512 float32 257, 288; 60000 x 256 x 1000 796, 898, bf16 262, 293; 8192 x 1024 x
+// 1024 float32 325, 376; of a product that half fills the card: 2000 x 2000 x 2000 bf16 73, 66.
 template <typename Dt>
 Split plan_split_wide(const GemmArgs& g) {
   constexpr int64_t kStep = Dt::kPlanes == 1 ? 64 : 32, kHeld = Dt::kPlanes == 1 ? 512 : 256;
@@ -290,15 +292,15 @@ int gemm_launch(GemmArgs& g, hipStream_t st) {
     constexpr bool kDense = Epi == kEpiDense || Epi == kEpiDenseBwd;
     const double large = kTwoAcross || kBwd ? cost(256, 128, kBwd ? 1 : 2, 1.0) : cost(256, 256, 1, 1.0);
     const double c128 = cost(128, 128, 2, 0.8), c64 = cost(64, 64, 3, 0.45);
-    if (!kDense && large <= c128 && large <= c64) {
-      if constexpr (kDense)
-        return 0;  // not reached
-      else if constexpr (kTwoAcross)
-        return gemm_launch_tile<Dt, 256, 128, 2, 2, 32, 3, AAcross, BAcross, Epi>(g, st);
-      else if constexpr (kBwd)
-        return gemm_launch_tile<Dt, 256, 128, 4, 2, 64, 3, AAcross, BAcross, Epi>(g, st);
-      else
-        return gemm_launch_tile<Dt, 256, 256, 2, 4, 64, 2, AAcross, BAcross, Epi>(g, st);
+    if constexpr (!kDense) {
+      if (large <= c128 && large <= c64) {
+        if constexpr (kTwoAcross)
+          return gemm_launch_tile<Dt, 256, 128, 2, 2, 32, 3, AAcross, BAcross, Epi>(g, st);
+        else if constexpr (kBwd)
+          return gemm_launch_tile<Dt, 256, 128, 4, 2, 64, 3, AAcross, BAcross, Epi>(g, st);
+        else
+          return gemm_launch_tile<Dt, 256, 256, 2, 4, 64, 2, AAcross, BAcross, Epi>(g, st);
+      }
     }
     if (c128 <= c64) return gemm_launch_tile<Dt, 128, 128, 2, 2, 64, 2, AAcross, BAcross, Epi>(g, st);
     return gemm_launch_tile<Dt, 64, 64, 2, 2, kSmallK<Dt>, kSmallS<Dt>, AAcross, BAcross, Epi>(g, st);

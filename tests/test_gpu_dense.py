@@ -103,7 +103,8 @@ def run(n, di, do, dtype, act, seed, bias=True, residual=True):
 
 
 SHAPES = [(1, 1, 1), (1, 8, 8), (3, 64, 128), (16, 72, 40), (17, 61, 35), (5, 1001, 333), (65, 128, 96), (130, 322, 257),
-          (300, 200, 520), (33, 2048, 96), (1000, 8, 64), (1000, 64, 64), (777, 128, 100), (700, 7, 3), (64, 256, 1)]
+          (300, 200, 520), (33, 2048, 96), (1000, 8, 64), (1000, 64, 64), (777, 128, 100), (700, 7, 3), (64, 256, 1),
+          (24, 1000, 70), (32, 130, 1030), (20, 1024, 33), (12, 100, 90), (12, 520, 90)]
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -118,7 +119,7 @@ def test_dense(n, di, do, dtype, act):
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("n,di,do", [(4096, 72, 2048), (2048, 4096, 136), (4100, 1030, 1032), (300, 8000, 20),
                                      (40, 3000, 5000), (70, 9000, 64), (20000, 33, 17), (50000, 64, 64), (9, 64, 4000),
-                                     (30000, 128, 512), (257, 64, 8000)])
+                                     (30000, 128, 512), (257, 64, 8000), (8000, 512, 512)])
 def test_dense_large(n, di, do, dtype, act):
     """Every tile, sums shared out over workgroups, many rows of few columns."""
     need_gpu()

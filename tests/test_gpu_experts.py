@@ -47,7 +47,7 @@ def sorted_on_host(e, num):
 
 SORTS = [(0, 2, 5), (1, 1, 1), (5, 2, 8), (64, 1, 3), (65, 1, 2048), (1024, 1, 64), (1025, 1, 64), (1000, 8, 128),
          (4096, 1, 1), (4097, 1, 7), (16384, 8, 128), (30000, 2, 2048), (70001, 4, 10), (300000, 2, 513),
-         (300000, 4, 2047)]
+         (300000, 4, 2047), (40000, 3, 400), (262144, 1, 50), (262145, 1, 50), (300000, 8, 20)]
 
 
 @pytest.mark.parametrize("idx", [torch.int32, torch.int64])
@@ -80,7 +80,8 @@ def test_sort_of_equal_and_missing_experts():
 
 
 ROWS = [(1, 1, 1, 1), (5, 2, 8, 1000), (33, 3, 4, 7), (700, 2, 16, 128), (257, 9, 5, 70), (100, 1, 3, 1030),
-        (40, 17, 64, 264), (6, 2, 3, 8200), (3000, 4, 10, 33), (64, 8, 8, 2048)]
+        (40, 17, 64, 264), (6, 2, 3, 8200), (3000, 4, 10, 33), (64, 8, 8, 2048),
+        (20000, 2, 8, 300), (2000, 3, 4, 1500), (3000, 2, 4, 1500)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
