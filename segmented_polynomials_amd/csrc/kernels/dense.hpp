@@ -268,7 +268,7 @@ int dense_bwd_fused(const DenseArgs& a, size_t* bytes) {
   using T = typename Dt::T;
   const hipStream_t st = static_cast<hipStream_t>(a.stream);
   Arena arena{static_cast<char*>(a.workspace)};
-  const int64_t blocks = fused_blocks<T>(a.n), ld = round_up(a.d_in, 4), ld_bias = round_up(a.d_out, 4);
+  const int64_t blocks = fused_blocks(a.n), ld = round_up(a.d_in, 4), ld_bias = round_up(a.d_out, 4);
   float* dw = arena.take<float>(blocks * a.d_out * ld);
   float* dbias = arena.take<float>(blocks * ld_bias);
   if (bytes) {

@@ -321,17 +321,14 @@ template <typename T>
 bool takes_fused_bwd(int64_t n, int64_t d_in, int64_t d_out) {
   return d_in <= kFusedWidth && d_out <= kFusedWidth && n >= (sizeof(T) == 4 ? 256 : 12288);
 }
-template <typename T>
-int64_t fused_blocks(int64_t n) {
-  const int64_t each = kFusedLds<T> > 80 * 1024 ? 1 : 2;  // workgroups that share a unit's LDS
-  return std::min<int64_t>((n + 15) / 16, 256 * each);
-}
+// one workgroup a unit: its registers take the unit whole
+inline int64_t fused_blocks(int64_t n) { return std::min<int64_t>((n + 15) / 16, 256); }
 
 template <typename Dt>
 int dense_fused_bwd(const FusedArgs& g, hipStream_t st) {
   using T = typename Dt::T;
   auto* kernel = g.k % 8 == 0 && g.cols % 8 == 0 ? dense_fused_bwd_kernel<Dt, true> : dense_fused_bwd_kernel<Dt, false>;
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(fused_blocks<T>(g.n))), dim3(kFusedWaves * 64), kFusedLds<T>, st, g);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(fused_blocks(g.n))), dim3(kFusedWaves * 64), kFusedLds<T>, st, g);
   return static_cast<int>(hipGetLastError());
 }
 
