@@ -129,3 +129,31 @@ def test_binding_checks_host_tensors():
         sp.expert_combine_fwd(t, e, off, w)
     with pytest.raises(ValueError):
         sp.expert_combine_bwd(t, t, e, off, w)
+
+
+def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(sp, "_raw_stream", lambda index: 100 + index)
+
+    def call(*args):
+        seen.append((current[0], args))
+        return sp.OK if args[0] == "good" else sp.E_INVALID
+
+    sp._call(0, call, "good")
+    sp._call(1, call, "good", 7)
+    with pytest.raises(sp.SegpolyError):
+        sp._call(1, call, "bad")
+    assert seen == [(0, ("good", 100)), (1, ("good", 7, 101)), (1, ("bad", 101))] and current[0] == 0

@@ -326,3 +326,28 @@ def test_graph_replays_and_side_stream(n, di, do, dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(captured, step()))
+
+
+@pytest.mark.parametrize("n,di,do,dtype,stride", [(1100, 64, 40, "f32", 1 << 21), (1100, 64, 72, "f32", 1 << 21),
+                                                  (1100, 520, 72, "f32", 1 << 21), (1100, 72, 520, "bf16", 1 << 21),
+                                                  (1100, 520, 72, "f16", 1 << 21), (12300, 64, 64, "bf16", 180000)])
+def test_rows_past_32_bits_of_elements(n, di, do, dtype, stride):
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"dense: rows {stride} elements apart {n} {di} {do} {dtype}")
+    x, w, b, res, g = case(n, di, do, dtype, 4)
+    out = sp.dense_fwd(x, w, bias=b, act="silu", residual=res)
+    full = sp.dense_bwd(x, w, g, bias=b, act="silu")
+    held = torch.empty(n * stride, dtype=T[dtype], device="cuda")
+    assert held.numel() > 2 ** 31
+
+    def apart(t, at):
+        v = torch.as_strided(held, t.shape, (stride, 1), at)
+        v.copy_(t)
+        return v
+
+    far, to = apart(x, 0), apart(res, 1024)
+    sp.dense_fwd(far, w, bias=b, act="silu", residual=to, out=to)
+    assert torch.equal(to, out)
+    got = sp.dense_bwd(far, w, apart(g, 2048), bias=b, act="silu")
+    assert all(torch.equal(p, q) for p, q in zip(got, full))

@@ -151,3 +151,25 @@ def test_share_that_is_kept():
         out = sp.dropout_fwd(torch.ones(2000, 1000, device="cuda"), p, 5)
         share = (out != 0).double().mean().item()
         assert abs(share - (1 - p)) <= 6 * (p * (1 - p) / 2e6) ** 0.5
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", ["element", "row"])
+def test_rows_past_32_bits_of_elements(mode):
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"dropout: rows far apart, and more than 2^31 elements, {mode}")
+    n, d, stride = 1100, 130, 1 << 21
+    x = normal(n, d, "bf16", 5)
+    want = sp.dropout_fwd(x, 0.3, 8, offset=2, mode=mode)
+    held = torch.empty(n * stride, dtype=torch.bfloat16, device="cuda")
+    far = torch.as_strided(held, (n, d), (stride, 1))
+    far.copy_(x)
+    assert torch.equal(sp.dropout_fwd(far, 0.3, 8, offset=2, mode=mode, out=far), want)
+    # the first columns of a wide call: a row's mask does not depend on the width
+    rows, wide = (1 << 17) + 5, 1 << 14
+    held = held[:rows * wide].view(rows, wide)
+    assert held.numel() > 2 ** 31
+    held.fill_(1.0)
+    a = sp.dropout_fwd(held[:, :40], 0.3, 8, mode=mode)
+    assert torch.equal(sp.dropout_fwd(held, 0.3, 8, mode=mode, out=held)[:, :40], a)
