@@ -2,7 +2,7 @@
 //   d = g act'(x W^T + bias),   dx = d W,   dW = d^T x,   dbias = sums of d's columns
 // Bound by memory: x and g are read once and dx is written once; a product at a time
 // would write d and read it twice, x twice and g three times.  A wave takes 16 rows at
-// a time (32 at once spill: float32 293 us for 600000 x 64 x 64, 150 with 16).  The
+// a time (32 at once spill: float32 293 us for 600000 x 64 x 64, 147 with 16).  The
 // weight stays in LDS in the two orders that its products take.  The product leaves
 // each lane eight neighbouring columns of a row (dense_stream.hpp), and d of these is
 // at once an operand of the next.  For dW the 16 rows are the sum: x and d go through
@@ -103,19 +103,32 @@ dense_fused_bwd_kernel(FusedArgs g) {
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const T* w = static_cast<const T*>(g.w);
   // fragments of both orders; of the second a lane's eight are a column of the weight
-  for (int u = wave; u < 2 * NF * KC; u += kFusedWaves) {
-    const bool second = u >= NF * KC;
-    const int f = u % (NF * KC) / KC, c = u % KC, i = stream_column(f, lane % 16), at = c * 32 + lane / 16 * 8;
+  constexpr int kUnits = 2 * NF * KC / kFusedWaves;  // of a wave, whose loads are in flight together: no branches
+  T raw[kUnits][8];
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    const int u = wave + j * kFusedWaves, f = u % (NF * KC) / KC, i = stream_column(f, lane % 16);
+    const int at = u % KC * 32 + lane / 16 * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int n = u >= NF * KC ? at + e : i, k = u >= NF * KC ? i : at + e;
+      raw[j][e] = w[(n < g.cols ? n : g.cols - 1) * g.k + (k < g.k ? k : g.k - 1)];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    const int u = wave + j * kFusedWaves, f = u % (NF * KC) / KC, i = stream_column(f, lane % 16);
+    const int at = u % KC * 32 + lane / 16 * 8;
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int n = second ? at + e : i, k = second ? i : at + e;
-      v[e] = n < g.cols && k < g.k ? static_cast<float>(w[static_cast<int64_t>(n) * g.k + k]) : 0.f;
+      const int n = u >= NF * KC ? at + e : i, k = u >= NF * KC ? i : at + e;
+      v[e] = n < g.cols && k < g.k ? static_cast<float>(raw[j][e]) : 0.f;
     }
     u16x8 p[PX];
     split_planes(v, p);
 #pragma unroll
-    for (int q = 0; q < PX; ++q) (second ? wx : wz)[((f * KC + c) * PX + q) * 64 + lane] = p[q];
+    for (int q = 0; q < PX; ++q) (u >= NF * KC ? wx : wz)[((f * KC + u % KC) * PX + q) * 64 + lane] = p[q];
   }
   if (threadIdx.x < kFusedWidth)
     bias[threadIdx.x] = g.bias && static_cast<int>(threadIdx.x) < g.cols
@@ -273,7 +286,9 @@ dense_fused_bwd_kernel(FusedArgs g) {
       asm volatile("" ::: "memory");
     }
   }
-  // the waves' sums: in each turn a wave adds its own to another eighth
+  // the waves' sums: in each turn a wave adds its own to another eighth.  Four columns of a row together, where
+  // neither neighbouring rows nor neighbouring columns share a bank (rows one after another: 7 us of turns, now 3).
+  auto place = [](int row, int four) { return row * kFusedWidth + (four ^ row % 16) * 4; };
   float* sums = reinterpret_cast<float*>(stage);
   float* bias_sums = sums + kFusedWidth * kFusedWidth;
   const int ld = (g.k + 3) / 4 * 4;
@@ -291,7 +306,7 @@ dense_fused_bwd_kernel(FusedArgs g) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int f = (e * 2 + h) / NF, j = (e * 2 + h) % NF;
-        v4f* at = reinterpret_cast<v4f*>(sums + (f * 16 + lane % 16) * kFusedWidth + j * 16 + lane / 16 * 4);
+        v4f* at = reinterpret_cast<v4f*>(sums + place(f * 16 + lane % 16, j * 4 + lane / 16));
         *at = turn ? *at + dw[f][j / 2][j % 2] : dw[f][j / 2][j % 2];
         float* b = bias_sums + (e * 2 + h) / 8 * 32 + chunk + (e * 2 + h) % 8;
         const float s = db[(e * 2 + h) / 8][(e * 2 + h) % 8];
@@ -302,7 +317,9 @@ dense_fused_bwd_kernel(FusedArgs g) {
   __syncthreads();
   if (g.dw) {
     float* to = g.dw + static_cast<int64_t>(blockIdx.x) * g.cols * ld;
-    for (int i = threadIdx.x; i < g.cols * ld; i += kFusedWaves * 64) to[i] = sums[i / ld * kFusedWidth + i % ld];
+    const int fours = ld / 4;
+    for (int i = threadIdx.x; i < g.cols * fours; i += kFusedWaves * 64)
+      *reinterpret_cast<v4f*>(to + i * 4) = *reinterpret_cast<const v4f*>(sums + place(i / fours, i % fours));
   }
   if (g.dbias) {
     const int ld_bias = (g.cols + 3) / 4 * 4;
@@ -313,13 +330,15 @@ dense_fused_bwd_kernel(FusedArgs g) {
 
 // Filling the weight in and adding up its gradients takes as long as some rows in
 // products of their own.  64 x 64, silu, one MI355X, us here and so:
-//           100       300       1500      6000      20000      600000
-//   f32   19, 16    19, 22    20, 40    22, 36     25, 42    150, 331
-//   bf16  18, 11    18, 12    19, 17    21, 20     21, 24     74, 253
-//   f16   20, 12    20, 13    21, 19    23, 22     22, 26     95, 319
+//           100       300       600      1500      6000      20000      600000
+//   f32   15, 16    15, 18    15, 22    16, 21    18, 25    21, 42    147, 331
+//   bf16  13, 12    13, 13    13, 14    14, 17    16, 21    17, 24     75, 253
+//   f16   14, 13    14, 14    15, 15    15, 19    17, 22    19, 26     96, 319
+// and without an activation, whose product in tiles is not done again: f32 100 rows 14,
+// 12, 300 rows 14, 14; bf16 600 rows 13, 11, 1500 rows 14, 15.
 template <typename T>
 bool takes_fused_bwd(int64_t n, int64_t d_in, int64_t d_out) {
-  return d_in <= kFusedWidth && d_out <= kFusedWidth && n >= (sizeof(T) == 4 ? 256 : 12288);
+  return d_in <= kFusedWidth && d_out <= kFusedWidth && n >= (sizeof(T) == 4 ? 128 : 1024);
 }
 // one workgroup a unit: its registers take the unit whole
 inline int64_t fused_blocks(int64_t n) { return std::min<int64_t>((n + 15) / 16, 256); }

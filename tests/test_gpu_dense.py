@@ -104,7 +104,8 @@ def run(n, di, do, dtype, act, seed, bias=True, residual=True):
 
 SHAPES = [(1, 1, 1), (1, 8, 8), (3, 64, 128), (16, 72, 40), (17, 61, 35), (5, 1001, 333), (65, 128, 96), (130, 322, 257),
           (300, 200, 520), (33, 2048, 96), (1000, 8, 64), (1000, 64, 64), (777, 128, 100), (700, 7, 3), (64, 256, 1),
-          (24, 1000, 70), (32, 130, 1030), (20, 1024, 33), (12, 100, 90), (12, 520, 90)]
+          (24, 1000, 70), (32, 130, 1030), (20, 1024, 33), (12, 100, 90), (12, 520, 90),
+          (1500, 40, 24), (1025, 64, 63), (129, 5, 64)]
 
 
 @pytest.mark.parametrize("act", ACTS)
