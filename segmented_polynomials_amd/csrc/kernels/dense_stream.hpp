@@ -9,14 +9,16 @@
 // that do not fit in LDS, and those of few rows, are shared out over workgroups.
 // One MI355X, us here and in tiles, silu (floor: the bytes at 5.0 TB/s):
 //                              bf16               f32
-//   600000 x 64 x 64       29,  50 (31)      69, 166 (61)
-//   100000 x 128 x 128     16,  22 (10)      37,  59 (21)
-//   20162 x 64 x 896       15,  26  (8)      31,  40 (16)
-//   50000 x 256 x 256      22,  24 (10)      75,  79 (28)
-//   5000 x 256 x 512       9.5, 8.7 (2)      26,  26  (6)
-//   1000 x 64 x 64        4.2, 4.8          5.9, 8.2
-//   20000 x 256 x 1024     27,  33 (10)     110,  91 (45)
-// float32 above 128 columns of x has no registers for the rows, and takes the tiles.
+//   600000 x 64 x 64       29,  54 (31)      69,  96 (61)
+//   100000 x 128 x 128     16,  20 (10)      37,  45 (21)
+//   20162 x 64 x 896       15,  22  (8)      31,  38 (16)
+//   200 x 128 x 128       4.5, 5.0          5.9, 8.1
+//   1000 x 64 x 64        4.2, 4.8          5.8, 6.2
+//   50000 x 256 x 256      23,  22 (10)      75,  64 (28)
+//   5000 x 256 x 512       9.3, 8.4 (2)      26,  19  (6)
+//   20000 x 256 x 1024     28,  29 (10)     110,  90 (45)
+// float32 above 128 columns of x has no registers for the rows, and takes the tiles; 16-bit
+// rows up to 256 do not, as those of odd widths need no packing launch here.
 // A pair of column fragments holds the columns in an order that leaves a lane
 // eight neighbouring ones of its row, 16 or 32 bytes to store together.
 #pragma once
