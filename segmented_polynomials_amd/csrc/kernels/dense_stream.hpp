@@ -4,9 +4,9 @@
 // time, its x from memory straight into the registers of the matrix instructions
 // (the next rows' loads in flight meanwhile, float32 split into its planes in
 // registers), and goes over the columns 32 at a time.  No barrier after the
-// weight has been filled in, no copy of x: the tiles of gemm_tile.hpp write
-// float32 rows as planes and read them again, three times the bytes of x.  Columns
-// that do not fit in LDS, and those of few rows, are shared out over workgroups.
+// weight has been filled in, where the tiles bring both operands to LDS step by step,
+// of which short sums have one to four.  Columns that do not fit in LDS, and those of
+// few rows, are shared out over workgroups.
 // One MI355X, us here and in tiles, silu (floor: the bytes at 5.0 TB/s):
 //                              bf16               f32
 //   600000 x 64 x 64       29,  54 (31)      69,  96 (61)
