@@ -218,9 +218,12 @@ dense_fused_bwd_kernel(FusedArgs g) {
             }
           });
         }
+        // rows past the last and columns past the width are zeros whatever their slopes: an infinity times the
+        // weight's zeros there is NaN, which the next product would spread over the row
+        const int real = is ? g.cols - (c * 32 + chunk) : 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          v[i] = is ? v[i] : 0.f;
+          v[i] = (Whole ? 0 : i) < real ? v[i] : 0.f;
           db[c][i] += v[i];
         }
         split_planes(v, d[c]);
