@@ -425,7 +425,6 @@ __device__ __forceinline__ void finish_tile(const GemmArgs& g, int z, int64_t m0
         const T* row = static_cast<const T*>(g.res) + (m < gm ? m : 0) * g.ld_res;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-          // past the last row and column the gradients are zero, the products too
           v4f r = {0.f, 0.f, 0.f, 0.f};
           if (g.res && m < gm) r = load_four(row, col0 + j * 16, gn);
 #pragma unroll
@@ -436,6 +435,17 @@ __device__ __forceinline__ void finish_tile(const GemmArgs& g, int z, int64_t m0
         }
       }
     });
+    // d past the last row and column is zero whatever its slope, which an infinity times the operands' zeros there
+    // makes NaN: the column sums take the rows, the next product the columns up to a multiple of eight
+    if (Epi == kEpiDenseBwd && (m0 + BM > gm || n0 + BN > gn)) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (row0 + i * 16 >= gm || col0 + j * 16 + q >= gn) acc[i][j][q] = 0.f;
+    }
   }
   // float32 rows: 16 bytes a lane, 64 of a row together
   auto store_rows = [&](T* to, int64_t ld) __attribute__((always_inline)) {

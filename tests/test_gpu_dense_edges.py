@@ -12,8 +12,10 @@ from tests.test_gpu_dense import case
 pytestmark = pytest.mark.gpu
 
 INF, NAN = float("inf"), float("nan")
-# few rows, and one pass over the rows; widths of d_out that end inside a chunk of eight or a block of 32
-FORMS = [(3, 72, 40), (3, 72, 33), (2000, 64, 40), (2000, 40, 33), (2000, 20, 7)]
+# few rows (two forms), products again of few rows and in shares, tiles of 64 and 128 rows, one pass over the rows;
+# widths of d_out that end inside a chunk of eight, a block of 32 or a tile
+FORMS = [(3, 72, 40), (3, 72, 33), (12, 600, 33), (40, 3000, 65), (300, 72, 33), (300, 72, 40), (700, 130, 853),
+         (9000, 200, 300), (150, 64, 40), (150, 40, 33), (2000, 64, 40), (2000, 40, 33), (2000, 20, 7)]
 
 
 def rows_without(t, *at):
