@@ -942,6 +942,17 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int64_t id, int sha
       }
     };
     wait_and_meet<0>();  // every wave has read its last fragments
+    // hidden columns past the last, which the next products read up to a multiple of eight, are zero: an infinity in a
+    // row makes NaN of it and the weights' zeros there
+    if (n0 + BN / 2 > gn) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN / 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (n0 + col0 + j * 16 + q >= gn) acc[i][j][q] = acc[i][j + FN / 2][q] = 0.f;
+    }
     // dh of the wave's fragments
     constexpr int kD = Epi == kEpiGatedBwd ? 1 : 0;
     v4f d[kD ? FM : 1][kD ? FN / 2 : 1];
