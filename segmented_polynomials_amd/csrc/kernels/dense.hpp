@@ -308,7 +308,7 @@ int dense_bwd(const DenseArgs& a, size_t* bytes) {
   GemmArgs dx = product<Dt>(a.n, a.d_in, a.d_out, d, w, a.gx, a.d_in);
   GemmArgs dw = product<Dt>(a.d_out, a.d_in, a.n, d, x, a.gw, a.d_in);
   SplitSpace<Dt> space;  // sized for every gradient, asked for or not
-  space.add(product_again ? shared.splits * shared.elements : 0);
+  space.add(few ? shared.splits * shared.elements : space.of(shared));
   space.add(space.of(dx) + space.of(dw));
   space.add(space.of(plan_split_wide<Dt>(dx)));
   space.add(space.of(plan_split_wide<Dt>(dw)));
