@@ -838,8 +838,8 @@ int dense_workspace(int dtype, int act, int64_t n, int64_t d_in, int64_t d_out, 
  *   x [n, d_in], w [d_out, d_in], bias [d_out] or NULL, residual [n, d_out] or
  *   NULL, out [n, d_out] (may be residual itself), all T.  act: SEGPOLY_ACT_*.
  * Widths and, of more than one row, x's row stride are at most 2^21
- * (E_UNSUPPORTED, E_INVALID above); out, x and w have fewer than 2^24 tiles of
- * 64 x 64 (E_UNSUPPORTED above).  Products on the matrix cores with float32 sums, float32
+ * (E_UNSUPPORTED, E_INVALID above), the residual's and out's row strides any; out,
+ * x and w have fewer than 2^24 tiles of 64 x 64 (E_UNSUPPORTED above).  Products on the matrix cores with float32 sums, float32
  * operands with 24 bits.
  */
 int dense_fwd(int dtype, int act, const void* x, int64_t x_stride, const void* w, const void* bias, const void* residual,
@@ -852,8 +852,9 @@ int dense_fwd(int dtype, int act, const void* x, int64_t x_stride, const void* w
  * ACT_NONE, which reads no bias), and the gradient before the activation is held
  * in T's precision or better.  grad_x [n, d_in], grad_w [d_out, d_in], grad_bias [d_out],
  * T, any of them NULL but not all; fully overwritten.  The residual's gradient is
- * grad_out itself.  With n == 0 the weight's and the bias's gradients are zero,
- * and no input or workspace is read (all may be NULL).
+ * grad_out itself.  Limits as dense_fwd; grad_out's row stride, of more than one row,
+ * is at most 2^21 too (E_INVALID above).  With n == 0 the weight's and the bias's
+ * gradients are zero, and no input or workspace is read (all may be NULL).
  */
 int dense_bwd(int dtype, int act, const void* x, int64_t x_stride, const void* w, const void* bias, const void* grad_out,
               int64_t grad_out_stride, int64_t n, int64_t d_in, int64_t d_out, void* grad_x, void* grad_w,
@@ -902,7 +903,7 @@ int expert_sort_workspace(int64_t entries, int64_t num_experts, size_t* bytes);
  *   entry.  offsets [num_experts + 1]: expert q has the slots from offsets[q] to
  *   offsets[q + 1]; slots from offsets[num_experts] on have none.  ids [entries]:
  *   the expert of each slot, -1 without one (the sorted class indices of
- *   linear_fwd, whose rows out of range are zero).
+ *   linear_fwd, of float32 and float64, whose rows out of range are zero).
  * num_experts at most 2048 (E_UNSUPPORTED above).  With no entries experts, order,
  * place and ids may be NULL.
  */

@@ -1310,7 +1310,8 @@ def dense_fwd(x, w, bias=None, act="none", residual=None, out=None, workspace=No
     """out = act(x w^T + bias) + residual; ``x`` [n, d_in] and ``residual``
     [n, d_out] with contiguous rows, ``w`` [d_out, d_in], ``bias`` [d_out], all of
     one dtype; ``act`` 'none', 'silu', 'gelu', 'relu' or 'sigmoid'.  ``out`` may
-    be ``residual``."""
+    be ``residual``.  Rows of ``x``, and of ``grad_out`` in ``dense_bwd``, are at most
+    2^21 elements apart."""
     dt, a, n, d_in, d_out, stride = _dense_common(x, w, bias, act)
     rs = 0 if residual is None else _rows("residual", residual, x, n, d_out)
     out, os_ = _out_rows("out", out, x, n, d_out)
@@ -1400,7 +1401,7 @@ def expert_sort(experts, num_experts, workspace=None):
     slot; ``place`` [n, k]: the slot of each entry; ``offsets``
     [num_experts + 1]: the slots of expert q are offsets[q] to offsets[q + 1];
     ``ids`` [n * k]: the expert of each slot, the class indices of
-    ``linear_fwd``.  Equal ones keep their order; entries outside
+    ``linear_fwd`` (float32 and float64).  Equal ones keep their order; entries outside
     [0, num_experts) come last and have the id -1."""
     import torch
     idx = _index_dtype(experts)

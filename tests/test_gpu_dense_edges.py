@@ -130,3 +130,24 @@ def test_infinities_and_nan_in_the_bias(n, di, do, dtype):
         else:
             assert torch.isnan(dx).all() and torch.isnan(dw[3]).all() and torch.isnan(db[3])
             assert torch.equal(rows_without(db, 3), rows_without(none[2], 3)) and torch.isfinite(rows_without(dw, 3)).all()
+
+
+@pytest.mark.parametrize("n,di,do,dtype", [(3, 72, 40, "f32"), (40, 64, 72, "bf16"), (40, 64, 72, "f32"), (40, 520, 72, "f16"),
+                                           (40, 520, 72, "f32"), (5, 4096, 40, "bf16")])
+def test_output_rows_far_apart(n, di, do, dtype):
+    """The residual's and the output's rows may be any distance apart; those of x
+    and grad_out are refused past 2^21 elements."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"dense: rows of the output far apart {n} {di} {do} {dtype}")
+    x, w, b, res, g = case(n, di, do, dtype, 8)
+    stride = (1 << 21) + 24
+    held = torch.empty(n * stride, dtype=x.dtype, device="cuda")
+    to = torch.as_strided(held, (n, do), (stride, 1), 5)
+    to.copy_(res)
+    sp.dense_fwd(x, w, bias=b, act="silu", residual=to, out=to)
+    assert torch.equal(to, sp.dense_fwd(x, w, bias=b, act="silu", residual=res))
+    with pytest.raises(sp.SegpolyError):
+        sp.dense_bwd(x, w, to, bias=b, act="silu")
+    with pytest.raises(sp.SegpolyError):
+        sp.dense_fwd(torch.as_strided(held, (n, di), (stride, 1)), w, bias=b)
