@@ -11,9 +11,11 @@ experts on its nodes:
 
     python examples/expert_network.py [--steps 20]
 
-Everything but the softmax of the chosen scores, the loss and the weight update
-runs in the library's kernels, forward and backward.  Float32 (the class-indexed
-linear layer's type); data: seeded random graph and targets.
+The five steps run in the library's kernels, forward and backward.  PyTorch's are
+the choice of the experts (top-k, the softmax of their scores and its gradient), the
+order of the edges by source, the sums of gradients of one tensor, the loss and the
+weight update.  Float32 (the class-indexed linear layer's type); data: seeded random
+graph and targets.
 """
 
 import argparse
