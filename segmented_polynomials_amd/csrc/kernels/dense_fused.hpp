@@ -57,10 +57,11 @@ __device__ __forceinline__ v4f mma16(bf16, s16x4 a, s16x4 b, v4f c) {
 }
 
 // c (large products) and s (small ones) of the planes of two operands with those of b,
-// in turn: neither waits for its own last
+// in turn: neither waits for its own last.  Of two planes each, whole float16 values, all
+// four products count: the smallest is up to 2^-16 of the largest.
 template <int PA, int PB, typename V>
 __device__ __forceinline__ void multiply_two(const V (&a)[2][PA], const V (&b)[PB], v4f (&c)[2], v4f (&s)[2]) {
-  constexpr int kTop = (PA > PB ? PA : PB) - 1;  // of the sum of two planes' numbers
+  constexpr int kTop = PA == 2 && PB == 2 ? 2 : (PA > PB ? PA : PB) - 1;  // of the sum of two planes' numbers
 #pragma unroll
   for (int t = kTop; t > 0; --t)
 #pragma unroll
@@ -336,7 +337,7 @@ dense_fused_bwd_kernel(FusedArgs g) {
 //           100       300       600      1500      6000      20000      600000
 //   f32   15, 16    15, 18    15, 22    16, 21    18, 25    21, 42    147, 331
 //   bf16  13, 12    13, 13    13, 14    14, 17    16, 21    17, 24     75, 253
-//   f16   14, 13    14, 14    15, 15    15, 19    17, 22    19, 26     96, 319
+//   f16   14, 13    14, 14    15, 15    16, 19    17, 22    19, 26    102, 319
 // and without an activation, whose product in tiles is not done again: f32 100 rows 14,
 // 12, 300 rows 14, 14; bf16 600 rows 13, 11, 1500 rows 14, 15.
 template <typename T>

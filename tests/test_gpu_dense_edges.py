@@ -151,3 +151,27 @@ def test_output_rows_far_apart(n, di, do, dtype):
         sp.dense_bwd(x, w, to, bias=b, act="silu")
     with pytest.raises(sp.SegpolyError):
         sp.dense_fwd(torch.as_strided(held, (n, di), (stride, 1)), w, bias=b)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("n,di,do", FORMS + [(66000, 64, 16)])
+def test_products_are_whole(n, di, do, dtype):
+    """(1 + 2^-8)^2 - (1 + 2^-7) is 2^-16 exactly: the square's last bit, past what one bfloat16 part of a factor
+    holds, counts in the output and in both gradients."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"dense: whole products {n} {di} {do} {dtype}")
+    t = {"f32": torch.float32, "f16": torch.float16}[dtype]
+    one, two = 1 + 2.0 ** -8, 1 + 2.0 ** -7
+    x, w, g = (torch.zeros(s, dtype=t, device="cuda") for s in ((n, di), (do, di), (n, do)))
+    x[1, 2], x[1, 3], w[4, 2], w[4, 3] = one, two, one, -1
+    out = sp.dense_fwd(x, w)
+    assert out[1, 4].item() == 2.0 ** -16 and out.count_nonzero() == 1
+    x.zero_(), w.zero_()
+    g[1, 2], g[1, 3], w[2, 4], w[3, 4] = one, two, one, -1
+    dx = sp.dense_bwd(x, w, g, need_dw=False)[0]
+    assert dx[1, 4].item() == 2.0 ** -16 and dx.count_nonzero() == 1
+    g.zero_(), w.zero_()
+    g[1, 4], g[2, 4], x[1, 2], x[2, 2] = one, two, one, -1
+    dw = sp.dense_bwd(x, w, g, need_dx=False)[1]
+    assert dw[4, 2].item() == 2.0 ** -16 and dw.count_nonzero() == 1
