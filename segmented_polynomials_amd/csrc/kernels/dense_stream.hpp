@@ -42,11 +42,17 @@ __device__ __forceinline__ int stream_column(int fragment, int i) {
   return fragment / 2 * 32 + i / 4 * 8 + fragment % 2 * 4 + i % 4;
 }
 
+// Workgroups that a unit's registers hold: two of at most 128 a lane.
+template <typename Dt>
+constexpr int stream_held(int chunks, bool res, bool whole) {
+  return (Dt::kPlanes > 1 ? chunks == 1 && (whole || !res) : chunks <= 2 || whole) ? 2 : 1;
+}
+
 // KC: 32 k each of a row.  Loads return in order: the residual's would wait for the
 // next rows' if those were on their way already, so with it they are fetched later.
 // Whole: x's width is a multiple of 16 bytes, the output's of eight columns.
 template <typename Dt, int KC, int R, bool Res, bool Whole>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, 2 * stream_held<Dt>(KC, Res, Whole))
 dense_stream_kernel(StreamArgs g) {
   using T = typename Dt::T;
   constexpr int P = Dt::kPlanes;
@@ -185,14 +191,15 @@ int64_t stream_pair_bytes(int chunks) { return 32 * (chunks * Dt::kPlanes * 64 +
 template <typename Dt, int KC, int R>
 int stream_launch(StreamArgs g, hipStream_t st) {
   const int64_t tiles = (g.n + 16 * R - 1) / (16 * R), all = (g.cols + 31) / 32;
-  // two workgroups share a unit's LDS; fewer columns each until eight waves a unit have
-  // work (20162 x 64 x 896 bf16: 15 us, 19 with four)
+  // two workgroups share a unit's LDS, where its registers hold two (where they do not, a second round of them would
+  // fill the weight in again: 5000 x 64 x 64 float32 7.5 us, now 5.8; 20000 x 64 x 64 9.6, 7.7); fewer columns each
+  // until eight waves a unit have work (20162 x 64 x 896 bf16: 15 us, 19 with four)
+  const bool whole = g.k % Chunk<typename Dt::T>::kN == 0 && g.cols % 8 == 0;
   int64_t pairs = std::min(all, std::max<int64_t>(1, 80 * 1024 / stream_pair_bytes<Dt>(KC)));
   while (pairs > 1 && tiles * ((all + pairs - 1) / pairs) < 2048) pairs = (pairs + 1) / 2;
   const int64_t groups = (all + pairs - 1) / pairs;
   g.pairs = static_cast<int>((all + groups - 1) / groups);
-  const int64_t blocks = std::min<int64_t>(tiles, std::max<int64_t>(1, 512 / groups));
-  const bool whole = g.k % Chunk<typename Dt::T>::kN == 0 && g.cols % 8 == 0;
+  const int64_t blocks = std::min<int64_t>(tiles, std::max<int64_t>(1, 256 * stream_held<Dt>(KC, g.res, whole) / groups));
   auto* kernel = whole ? (g.res ? dense_stream_kernel<Dt, KC, R, true, true> : dense_stream_kernel<Dt, KC, R, false, true>)
                        : (g.res ? dense_stream_kernel<Dt, KC, R, true, false> : dense_stream_kernel<Dt, KC, R, false, false>);
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(groups)), dim3(512),
