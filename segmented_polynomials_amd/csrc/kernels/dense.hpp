@@ -199,7 +199,7 @@ int dense_fwd(const DenseArgs& a, size_t* bytes) {
               : dense_sum<T>({sums, a.n * ld, a.n, a.d_out, ld, static_cast<int>(shares), a.act, a.bias, a.residual,
                               a.residual_stride, a.out, a.out_stride}, st);
   }
-  if (stream_chunks<Dt>(a.d_in)) {
+  if (takes_stream<Dt>(a.n, a.d_in, a.d_out)) {
     if (worst) {
       *bytes = 0;
       return 0;

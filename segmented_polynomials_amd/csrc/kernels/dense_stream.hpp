@@ -7,18 +7,7 @@
 // weight has been filled in, where the tiles bring both operands to LDS step by step,
 // of which short sums have one to four.  Columns that do not fit in LDS, and those of
 // few rows, are shared out over workgroups.
-// One MI355X, us here and in tiles, silu (floor: the bytes at 5.0 TB/s):
-//                              bf16               f32
-//   600000 x 64 x 64       29,  54 (31)      69,  96 (61)
-//   100000 x 128 x 128     16,  20 (10)      37,  45 (21)
-//   20162 x 64 x 896       15,  22  (8)      31,  38 (16)
-//   200 x 128 x 128       4.5, 5.0          5.9, 8.1
-//   1000 x 64 x 64        4.2, 4.8          5.8, 6.2
-//   50000 x 256 x 256      23,  22 (10)      75,  64 (28)
-//   5000 x 256 x 512       9.3, 8.4 (2)      26,  19  (6)
-//   20000 x 256 x 1024     28,  29 (10)     110,  90 (45)
-// float32 above 128 columns of x has no registers for the rows, and takes the tiles; 16-bit
-// rows up to 256 do not, as those of odd widths need no packing launch here.
+// The times of both forms stand at takes_stream.
 // A pair of column fragments holds the columns in an order that leaves a lane
 // eight neighbouring ones of its row, 16 or 32 bytes to store together.
 #pragma once
@@ -182,6 +171,34 @@ int stream_chunks(int64_t d_in) {
   for (int chunks = 1; chunks <= kMost; chunks *= 2)
     if (d_in <= chunks * 32) return chunks;
   return 0;
+}
+
+// Which calls of more rows than gemm_rows.hpp's take this form.  One MI355X, us here and in tiles, silu, operands in
+// the last-level cache (from memory both take longer, to the same sides):
+//   float32                     bf16, whole chunks          bf16, widths of x or out that are none
+//   1000 x 64 x 64    5.4, 5.8   1000 x 64 x 64    3.7, 4.4   400 x 255 x 256    5.9, 7.6   20000 x 64 x 250    9.3,  11
+//   200 x 128 x 128   5.5, 7.7   200 x 128 x 128   4.0, 4.5   2000 x 255 x 1024   19,  10   100000 x 64 x 1023  109,  81
+//   5000 x 64 x 256   7.8, 7.3   2000 x 64 x 1024  5.1, 5.8   20000 x 255 x 64    13,  16   1000 x 192 x 1023   6.6, 5.6
+//   20000 x 64 x 64   7.7, 7.2   20000 x 128 x 128 6.9, 6.9   100000 x 255 x 16   26,  37   5000 x 256 x 250    7.6, 6.8
+//   20000 x 128 x 128  13,  13   20162 x 64 x 896   15,  21   154122 x 243 x 124  42,  63   20000 x 250 x 1020   31,  39
+//   20162 x 64 x 896   28,  38   600000 x 64 x 64   28,  50   2000 x 127 x 1024   12, 8.5   100000 x 62 x 255    32,  38
+//   600000 x 64 x 64   64,  90   2000 x 256 x 1024 8.5, 6.9   100000 x 127 x 256  52,  41   100000 x 62 x 1024  130,  89
+//   100000 x 127 x 256 58,  84   20000 x 256 x 256  13,  12   100000 x 63 x 1024 139,  89   113893 x 19 x 134    22,  36
+//   2000 x 64 x 1022   11, 7.8   50000 x 256 x 256  22,  21
+//   100000 x 64 x 63   23,  19   300 x 256 x 1024  5.0, 5.2
+//   82491 x 61 x 27    12,  17   200000 x 256 x 256 51,  64
+// 16-bit rows of x that are no whole chunks are copied before the tiles take them, 3 us and more; those of odd width, at
+// any two bytes, cost the streamed loads and stores more than that where there are many.
+template <typename Dt>
+bool takes_stream(int64_t n, int64_t d_in, int64_t d_out) {
+  const int64_t chunks = stream_chunks<Dt>(d_in), size = n * d_out;
+  if (chunks == 0) return false;
+  if (Dt::kPlanes > 1) return !(chunks <= 2 && d_out % 8 != 0 && d_out > 32 && size >= 1 << 19 && size < 1 << 24);
+  if (d_in % 8 == 0 && d_out % 8 == 0)  // all but whole steps of the tiles' sums
+    return !(d_in > 128 && d_in % 64 == 0 && d_out >= 256 && size >= 1 << 20 && size <= 3 << 22);
+  if (d_out <= (n >= 1 << 16 ? 192 : 64)) return true;
+  if (d_in % 8 != 0 && d_in % 2 == 0) return size < 1 << 25;
+  return size < (chunks <= 4 ? 1 << 23 : 1 << 20);
 }
 
 // Bytes of LDS of 32 columns of the weight and their bias.

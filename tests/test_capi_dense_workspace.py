@@ -83,3 +83,19 @@ def test_backward_in_tiles(n, di, do, dtype):
     assert fixed <= size <= fixed + taken(512 * 128 * 128 + 768 * 64 * 64)
     none = sp.dense_workspace(dtype, "none", n, di, do, True)
     assert none <= packed(dtype, (n, di), (do, di), (n, do)) + taken(4096 * up(do, 4)) + taken(512 * 128 * 128 + 768 * 64 * 64)
+
+
+@pytest.mark.parametrize("dtype", [sp.BF16, sp.F16])
+def test_forward_rules_of_16_bit_rows(dtype):
+    """Both sides of the rule: the streaming form asks for nothing, tiles for
+    their operands' copies."""
+    copies = lambda n, di, do: packed(dtype, (n, di), (do, di))
+    none = [(400, 255, 256), (200000, 255, 64), (400, 127, 512), (5000, 63, 512), (8000, 31, 1000), (1000, 192, 1024),
+            (50000, 256, 256), (2000, 256, 248), (2000, 184, 1024), (20000, 250, 1020), (100000, 62, 255),
+            (20000, 64, 250), (400, 256, 250), (70000, 255, 120), (70000, 31, 190), (500000, 255, 190)]
+    for n, di, do in none:
+        assert sp.dense_workspace(dtype, "silu", n, di, do) == 0, (n, di, do)
+    for n, di, do in ((4200, 255, 256), (17000, 127, 512), (17000, 63, 520), (9000, 31, 1000), (1100, 192, 1024),
+                      (4100, 256, 256), (40000, 62, 1024), (1100, 192, 1023), (5000, 256, 255), (20000, 128, 1023),
+                      (70000, 255, 200), (70000, 31, 260)):
+        assert sp.dense_workspace(dtype, "silu", n, di, do) == copies(n, di, do) > 0, (n, di, do)
