@@ -155,13 +155,33 @@ inline int64_t segments(int64_t n) { return (n + segment_rows(n) - 1) / segment_
 constexpr int64_t kFewRows = 16, kFewRowsBwd = 4;
 
 // The rows' form of the product against tiles (or the streaming form).  One MI355X, us, silu, rows' form first:
-//                 16 x 64 x 64    16 x 1024 x 1024   16 x 4096 x 4096   32 x 256 x 256   32 x 1024 x 4096   32 x 4096 x 4096
-//   forward bf16      3.1, 3.6          6.4, 8.1            11, 12          4.3, 4.4          6.7, 8.1            16, 13
-//           f32       4.6, 5.3          9.1, 13             23, 29          7.2, 12            14, 16             39, 28
+//                 16 x 64 x 64    16 x 1024 x 1024   16 x 4096 x 4096   32 x 256 x 256   32 x 1024 x 4096
+//   forward bf16      3.1, 3.6          6.4, 8.1            11, 12          3.9, 4.1          6.3, 7.9
+//           f32       4.6, 5.3          9.1, 13             23, 29          6.9, 11           13, 15
 //   gradient's: 16 rows of 64 x 64 bf16 9.2, 8.1, f32 12, 10; of 256 x 256 10.5, 9.7 and 19, 22; of 1024 x 1024
 //   15, 16 and 23, 27; of 4096 x 4096 41, 39 and 83, 87 (its slope takes a launch more)
-inline bool takes_few_fwd(int64_t n, int64_t d_in, int64_t d_out) {
-  return n <= kFewRows || (n <= 2 * kFewRows && d_in > 128 && d_in <= 1024 && d_out <= 4096);
+// and where 17 to 32 rows end, 17 and 32 rows (f16 as bf16):
+//   bf16  64 x 64 3.3, 3.4 and 3.4, 3.6; 2048 x 512 7.0, 9.6 and 7.5, 9.6; 2048 x 4096 8.5, 10.8 and 9.7, 11.0; 8192 x
+//         512 7.9, 9.5 and 8.6, 9.6; 4096 x 1024 8.5, 10.1 and 9.3, 10.3; 1024 x 8192 7.8, 8.8 and 9.2, 8.9; 7920 x
+//         791 (28 rows) 10.5, 12.9; past these 4096 x 2048 12.3, 11.2 and 15.1, 11.4; 8192 x 1024 11.2, 10.8 and 12.6,
+//         10.9; 512 x 16384 7.8, 7.1 and 9.3, 7.2.
+//         Weights of even width that the tiles need copied: 510 x 512 4.2, 8.4 and 4.5, 8.4; 2046 x 4096 8.5, 22 and
+//         9.4, 22; 8190 x 8192 38, 78 and 49, 83; odd ones, whose loads cost more, as those of whole chunks
+//   f32   136 x 64 6.1, 8.1 and 6.0, 8.2; 512 x 512 7.8, 11.4 and 8.5, 11.7; 1024 x 8192 18, 23 and 20, 23; 2048 x 512
+//         10.8, 12.3 and 11.3, 12.6; 4096 x 512 10.1, 12.4 and 10.7, 12.8; past these 128 x 1024 6.1, 5.4 and 6.2, 5.4;
+//         2048 x 2048 20.4, 14.4 and 21.6, 14.5; 4096 x 4096 37, 27 and 39, 27; 256 x 32768 18.9, 14.8 and 20.9, 15.3;
+//         and of widths that the tiles load in pieces, 125 x 5920 (19 rows) 7.1, 10.2; 1897 x 2959 (31) 19.7, 24.7; 1669 x
+//         5377 (22) 24.8, 37.4; but 2046 x 2048 6 to 10 % behind
+template <typename Dt>
+bool takes_few_fwd(int64_t n, int64_t d_in, int64_t d_out) {
+  if (n <= kFewRows || n > 2 * kFewRows) return n <= kFewRows;
+  const int64_t size = d_in * d_out;
+  if (kStaged<Dt>) {
+    if (d_in % 4 != 0 && d_in > 1024 && d_in <= 2048) return d_out <= 8192;
+    return d_in > (d_out <= 4096 ? 128 : 64) && d_out <= 8192 && (d_in <= 1024 || size <= 1 << 21);
+  }
+  if (d_in % 8 != 0 && d_in % 2 == 0) return true;
+  return d_out <= (d_in <= 1024 ? 8192 : 4096) && size <= (d_in <= 2048 ? 1 << 23 : 3 << 21);
 }
 template <typename Dt>
 bool takes_few_bwd(int64_t n, int64_t d_in) { return n <= kFewRows && d_in >= (kStaged<Dt> ? 128 : 512); }
@@ -182,7 +202,7 @@ int dense_fwd(const DenseArgs& a, size_t* bytes) {
   using T = typename Dt::T;
   const bool worst = bytes != nullptr;
   const hipStream_t st = static_cast<hipStream_t>(a.stream);
-  if (takes_few_fwd(a.n, a.d_in, a.d_out)) {
+  if (takes_few_fwd<Dt>(a.n, a.d_in, a.d_out)) {
     const int64_t shares = few_shares(a.d_in, a.d_out);
     Arena arena{static_cast<char*>(a.workspace)};
     const int64_t ld = round_up(a.d_out, 4);

@@ -87,15 +87,29 @@ def test_backward_in_tiles(n, di, do, dtype):
 
 @pytest.mark.parametrize("dtype", [sp.BF16, sp.F16])
 def test_forward_rules_of_16_bit_rows(dtype):
-    """Both sides of the rule: the streaming form asks for nothing, tiles for
-    their operands' copies."""
+    """Both sides of the rules: the streaming form asks for nothing, the rows'
+    form with one share neither, tiles for their operands' copies."""
     copies = lambda n, di, do: packed(dtype, (n, di), (do, di))
     none = [(400, 255, 256), (200000, 255, 64), (400, 127, 512), (5000, 63, 512), (8000, 31, 1000), (1000, 192, 1024),
             (50000, 256, 256), (2000, 256, 248), (2000, 184, 1024), (20000, 250, 1020), (100000, 62, 255),
-            (20000, 64, 250), (400, 256, 250), (70000, 255, 120), (70000, 31, 190), (500000, 255, 190)]
+            (20000, 64, 250), (400, 256, 250), (70000, 255, 120), (70000, 31, 190), (500000, 255, 190),  # streaming
+            (17, 64, 64), (32, 128, 1024), (32, 2048, 4096), (32, 1024, 8192), (24, 8190, 8192)]         # few rows
     for n, di, do in none:
         assert sp.dense_workspace(dtype, "silu", n, di, do) == 0, (n, di, do)
+    for n, di, do in ((32, 2048, 512), (32, 8192, 512)):
+        assert sp.dense_workspace(dtype, "silu", n, di, do) == taken(shares(di, do) * n * do)
     for n, di, do in ((4200, 255, 256), (17000, 127, 512), (17000, 63, 520), (9000, 31, 1000), (1100, 192, 1024),
                       (4100, 256, 256), (40000, 62, 1024), (1100, 192, 1023), (5000, 256, 255), (20000, 128, 1023),
                       (70000, 255, 200), (70000, 31, 260)):
         assert sp.dense_workspace(dtype, "silu", n, di, do) == copies(n, di, do) > 0, (n, di, do)
+    for n, di, do in ((24, 4096, 1600), (32, 2048, 4104)):  # tiles, whose sums are shared out
+        assert sp.dense_workspace(dtype, "silu", n, di, do) > copies(n, di, do)
+
+
+def test_forward_rules_of_float32_rows():
+    assert sp.dense_workspace(sp.F32, "silu", 17, 1000, 256) == 0  # one share
+    for n, di, do in ((32, 1024, 512), (32, 2048, 512), (17, 2048, 1024)):
+        assert sp.dense_workspace(sp.F32, "silu", n, di, do) == taken(shares(di, do) * n * do)
+    assert sp.dense_workspace(sp.F32, "silu", 32, 2048, 1040) != taken(shares(2048, 1040) * 32 * 1040)
+    for n, di, do in ((32, 64, 4096), (5000, 63, 512), (20000, 256, 1024)):  # streaming, and tiles that fill the card
+        assert sp.dense_workspace(sp.F32, "silu", n, di, do) == 0
