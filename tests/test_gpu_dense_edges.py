@@ -175,3 +175,25 @@ def test_products_are_whole(n, di, do, dtype):
     g[1, 4], g[2, 4], x[1, 2], x[2, 2] = one, two, one, -1
     dw = sp.dense_bwd(x, w, g, need_dx=False)[1]
     assert dw[4, 2].item() == 2.0 ** -16 and dw.count_nonzero() == 1
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,di,do", FORMS + [(3000, 192, 1024), (20, 500, 64)])
+def test_weight_with_nan_or_infinity(n, di, do, dtype):
+    """Without an activation: the weight's element reaches its column of the
+    output and of grad_x, nothing else."""
+    need_gpu()
+    import segmented_polynomials_amd as sp
+    announce(f"dense: a weight with NaN or an infinity {n} {di} {do} {dtype}")
+    x, w, b, res, g = case(n, di, do, dtype, 6)
+    x[:, 5] = x[:, 5].abs() + 0.5
+    g[:, 3] = g[:, 3].abs() + 0.5
+    clean, (cx, cw, cb) = sp.dense_fwd(x, w, bias=b, residual=res), sp.dense_bwd(x, w, g, bias=b)
+    v = w.clone()
+    for bad in (NAN, INF, -INF):
+        v[3, 5] = bad
+        same = torch.isnan if bad != bad else lambda t: t == bad
+        out, (dx, dw, db) = sp.dense_fwd(x, v, bias=b, residual=res), sp.dense_bwd(x, v, g, bias=b)
+        assert same(out[:, 3]).all() and torch.equal(rows_without(out.T, 3), rows_without(clean.T, 3))
+        assert same(dx[:, 5]).all() and torch.equal(rows_without(dx.T, 5), rows_without(cx.T, 5))
+        assert torch.equal(dw, cw) and torch.equal(db, cb)
