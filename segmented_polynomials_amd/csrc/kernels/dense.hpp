@@ -16,7 +16,7 @@
 // its rows' in float32, a second launch adds them in order.
 // Bound by the matrix units and, at sums of a few hundred, by the epilogue, which runs
 // beside a second workgroup's products.  One MI355X, 8192 x 2048 x 5632 bf16 with gelu:
-// gradients 610 to 640 us by card (930 TFLOP/s), the product with the slope 261 of them.
+// gradients 609 to 655 us by card (865 to 930 TFLOP/s), the product with the slope 259 of them.
 #pragma once
 #include <algorithm>
 

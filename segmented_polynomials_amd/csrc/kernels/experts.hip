@@ -6,7 +6,7 @@
 //             out[i] = residual[i] + sum over j of w[i, j] ys[place[i, j]]
 //   combine's gradient
 //             gys[place[i, j]] = w[i, j] g[i],   gw[i, j] = <g[i], ys[place[i, j]]>
-// The sort is a counting sort without atomics.  A wave ranks its entries 64 at
+// The sort is a counting sort without atomics on memory.  A wave ranks its entries 64 at
 // a time: one ballot per bit of the expert's number leaves each lane the mask
 // of the lanes with its expert; counts of a wave stay in LDS.  One workgroup
 // orders short lists in one launch; longer ones take one launch that counts and one
