@@ -67,7 +67,8 @@ def run_tests():
           os.path.join(ROOT, "tests", "test_capi_channel_host.py"),
           os.path.join(ROOT, "tests", "test_capi_channel_edges.py"),
           os.path.join(ROOT, "tests", "test_capi_rows_host.py"),
-          os.path.join(ROOT, "tests", "test_capi_dense_host.py")], env=env)
+          os.path.join(ROOT, "tests", "test_capi_dense_host.py"),
+          os.path.join(ROOT, "tests", "test_capi_dense_workspace.py")], env=env)
 
 
 if __name__ == "__main__":
